@@ -38,7 +38,8 @@
  *  - Arguments are validated on the host before any HIP call; a failed check
  *    returns its code and launches nothing. M == 0 is a valid empty call that
  *    launches nothing (pointers sized by M may then be NULL).
- *  - Base pointers must be 16-byte aligned (W8A8_ERR_ALIGN).
+ *  - Base pointers must be 16-byte aligned (W8A8_ERR_ALIGN), except where an
+ *    entry point states another rule.
  *  - K must be a positive multiple of 16 and at most W8A8_MAX_K, so that
  *    128*128*K < 2^31 and int32 accumulation is exact for any int8 operands,
  *    -128 included (pytorch/ao PR #821, the 2**31 / 2**14 headroom remark:
@@ -302,6 +303,174 @@ w8a8_status w4a16_dequant(const uint8_t *wq4, const void *scales, const void *ze
 w8a8_status w4a16_gemm(const void *x, int64_t M, const uint8_t *wq4, const void *scales,
                        const void *zeros, int64_t N, int64_t K, int64_t group_size,
                        w4a16_codes codes, w4a16_dtype dtype, void *out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * MXFP4: microscaled 4-bit floating point rows and their product.
+ *
+ * A row of K elements (K a positive multiple of 32) is cut into blocks of 32.
+ * A block holds one scale, a biased power of two, and 32 elements of 4 bits
+ * (sign, two exponent bits, one fraction bit): 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives for codes 0..7 and 8..15.
+ *   codes  [rows, K/2] uint8: byte j of a row holds element 2j in its low
+ *          nibble and element 2j+1 in its high nibble
+ *   scales [ceil(K/256), rows, 8] uint8: byte i of (b, row) is the scale code
+ *          of block 8b+i of that row: 2^(code - 127), NaN for 255. The bytes
+ *          past a row's last block are 0.
+ * Quantization of a block with largest magnitude a: code = max(floor(log2 a)
+ * - 2, -127) + 127 (0 when a = 0), elements x / 2^(code-127) rounded half to
+ * even to the nearest 4-bit value and saturated at 6 (signs kept, of zeros
+ * too). A block with an infinity or NaN gets scale code 255 and element codes
+ * 0: all of it is NaN, and so is every output it takes part in.
+ */
+typedef enum {
+    MXFP4_BF16 = 0, /* bfloat16 */
+    MXFP4_F16 = 1,  /* IEEE binary16 */
+    MXFP4_F32 = 2   /* IEEE binary32 */
+} mxfp4_dtype;
+
+/* Largest K of the MXFP4 entry points. */
+#define MXFP4_MAX_K 1048576
+
+/*
+ * Rows of x [M,K] (row stride ldx elements, ldx >= K) -> codes, scales. Exact
+ * (no other rounding than the definition's) for every finite input.
+ * x and ldx * element size must be 16-byte aligned.
+ * Errors: NULL, SHAPE (M < 0, K not a positive multiple of 32 or above
+ *         MXFP4_MAX_K, ldx < K, M * ceil(K/256) >= 2^27), ALIGN,
+ *         DTYPE, HIP.
+ */
+w8a8_status mxfp4_quantize_rows(const void *x, int64_t ldx, int64_t M, int64_t K,
+                                mxfp4_dtype dtype, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* codes, scales -> the values they stand for, out [M,K] (rounded to nearest
+ * even where dtype has fewer bits of exponent). Errors as above. */
+w8a8_status mxfp4_dequantize_rows(const uint8_t *codes, const uint8_t *scales, int64_t M,
+                                  int64_t K, mxfp4_dtype dtype, void *out, void *stream);
+
+/*
+ * out[m][n] = sum_k x[m][k] * w[n][k] for MXFP4 x [M,K] and w [N,K]: products
+ * and scales exact, accumulated in fp32, rounded once to dtype. M >= 0, N a
+ * positive multiple of 16, K as above.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, HIP.
+ */
+w8a8_status mxfp4_gemm(const uint8_t *xq, const uint8_t *xs, int64_t M, const uint8_t *wq,
+                       const uint8_t *ws, int64_t N, int64_t K, mxfp4_dtype dtype, void *out,
+                       void *stream);
+
+/*
+ * The dynamically quantized layer: mxfp4_quantize_rows of x (type x_dtype,
+ * row stride ldx), then mxfp4_gemm to out of out_dtype. The codes and scales
+ * go through `workspace` (device, 16-byte aligned, at least
+ * mxfp4_linear_workspace(M, K) bytes, free again once the call's work on the
+ * stream is done).
+ * Errors: as the two calls; SHAPE when workspace_bytes is too small.
+ */
+int64_t mxfp4_linear_workspace(int64_t M, int64_t K);
+w8a8_status mxfp4_linear(const void *x, int64_t ldx, mxfp4_dtype x_dtype, int64_t M,
+                         const uint8_t *wq, const uint8_t *ws, int64_t N, int64_t K,
+                         mxfp4_dtype out_dtype, void *out, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Mixture of experts: tokens sorted by expert and back.
+ *
+ * T tokens fill top slots each; expert_ids [T,top] names each slot's expert.
+ * An id outside [0, E) is a slot without an expert (dropped, over capacity).
+ * The slots are sorted by expert, in slot order within an expert, slots
+ * without one last:
+ *   offsets   [E+1] int32: expert e owns sorted rows offsets[e]..offsets[e+1]-1;
+ *             rows from offsets[E] on have no expert
+ *   slot_pos  [T,top] int32: the sorted row p of the slot, or ~p (negative)
+ *             for a slot without an expert
+ *   row_token [T*top] int32: the token of each sorted row, -1 without an expert
+ * Arrays in sorted order have T*top rows. A plan that was not made by moe_sort
+ * gives unspecified values but no access outside the given arrays.
+ */
+
+/* Largest number of experts. */
+#define MOE_MAX_EXPERTS 512
+
+/*
+ * expert_ids are int32 (ids_bits 32) or int64 (64). workspace: at least
+ * moe_sort_workspace(T * top, E) bytes (may be 0: then NULL).
+ * 0 <= T < 2^24, top >= 1, 1 <= E <= MOE_MAX_EXPERTS, T * top < 2^30 (the T
+ * and top of all entry points here). With T = 0 offsets are still written.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE (ids_bits), HIP.
+ */
+int64_t moe_sort_workspace(int64_t slots, int64_t E);
+w8a8_status moe_sort(const void *expert_ids, int ids_bits, int64_t T, int64_t top, int64_t E,
+                     int32_t *offsets, int32_t *slot_pos, int32_t *row_token, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+
+/*
+ * Rows in sorted order and back, H >= 1 elements of dtype each, any H. Arrays
+ * of rows need the alignment of their element type only (16-byte aligned rows
+ * take 16-byte accesses); x and d_out have a row stride (ldx, ldd >= H), the
+ * others are dense. Sums are made in fp32, in the order of the slots, and
+ * rounded once.
+ *   gather:            rows[p] = x[t], 0 for slots without an expert
+ *   gather_backward:   d_x[t] = sum_j d_rows[p(t,j)]
+ *   combine:           out[t] = sum_j weights[t,j] * rows[p(t,j)]
+ *   combine_backward:  d_rows[p] = weights[t,j] * d_out[t] (0 for slots without
+ *                      an expert), d_weights[t,j] = <d_out[t], rows[p]> (0 for
+ *                      those; d_weights may be NULL)
+ * Slots without an expert add nothing whatever their rows and weights hold; a
+ * token with no other slot gets 0. weights, d_weights: fp32 [T,top].
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, HIP.
+ */
+w8a8_status moe_gather(const void *x, int64_t ldx, const int32_t *slot_pos, int64_t T, int64_t top,
+                       int64_t H, mxfp4_dtype dtype, void *rows, void *stream);
+w8a8_status moe_gather_backward(const void *d_rows, const int32_t *slot_pos, int64_t T,
+                                int64_t top, int64_t H, mxfp4_dtype dtype, void *d_x,
+                                void *stream);
+w8a8_status moe_combine(const void *rows, const int32_t *slot_pos, const float *weights,
+                        int64_t T, int64_t top, int64_t H, mxfp4_dtype dtype, void *out,
+                        void *stream);
+w8a8_status moe_combine_backward(const void *d_out, int64_t ldd, const void *rows,
+                                 const int32_t *slot_pos, const float *weights, int64_t T,
+                                 int64_t top, int64_t H, mxfp4_dtype dtype, void *d_rows,
+                                 float *d_weights, void *stream);
+
+/*
+ * The experts' products on MXFP4 rows: sorted row r of expert e multiplies
+ * weight e, out[r][n] = sum_k x[row(r)][k] * w[e][n][k]; rows from offsets[E]
+ * on are written as 0. row(r) = row_token[r] of the T rows of x (no sorted
+ * copy of x is needed), or r itself when row_token is NULL (then T = S).
+ *   xq, xs     MXFP4 [T,K]; offsets [E+1], row_token [S] from moe_sort
+ *   wq         [E][N, K/2], ws [E][ceil(K/256), N, 8]
+ *   out        [S,N] of dtype
+ * S >= 0 rows, N a positive multiple of 16, K as for mxfp4_gemm.
+ * mxfp4_expert_swiglu: N = 2F, rows 2f and 2f+1 of a weight are the gate and
+ * the up projection of hidden unit f (F a positive multiple of 32); writes the
+ * hidden activations gate / (1 + exp(-gate)) * up, computed in fp32 from the
+ * accumulators, as MXFP4 rows: hq [S,F/2], hs [ceil(F/256), S, 8].
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, HIP.
+ */
+w8a8_status mxfp4_expert_gemm(const uint8_t *xq, const uint8_t *xs, int64_t T,
+                              const int32_t *row_token, int64_t S, const int32_t *offsets,
+                              int64_t E, const uint8_t *wq, const uint8_t *ws, int64_t N,
+                              int64_t K, mxfp4_dtype dtype, void *out, void *stream);
+w8a8_status mxfp4_expert_swiglu(const uint8_t *xq, const uint8_t *xs, int64_t T,
+                                const int32_t *row_token, int64_t S, const int32_t *offsets,
+                                int64_t E, const uint8_t *wq, const uint8_t *ws, int64_t F,
+                                int64_t K, uint8_t *hq, uint8_t *hs, void *stream);
+
+/*
+ * A whole expert layer: moe_sort, mxfp4_quantize_rows of x, mxfp4_expert_swiglu
+ * with w13 [E][2F,H], mxfp4_expert_gemm with w2 [E][H,F] (to dtype), and
+ * moe_combine with weights into out [T,H] of dtype.
+ *   x [T,H] of dtype with row stride ldx; H a positive multiple of 32 (and 16),
+ *   F a positive multiple of 32; expert_ids, ids_bits, top, E as for moe_sort.
+ * workspace: device, 16-byte aligned, at least mxfp4_moe_workspace(...) bytes.
+ * Errors: as the calls it is made of; SHAPE when workspace_bytes is too small.
+ */
+int64_t mxfp4_moe_workspace(int64_t T, int64_t top, int64_t E, int64_t H, int64_t F,
+                            mxfp4_dtype dtype);
+w8a8_status mxfp4_moe(const void *x, int64_t ldx, mxfp4_dtype dtype, int64_t T, int64_t H,
+                      const void *expert_ids, int ids_bits, const float *weights, int64_t top,
+                      int64_t E, const uint8_t *w13q, const uint8_t *w13s, const uint8_t *w2q,
+                      const uint8_t *w2s, int64_t F, void *out, void *workspace,
+                      int64_t workspace_bytes, void *stream);
 
 /* Static, human-readable text for a status code (never NULL). */
 const char *w8a8_status_string(int status);

@@ -58,3 +58,41 @@ hipError_t launch_gemm(const uint16_t *x, int M, const uint8_t *wq4, const uint1
                        uint16_t *out, hipStream_t stream);
 
 }  // namespace w4a16
+
+namespace mxfp4 {
+
+struct Groups;
+struct Output;
+
+// MXFP4 rows (dtype 0 bf16, 1 binary16, 2 binary32): x [M,K] with row stride
+// ldx -> codes [M,K/2], scales [ceil(K/256),M,8], and back to out [M,K].
+hipError_t launch_quantize(const void *x, int64_t ldx, int64_t M, int K, int dtype, uint8_t *codes,
+                           uint8_t *scales, hipStream_t stream);
+hipError_t launch_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t M, int K,
+                             int dtype, void *out, hipStream_t stream);
+
+// Product of MXFP4 rows and weights [E][N,K] (one weight without offsets);
+// epilogue: a dtype, or 3 for SwiGLU + MXFP4.
+hipError_t launch_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                       const Groups &g, int N, int K, int epilogue, const Output &o,
+                       hipStream_t stream);
+
+}  // namespace mxfp4
+
+namespace moe {
+
+// Bytes of scratch that launch_sort needs for S slots.
+int64_t sort_workspace(int64_t S, int64_t E);
+hipError_t launch_sort(const void *ids, bool ids64, int64_t S, int top, int E, int32_t *offsets,
+                       int32_t *slot_pos, int32_t *row_token, void *workspace, hipStream_t stream);
+hipError_t launch_gather(const void *x, int64_t ldx, const int32_t *slot_pos, int64_t T, int top,
+                         int H, int dtype, void *rows, hipStream_t stream);
+// weights null: the plain sum (the gather's gradient)
+hipError_t launch_combine(const void *rows, const int32_t *slot_pos, const float *weights,
+                          int64_t T, int top, int H, int dtype, void *out, hipStream_t stream);
+hipError_t launch_combine_backward(const void *d_out, int64_t ldd, const void *rows,
+                                   const int32_t *slot_pos, const float *weights, int64_t T,
+                                   int top, int H, int dtype, void *d_rows, float *d_weights,
+                                   hipStream_t stream);
+
+}  // namespace moe

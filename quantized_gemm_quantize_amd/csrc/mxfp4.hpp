@@ -1,0 +1,143 @@
+// MXFP4 building blocks shared by the kernels (gfx950 / CDNA4).
+//
+// A row is cut into blocks of 32 elements along K. Each block holds 4-bit
+// e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one
+// power-of-two scale stored as a biased exponent (e8m0: 2^(code - 127), code
+// 255 is NaN).
+//   codes  [rows, K/2]            byte j of a row: element 2j in the low nibble
+//   scales [ceil(K/256), rows, 8] byte i of (b, row): the scale of block 8b+i,
+//                                 0 past the row's last block
+// The scales are K-block-major so that the 8 scale bytes that a product needs
+// per row and 256-element step lie next to those of the neighbouring rows: a
+// 32-row fragment's scales are one 256-byte load.
+#pragma once
+
+#include "common.hpp"
+
+namespace mxfp4 {
+
+using w8a8::kWave;
+using w8a8::v4i;
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+enum Dtype { kBf16 = 0, kF16 = 1, kF32 = 2 };
+
+constexpr int kFp4 = 4;        // operand format selector of the scaled MFMA
+constexpr int kStep = 256;     // elements per scale group of 8 blocks
+constexpr int kStepBytes = 128;
+
+// The float behind a scale code: 2^(code - 127), 2^-127 for code 0, NaN for 255.
+__device__ __forceinline__ float scale_value(uint32_t code) {
+    return __uint_as_float(code == 0 ? 0x00400000u : code == 255 ? 0x7FC00000u : code << 23);
+}
+
+// Scale code of a block whose largest magnitude is `top`: floor(log2 top) - 2
+// (2 is the exponent of the largest element, 6 = 1.5 * 2^2), at least -127;
+// 255 when the block holds a value that is not finite.
+__device__ __forceinline__ uint32_t scale_code(float top) {
+    const uint32_t field = __float_as_uint(top) >> 23;  // top >= 0
+    return field == 255 ? 255u : field < 2 ? 0u : field - 2;
+}
+
+__device__ __forceinline__ v8i widen(v4i a) {
+    // the fp4 forms read the first four registers of the operand
+    return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+
+// Scaled fp4 MFMA, 32x32 output, K = 64: lane l holds row l % 32 of each
+// operand, 32 consecutive elements (block l / 32 of the two), and byte SEL of
+// its scale register is that block's scale. Output as the int8 form: lane l,
+// element r: row 8 * (r / 4) + 4 * (l / 32) + r % 4 of a, row l % 32 of b.
+template <int SEL>
+__device__ __forceinline__ v16f mfma_32x32x64(v4i a, uint32_t sa, v4i b, uint32_t sb, v16f c) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, SEL,
+                                                           (int)sa, SEL, (int)sb);
+}
+
+// The same with the byte chosen by a loop counter (constant once unrolled).
+__device__ __forceinline__ v16f mfma_32x32x64(int sel, v4i a, uint32_t sa, v4i b, uint32_t sb,
+                                              v16f c) {
+    switch (sel) {
+        case 0: return mfma_32x32x64<0>(a, sa, b, sb, c);
+        case 1: return mfma_32x32x64<1>(a, sa, b, sb, c);
+        case 2: return mfma_32x32x64<2>(a, sa, b, sb, c);
+        default: return mfma_32x32x64<3>(a, sa, b, sb, c);
+    }
+}
+
+// Rows of the product, in groups: rows offsets[e] .. offsets[e+1]-1 multiply
+// weight e; rows past offsets[E] belong to no weight (their outputs are 0).
+// offsets null: one group of all S rows. Row r reads activation row
+// row_token[r] of T (row_token null: row r itself).
+struct Groups {
+    const int32_t *offsets;
+    const int32_t *row_token;
+    int E, S, T;
+};
+
+struct Tile {
+    int e;       // group, E for the rows without a weight, -1 past the last tile
+    int m0, m1;  // its rows: m0 .. m1-1 with m1 the end of the group
+};
+
+// Tile t of the groups' rows cut into tiles of BM rows, group after group.
+// Every wavefront finds its workgroup's tile itself: 64 groups at a time, an
+// inclusive scan of the tile counts over the lanes. Bounds that a malformed
+// offsets array could break are clamped, so rows stay inside [0, S).
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const Groups &g, int t) {
+    if (!g.offsets) return Tile{t * BM < g.S ? 0 : -1, t * BM, g.S};
+    const int lane = threadIdx.x & (kWave - 1);
+    int before = 0;
+    for (int base = 0; base <= g.E; base += kWave) {
+        const int e = base + lane;
+        int lo = 0, n = 0;
+        if (e <= g.E) {
+            lo = min(max(g.offsets[e], 0), g.S);
+            const int hi = e < g.E ? min(max(g.offsets[e + 1], lo), g.S) : g.S;
+            n = hi - lo;
+        }
+        const int own = (n + BM - 1) / BM;
+        int upto = own;
+#pragma unroll
+        for (int off = 1; off < kWave; off <<= 1) {
+            const int o = __shfl_up(upto, off, kWave);
+            if (lane >= off) upto += o;
+        }
+        const uint64_t hit = __builtin_amdgcn_ballot_w64(before + upto > t);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            const int first = before + __builtin_amdgcn_readlane(upto - own, l);
+            const int glo = __builtin_amdgcn_readlane(lo, l), gn = __builtin_amdgcn_readlane(n, l);
+            return Tile{base + l, glo + (t - first) * BM, glo + gn};
+        }
+        before += __builtin_amdgcn_readlane(upto, kWave - 1);
+    }
+    return Tile{-1, 0, 0};
+}
+
+// Most tiles of BM rows that S rows in E groups (and the rows without a
+// weight) can have: every group ends in at most one partial tile, and no tile
+// is empty.
+inline int64_t most_tiles(int64_t S, int64_t E, int BM, bool grouped) {
+    const int64_t full = (S + BM - 1) / BM;
+    if (!grouped) return full;
+    const int64_t split = S / BM + E + 1;
+    return split < S ? split : S;
+}
+
+// Activation row of product row r.
+__device__ __forceinline__ int source_row(const Groups &g, int r) {
+    return g.row_token ? min(max(g.row_token[r], 0), g.T - 1) : r;
+}
+
+// Gate and up projections of one hidden unit -> its activation.
+__device__ __forceinline__ float swiglu(float gate, float up) {
+    return gate / (1.0f + __expf(-gate)) * up;
+}
+
+}  // namespace mxfp4

@@ -15,6 +15,7 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "mxfp4_epilogue.hpp"
 
 namespace {
 
@@ -278,6 +279,313 @@ w8a8_status w4a16_gemm(const void *x, int64_t M, const uint8_t *wq4, const void 
                                          (int)group_size, cs == W4A16_CODES_S4,
                                          dt == W4A16_F16, static_cast<uint16_t *>(out),
                                          static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- MXFP4
+
+static bool mx_dtype_ok(int d) { return d == MXFP4_BF16 || d == MXFP4_F16 || d == MXFP4_F32; }
+
+static int64_t dtype_size(int d) { return d == MXFP4_F32 ? 4 : 2; }
+
+// K and rows that the MXFP4 kernels index with 32-bit step counts.
+static w8a8_status mx_shape(int64_t rows, int64_t K) {
+    if (rows < 0 || rows > INT_MAX / 2 || K <= 0 || K % 32 != 0 || K > MXFP4_MAX_K)
+        return W8A8_ERR_SHAPE;
+    if (rows * ((K + 255) / 256) >= (1 << 27)) return W8A8_ERR_SHAPE;  // 32 threads each, one grid
+    return W8A8_OK;
+}
+
+static w8a8_status mx_weight(int64_t N, int64_t K) {
+    if (N <= 0 || N % 16 != 0) return W8A8_ERR_SHAPE;
+    return mx_shape(N, K);
+}
+
+static int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+static int64_t mx_codes(int64_t rows, int64_t K) { return align256(rows * (K / 2)); }
+static int64_t mx_scales(int64_t rows, int64_t K) { return align256((K + 255) / 256 * rows * 8); }
+
+w8a8_status mxfp4_quantize_rows(const void *x, int64_t ldx, int64_t M, int64_t K,
+                                mxfp4_dtype dtype, uint8_t *codes, uint8_t *scales, void *stream) {
+    if (w8a8_status s = mx_shape(M, K)) return s;
+    if (ldx < K || ldx > INT_MAX) return W8A8_ERR_SHAPE;
+    const int dt = selector(&dtype);
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    if (M == 0) return W8A8_OK;
+    if (!x || !codes || !scales) return W8A8_ERR_NULL;
+    if (misaligned(x) || misaligned(codes) || misaligned(scales) || ldx * dtype_size(dt) % 16 != 0)
+        return W8A8_ERR_ALIGN;
+    return hip_status(mxfp4::launch_quantize(x, ldx, M, (int)K, dt, codes, scales,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+w8a8_status mxfp4_dequantize_rows(const uint8_t *codes, const uint8_t *scales, int64_t M,
+                                  int64_t K, mxfp4_dtype dtype, void *out, void *stream) {
+    if (w8a8_status s = mx_shape(M, K)) return s;
+    const int dt = selector(&dtype);
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    if (M == 0) return W8A8_OK;
+    if (!codes || !scales || !out) return W8A8_ERR_NULL;
+    if (misaligned(codes) || misaligned(scales) || misaligned(out)) return W8A8_ERR_ALIGN;
+    return hip_status(mxfp4::launch_dequantize(codes, scales, M, (int)K, dt, out,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+w8a8_status mxfp4_gemm(const uint8_t *xq, const uint8_t *xs, int64_t M, const uint8_t *wq,
+                       const uint8_t *ws, int64_t N, int64_t K, mxfp4_dtype dtype, void *out,
+                       void *stream) {
+    if (w8a8_status s = mx_shape(M, K)) return s;
+    if (w8a8_status s = mx_weight(N, K)) return s;
+    const int dt = selector(&dtype);
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    if (M == 0) return W8A8_OK;
+    if (!xq || !xs || !wq || !ws || !out) return W8A8_ERR_NULL;
+    if (misaligned(xq) || misaligned(xs) || misaligned(wq) || misaligned(ws) || misaligned(out))
+        return W8A8_ERR_ALIGN;
+    const mxfp4::Groups g{nullptr, nullptr, 1, (int)M, (int)M};
+    return hip_status(mxfp4::launch_gemm(xq, xs, wq, ws, g, (int)N, (int)K, dt,
+                                         mxfp4::Output{out, nullptr, nullptr},
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int64_t mxfp4_linear_workspace(int64_t M, int64_t K) {
+    if (M <= 0 || mx_shape(M, K) != W8A8_OK) return 0;
+    return mx_codes(M, K) + mx_scales(M, K);
+}
+
+w8a8_status mxfp4_linear(const void *x, int64_t ldx, mxfp4_dtype x_dtype, int64_t M,
+                         const uint8_t *wq, const uint8_t *ws, int64_t N, int64_t K,
+                         mxfp4_dtype out_dtype, void *out, void *workspace,
+                         int64_t workspace_bytes, void *stream) {
+    if (w8a8_status s = mx_shape(M, K)) return s;
+    if (w8a8_status s = mx_weight(N, K)) return s;
+    const int xd = selector(&x_dtype), od = selector(&out_dtype);
+    if (!mx_dtype_ok(xd) || !mx_dtype_ok(od)) return W8A8_ERR_DTYPE;
+    if (ldx < K || ldx > INT_MAX || workspace_bytes < mxfp4_linear_workspace(M, K))
+        return W8A8_ERR_SHAPE;
+    if (M == 0) return W8A8_OK;
+    if (!x || !wq || !ws || !out || !workspace) return W8A8_ERR_NULL;
+    if (misaligned(x) || misaligned(wq) || misaligned(ws) || misaligned(out) ||
+        misaligned(workspace) || ldx * dtype_size(xd) % 16 != 0)
+        return W8A8_ERR_ALIGN;
+    uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + mx_codes(M, K);
+    if (w8a8_status s = mxfp4_quantize_rows(x, ldx, M, K, x_dtype, codes, scales, stream)) return s;
+    return mxfp4_gemm(codes, scales, M, wq, ws, N, K, out_dtype, out, stream);
+}
+
+// ---------------------------------------------------------------- experts
+
+// T, top and E of a routing plan.
+static w8a8_status moe_shape(int64_t T, int64_t top) {
+    if (T < 0 || top <= 0 || T >= (1 << 24) || top >= (1 << 30) || T * top >= (1 << 30))
+        return W8A8_ERR_SHAPE;  // a workgroup of 256 threads per token
+    return W8A8_OK;
+}
+
+static bool odd(const void *p, int64_t size) {
+    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)size != 0;
+}
+
+int64_t moe_sort_workspace(int64_t slots, int64_t E) {
+    return slots <= 0 || slots >= (1 << 30) || E <= 0 || E > MOE_MAX_EXPERTS
+               ? 0 : moe::sort_workspace(slots, E);
+}
+
+w8a8_status moe_sort(const void *expert_ids, int ids_bits, int64_t T, int64_t top, int64_t E,
+                     int32_t *offsets, int32_t *slot_pos, int32_t *row_token, void *workspace,
+                     int64_t workspace_bytes, void *stream) {
+    if (w8a8_status s = moe_shape(T, top)) return s;
+    if (E <= 0 || E > MOE_MAX_EXPERTS) return W8A8_ERR_SHAPE;
+    if (ids_bits != 32 && ids_bits != 64) return W8A8_ERR_DTYPE;
+    const int64_t need = moe_sort_workspace(T * top, E);
+    if (workspace_bytes < need) return W8A8_ERR_SHAPE;
+    if (!offsets || (need > 0 && !workspace)) return W8A8_ERR_NULL;
+    if (T > 0 && (!expert_ids || !slot_pos || !row_token)) return W8A8_ERR_NULL;
+    if (odd(expert_ids, ids_bits / 8) || odd(offsets, 4) || odd(slot_pos, 4) || odd(row_token, 4) ||
+        odd(workspace, 4))
+        return W8A8_ERR_ALIGN;
+    return hip_status(moe::launch_sort(expert_ids, ids_bits == 64, T * top, (int)top, (int)E,
+                                       offsets, slot_pos, row_token, workspace,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+// Shapes that the row kernels take: T workgroups along x, H in segments.
+static w8a8_status moe_rows(int64_t T, int64_t top, int64_t H, int64_t ld) {
+    if (w8a8_status s = moe_shape(T, top)) return s;
+    if (H <= 0 || H > (1 << 23) || ld < H || ld > INT_MAX) return W8A8_ERR_SHAPE;
+    return W8A8_OK;
+}
+
+w8a8_status moe_gather(const void *x, int64_t ldx, const int32_t *slot_pos, int64_t T, int64_t top,
+                       int64_t H, mxfp4_dtype dtype, void *rows, void *stream) {
+    if (w8a8_status s = moe_rows(T, top, H, ldx)) return s;
+    const int dt = selector(&dtype);
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    if (T == 0) return W8A8_OK;
+    if (!x || !slot_pos || !rows) return W8A8_ERR_NULL;
+    const int64_t size = dtype_size(dt);
+    if (odd(x, size) || odd(rows, size) || odd(slot_pos, 4)) return W8A8_ERR_ALIGN;
+    return hip_status(moe::launch_gather(x, ldx, slot_pos, T, (int)top, (int)H, dt, rows,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+// combine, and (weights null) the gather's gradient
+static w8a8_status combine_entry(const void *rows, const int32_t *slot_pos, const float *weights,
+                                 bool weighted, int64_t T, int64_t top, int64_t H, int dt,
+                                 void *out, void *stream) {
+    if (w8a8_status s = moe_rows(T, top, H, H)) return s;
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    if (T == 0) return W8A8_OK;
+    if (!rows || !slot_pos || !out || (weighted && !weights)) return W8A8_ERR_NULL;
+    const int64_t size = dtype_size(dt);
+    if (odd(rows, size) || odd(out, size) || odd(slot_pos, 4) || odd(weights, 4))
+        return W8A8_ERR_ALIGN;
+    return hip_status(moe::launch_combine(rows, slot_pos, weights, T, (int)top, (int)H, dt, out,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+w8a8_status moe_gather_backward(const void *d_rows, const int32_t *slot_pos, int64_t T,
+                                int64_t top, int64_t H, mxfp4_dtype dtype, void *d_x,
+                                void *stream) {
+    return combine_entry(d_rows, slot_pos, nullptr, false, T, top, H, selector(&dtype), d_x, stream);
+}
+
+w8a8_status moe_combine(const void *rows, const int32_t *slot_pos, const float *weights,
+                        int64_t T, int64_t top, int64_t H, mxfp4_dtype dtype, void *out,
+                        void *stream) {
+    return combine_entry(rows, slot_pos, weights, true, T, top, H, selector(&dtype), out, stream);
+}
+
+w8a8_status moe_combine_backward(const void *d_out, int64_t ldd, const void *rows,
+                                 const int32_t *slot_pos, const float *weights, int64_t T,
+                                 int64_t top, int64_t H, mxfp4_dtype dtype, void *d_rows,
+                                 float *d_weights, void *stream) {
+    if (w8a8_status s = moe_rows(T, top, H, ldd)) return s;
+    const int dt = selector(&dtype);
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    if (T == 0) return W8A8_OK;
+    if (!d_out || !rows || !slot_pos || !weights || !d_rows) return W8A8_ERR_NULL;
+    const int64_t size = dtype_size(dt);
+    if (odd(d_out, size) || odd(rows, size) || odd(d_rows, size) || odd(slot_pos, 4) ||
+        odd(weights, 4) || odd(d_weights, 4))
+        return W8A8_ERR_ALIGN;
+    return hip_status(moe::launch_combine_backward(d_out, ldd, rows, slot_pos, weights, T, (int)top,
+                                                   (int)H, dt, d_rows, d_weights,
+                                                   static_cast<hipStream_t>(stream)));
+}
+
+// Checks shared by the experts' products, then the launch.
+static w8a8_status expert_entry(const uint8_t *xq, const uint8_t *xs, int64_t T,
+                                const int32_t *row_token, int64_t S, const int32_t *offsets,
+                                int64_t E, const uint8_t *wq, const uint8_t *ws, int64_t N,
+                                int64_t K, int epilogue, const mxfp4::Output &o, void *stream) {
+    if (w8a8_status s = mx_shape(S, K)) return s;
+    if (w8a8_status s = mx_shape(T, K)) return s;
+    if (w8a8_status s = mx_weight(N, K)) return s;
+    if (E <= 0 || E > MOE_MAX_EXPERTS || (!row_token && T != S) || (S > 0 && T == 0))
+        return W8A8_ERR_SHAPE;
+    if (S == 0) return W8A8_OK;
+    if (!xq || !xs || !offsets || !wq || !ws) return W8A8_ERR_NULL;
+    if (epilogue == mxfp4::kSwiglu ? !o.codes || !o.scales : !o.out) return W8A8_ERR_NULL;
+    if (misaligned(xq) || misaligned(xs) || misaligned(wq) || misaligned(ws) || misaligned(o.out) ||
+        misaligned(o.codes) || misaligned(o.scales) || odd(offsets, 4) || odd(row_token, 4))
+        return W8A8_ERR_ALIGN;
+    const mxfp4::Groups g{offsets, row_token, (int)E, (int)S, (int)T};
+    return hip_status(mxfp4::launch_gemm(xq, xs, wq, ws, g, (int)N, (int)K, epilogue, o,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+w8a8_status mxfp4_expert_gemm(const uint8_t *xq, const uint8_t *xs, int64_t T,
+                              const int32_t *row_token, int64_t S, const int32_t *offsets,
+                              int64_t E, const uint8_t *wq, const uint8_t *ws, int64_t N,
+                              int64_t K, mxfp4_dtype dtype, void *out, void *stream) {
+    const int dt = selector(&dtype);
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    return expert_entry(xq, xs, T, row_token, S, offsets, E, wq, ws, N, K, dt,
+                        mxfp4::Output{out, nullptr, nullptr}, stream);
+}
+
+w8a8_status mxfp4_expert_swiglu(const uint8_t *xq, const uint8_t *xs, int64_t T,
+                                const int32_t *row_token, int64_t S, const int32_t *offsets,
+                                int64_t E, const uint8_t *wq, const uint8_t *ws, int64_t F,
+                                int64_t K, uint8_t *hq, uint8_t *hs, void *stream) {
+    if (w8a8_status s = mx_shape(S, F)) return s;  // the hidden rows
+    return expert_entry(xq, xs, T, row_token, S, offsets, E, wq, ws, 2 * F, K, mxfp4::kSwiglu,
+                        mxfp4::Output{nullptr, hq, hs}, stream);
+}
+
+// Parts of mxfp4_moe's workspace, in bytes from its start.
+struct MoeParts {
+    int64_t offsets, slot_pos, row_token, sort, sort_bytes, xq, xs, hq, hs, y, total;
+};
+
+static w8a8_status moe_parts(int64_t T, int64_t top, int64_t E, int64_t H, int64_t F, int dt,
+                      MoeParts &p) {
+    if (w8a8_status s = moe_shape(T, top)) return s;
+    if (E <= 0 || E > MOE_MAX_EXPERTS) return W8A8_ERR_SHAPE;
+    const int64_t S = T * top;
+    if (w8a8_status s = mx_shape(S, H)) return s;
+    if (w8a8_status s = mx_shape(S, F)) return s;
+    if (w8a8_status s = mx_weight(H, F)) return s;
+    if (w8a8_status s = mx_weight(2 * F, H)) return s;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) { const int64_t b = at; at += align256(bytes); return b; };
+    p.offsets = take((E + 1) * 4);
+    p.slot_pos = take(S * 4);
+    p.row_token = take(S * 4);
+    p.sort_bytes = moe_sort_workspace(S, E);
+    p.sort = take(p.sort_bytes);
+    p.xq = take(mx_codes(T, H));
+    p.xs = take(mx_scales(T, H));
+    p.hq = take(mx_codes(S, F));
+    p.hs = take(mx_scales(S, F));
+    p.y = take(S * H * dtype_size(dt));
+    p.total = at;
+    return W8A8_OK;
+}
+
+int64_t mxfp4_moe_workspace(int64_t T, int64_t top, int64_t E, int64_t H, int64_t F,
+                            mxfp4_dtype dtype) {
+    MoeParts p;
+    const int dt = selector(&dtype);
+    if (T <= 0 || !mx_dtype_ok(dt) || moe_parts(T, top, E, H, F, dt, p) != W8A8_OK) return 0;
+    return p.total;
+}
+
+w8a8_status mxfp4_moe(const void *x, int64_t ldx, mxfp4_dtype dtype, int64_t T, int64_t H,
+                      const void *expert_ids, int ids_bits, const float *weights, int64_t top,
+                      int64_t E, const uint8_t *w13q, const uint8_t *w13s, const uint8_t *w2q,
+                      const uint8_t *w2s, int64_t F, void *out, void *workspace,
+                      int64_t workspace_bytes, void *stream) {
+    const int dt = selector(&dtype);
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    if (ids_bits != 32 && ids_bits != 64) return W8A8_ERR_DTYPE;
+    MoeParts p;
+    if (w8a8_status s = moe_parts(T, top, E, H, F, dt, p)) return s;
+    if (ldx < H || ldx > INT_MAX) return W8A8_ERR_SHAPE;
+    if (T > 0 && workspace_bytes < p.total) return W8A8_ERR_SHAPE;
+    if (T == 0) return W8A8_OK;
+    if (!x || !expert_ids || !weights || !w13q || !w13s || !w2q || !w2s || !out || !workspace)
+        return W8A8_ERR_NULL;
+    if (misaligned(x) || misaligned(w13q) || misaligned(w13s) || misaligned(w2q) ||
+        misaligned(w2s) || misaligned(out) || misaligned(workspace) || odd(weights, 4) ||
+        odd(expert_ids, ids_bits / 8) || ldx * dtype_size(dt) % 16 != 0)
+        return W8A8_ERR_ALIGN;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    int32_t *offsets = reinterpret_cast<int32_t *>(ws + p.offsets);
+    int32_t *slot_pos = reinterpret_cast<int32_t *>(ws + p.slot_pos);
+    int32_t *row_token = reinterpret_cast<int32_t *>(ws + p.row_token);
+    const int64_t S = T * top;
+    if (w8a8_status s = moe_sort(expert_ids, ids_bits, T, top, E, offsets, slot_pos, row_token,
+                                 ws + p.sort, p.sort_bytes, stream))
+        return s;
+    if (w8a8_status s = mxfp4_quantize_rows(x, ldx, T, H, dtype, ws + p.xq, ws + p.xs, stream)) return s;
+    if (w8a8_status s = mxfp4_expert_swiglu(ws + p.xq, ws + p.xs, T, row_token, S, offsets, E, w13q,
+                                            w13s, F, H, ws + p.hq, ws + p.hs, stream))
+        return s;
+    if (w8a8_status s = mxfp4_expert_gemm(ws + p.hq, ws + p.hs, S, nullptr, S, offsets, E, w2q, w2s,
+                                          H, F, dtype, ws + p.y, stream))
+        return s;
+    return moe_combine(ws + p.y, slot_pos, weights, T, top, H, dtype, out, stream);
 }
 
 const char *w8a8_status_string(int status) {
