@@ -84,24 +84,39 @@ struct Tile {
     int m0, m1;  // its rows: m0 .. m1-1 with m1 the end of the group
 };
 
-// Tile t of the groups' rows cut into tiles of BM rows, group after group.
-// Every wavefront finds its workgroup's tile itself: 64 groups at a time, an
-// inclusive scan of the tile counts over the lanes. Bounds that a malformed
-// offsets array could break are clamped, so rows stay inside [0, S).
+// Tiles of BM rows in group e (0 past the last group); lo, n: its rows. Bounds
+// that a malformed offsets array could break are clamped, so rows stay inside
+// [0, S). Group E holds the rows without a weight.
+template <int BM>
+__device__ __forceinline__ int group_tiles(const Groups &g, int e, int &lo, int &n) {
+    lo = n = 0;
+    if (e <= g.E) {
+        lo = min(max(g.offsets[e], 0), g.S);
+        n = (e < g.E ? min(max(g.offsets[e + 1], lo), g.S) : g.S) - lo;
+    }
+    return (n + BM - 1) / BM;
+}
+
+// All tiles of BM rows, found by every wavefront for itself.
+template <int BM>
+__device__ __forceinline__ int count_tiles(const Groups &g) {
+    int own = 0, lo, n;
+    for (int e = threadIdx.x & (kWave - 1); e <= g.E; e += kWave) own += group_tiles<BM>(g, e, lo, n);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) own += __shfl_xor(own, off, kWave);
+    return __builtin_amdgcn_readfirstlane(own);
+}
+
+// Tile t of the groups' rows cut into tiles of BM rows, group after group:
+// 64 groups at a time, an inclusive scan of the tile counts over the lanes.
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const Groups &g, int t) {
     if (!g.offsets) return Tile{t * BM < g.S ? 0 : -1, t * BM, g.S};
     const int lane = threadIdx.x & (kWave - 1);
     int before = 0;
     for (int base = 0; base <= g.E; base += kWave) {
-        const int e = base + lane;
-        int lo = 0, n = 0;
-        if (e <= g.E) {
-            lo = min(max(g.offsets[e], 0), g.S);
-            const int hi = e < g.E ? min(max(g.offsets[e + 1], lo), g.S) : g.S;
-            n = hi - lo;
-        }
-        const int own = (n + BM - 1) / BM;
+        int lo, n;
+        const int own = group_tiles<BM>(g, base + lane, lo, n);
         int upto = own;
 #pragma unroll
         for (int off = 1; off < kWave; off <<= 1) {

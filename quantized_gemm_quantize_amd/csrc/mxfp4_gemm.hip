@@ -69,9 +69,14 @@ __global__ __launch_bounds__(kWaves *kWave) void gemm_kernel(
 
 }  // namespace
 
+hipError_t launch_gemm_tiled(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
+                             const uint8_t *ws, const Groups &g, int N, int K, int epilogue,
+                             const Output &o, hipStream_t stream);
+
 hipError_t launch_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
                        const Groups &g, int N, int K, int epilogue, const Output &o,
                        hipStream_t stream) {
+    if (g.S > 64) return launch_gemm_tiled(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
     const int KB = (K + kStep - 1) / kStep;
     const dim3 grid((unsigned)most_tiles(g.S, g.E, 32, g.offsets != nullptr),
                     (unsigned)((N + 64 * kWaves - 1) / (64 * kWaves)));
