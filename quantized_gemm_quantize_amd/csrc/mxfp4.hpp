@@ -84,45 +84,50 @@ struct Tile {
     int m0, m1;  // its rows: m0 .. m1-1 with m1 the end of the group
 };
 
-// Tiles of BM rows in group e (0 past the last group); lo, n: its rows. Bounds
-// that a malformed offsets array could break are clamped, so rows stay inside
-// [0, S). Group E holds the rows without a weight.
-template <int BM>
-__device__ __forceinline__ int group_tiles(const Groups &g, int e, int &lo, int &n) {
-    lo = n = 0;
-    if (e <= g.E) {
-        lo = min(max(g.offsets[e], 0), g.S);
-        n = (e < g.E ? min(max(g.offsets[e + 1], lo), g.S) : g.S) - lo;
-    }
-    return (n + BM - 1) / BM;
+// Inclusive sum over the lanes of a wavefront, in six lane moves of the vector
+// unit (shuffles go through LDS: several times their latency, and every
+// workgroup of the grouped kernels starts with this).
+__device__ __forceinline__ int scan_lanes(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // last lane of rows 0, 2 to 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2, 3
+    return v;
+}
+
+// Group `e` of 64 consecutive ones, one per lane: its first row and rows (none
+// past group E, which holds the rows without a weight). Bounds that a malformed
+// offsets array could break are clamped, so rows stay inside [0, S).
+__device__ __forceinline__ void group_rows(const Groups &g, int e, int &lo, int &n) {
+    const int a = g.offsets[min(e, g.E)], b = g.offsets[min(e + 1, g.E)];
+    lo = min(max(a, 0), g.S);
+    n = e < g.E ? min(max(b, lo), g.S) - lo : e == g.E ? g.S - lo : 0;
 }
 
 // All tiles of BM rows, found by every wavefront for itself.
 template <int BM>
 __device__ __forceinline__ int count_tiles(const Groups &g) {
-    int own = 0, lo, n;
-    for (int e = threadIdx.x & (kWave - 1); e <= g.E; e += kWave) own += group_tiles<BM>(g, e, lo, n);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) own += __shfl_xor(own, off, kWave);
-    return __builtin_amdgcn_readfirstlane(own);
+    int own = 0;
+    for (int base = 0; base <= g.E; base += kWave) {
+        int lo, n;
+        group_rows(g, base + (threadIdx.x & (kWave - 1)), lo, n);
+        own += (n + BM - 1) / BM;
+    }
+    return __builtin_amdgcn_readlane(scan_lanes(own), kWave - 1);
 }
 
-// Tile t of the groups' rows cut into tiles of BM rows, group after group:
-// 64 groups at a time, an inclusive scan of the tile counts over the lanes.
+// Tile t of the groups' rows cut into tiles of BM rows, group after group, 64
+// groups at a time.
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const Groups &g, int t) {
     if (!g.offsets) return Tile{t * BM < g.S ? 0 : -1, t * BM, g.S};
-    const int lane = threadIdx.x & (kWave - 1);
     int before = 0;
     for (int base = 0; base <= g.E; base += kWave) {
         int lo, n;
-        const int own = group_tiles<BM>(g, base + lane, lo, n);
-        int upto = own;
-#pragma unroll
-        for (int off = 1; off < kWave; off <<= 1) {
-            const int o = __shfl_up(upto, off, kWave);
-            if (lane >= off) upto += o;
-        }
+        group_rows(g, base + (threadIdx.x & (kWave - 1)), lo, n);
+        const int own = (n + BM - 1) / BM, upto = scan_lanes(own);
         const uint64_t hit = __builtin_amdgcn_ballot_w64(before + upto > t);
         if (hit) {
             const int l = __builtin_ctzll(hit);
@@ -150,9 +155,12 @@ __device__ __forceinline__ int source_row(const Groups &g, int r) {
     return g.row_token ? min(max(g.row_token[r], 0), g.T - 1) : r;
 }
 
-// Gate and up projections of one hidden unit -> its activation.
+// Gate and up projections of one hidden unit -> its activation, gate / (1 +
+// exp(-gate)) * up. The reciprocal is v_rcp_f32 (within 1 ulp; it flushes
+// results below 2^-126, which only gates under -87 reach): the correctly
+// rounded division made the epilogue of a 256 x 256 tile several times as long.
 __device__ __forceinline__ float swiglu(float gate, float up) {
-    return gate / (1.0f + __expf(-gate)) * up;
+    return gate * __builtin_amdgcn_rcpf(1.0f + __expf(-gate)) * up;
 }
 
 }  // namespace mxfp4

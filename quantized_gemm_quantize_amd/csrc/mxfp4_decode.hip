@@ -1,0 +1,268 @@
+// Weight-streaming MXFP4 products (few rows): a dense layer of up to 64 rows, or
+// groups of a few rows each.
+//
+// With few rows the kernel is bound by reading each weight in use from HBM
+// once. A workgroup owns 16 CT channels of one group's weight and up to 16 MT
+// of its rows; its WAVES wavefronts split K in pairs of 128 bytes of codes (256
+// elements), wavefront w taking pairs w, w + WAVES, ..., so that neighbouring
+// wavefronts read neighbouring cache lines.
+//
+//  - Codes of weights and activations travel global -> LDS with 16-byte
+//    direct-to-LDS loads of 8 whole lines each, two pairs in flight per
+//    wavefront, into LDS that only this wavefront touches: the mainloop has no
+//    barrier. Slot i of a load holds row 8h + i / 8, chunk
+//    (i % 8) ^ (i / 8) ^ h, so that fragment reads meet distinct banks.
+//  - v_mfma_scale_f32_16x16x128_f8f6f4, twice per pair: lane l holds row l % 16
+//    and, in product t, block 2 (l / 16) + t of the pair's eight; its two scale
+//    bytes are one 16-bit load.
+//  - Blocks past K are read from inside the row; their scale codes are the
+//    storage's padding 0 on both sides, and add nothing.
+//  - The wavefronts' partial sums are joined in LDS in a fixed order. SwiGLU
+//    needs whole blocks of 32 hidden units: CT = 4, 64 channels.
+#include "launch.hpp"
+#include "mxfp4_epilogue.hpp"
+
+namespace mxfp4 {
+namespace {
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) void global_void;
+
+__device__ __forceinline__ v4f mfma_16x16x128(int sel, v4i a, uint32_t sa, v4i b, uint32_t sb, v4f c) {
+    if (sel == 0)
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, 0, (int)sa, 0, (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, 1, (int)sa, 1, (int)sb);
+}
+
+// One pair in flight: its scales, and the LDS that its codes fill.
+template <int MT, int CT>
+struct Pair {
+    uint32_t sw[CT], sx[MT];
+};
+
+template <int MT, int CT, int WAVES, Epilogue EP>
+__global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
+    const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xs, const uint8_t *__restrict__ wq,
+    const uint8_t *__restrict__ ws, Groups grp, int N, int K, int KB, int tiles_n, Output o) {
+    constexpr int kSlots = WAVES * (MT + CT) * 128;  // 16-byte slots of one pair, all wavefronts
+    // one array per pair in flight: the compiler then waits for that pair only
+    __shared__ uint4 q0[kSlots], q1[kSlots];
+    static_assert(WAVES * MT * CT * kWave <= kSlots, "the partial sums fit a pair's place");
+    w8a8::lds_poison(q0);
+    w8a8::lds_poison(q1);
+    w8a8::lds_poison_done();
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const Tile t = find_tile<16 * MT>(grp, blockIdx.x / tiles_n);
+    if (t.e < 0) return;
+    const int n0 = (blockIdx.x % tiles_n) * 16 * CT;
+    const int rows = t.m1 - t.m0;
+    const bool weight = t.e < grp.E;
+
+    v4f acc[MT][CT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[m][c] = v4f{};
+    const int r16 = lane & 15, quarter = lane >> 4;
+    if (weight) {
+        const int lr = lane >> 3, lc = lane & 7;
+        int row[MT][2], srow[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) row[m][h] = source_row(grp, t.m0 + min(16 * m + 8 * h + lr, rows - 1));
+            srow[m] = source_row(grp, t.m0 + min(16 * m + r16, rows - 1));
+        }
+        const uint8_t *wrow[CT][2], *xrow[MT][2], *wsc[CT], *xsc[MT];
+        int chunk[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            chunk[h] = lc ^ lr ^ h;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                wrow[c][h] = wq + ((int64_t)t.e * N + min(n0 + 16 * c + 8 * h + lr, N - 1)) * (K / 2);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) xrow[m][h] = xq + (int64_t)row[m][h] * (K / 2);
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+            wsc[c] = ws + ((int64_t)t.e * KB * N + min(n0 + 16 * c + r16, N - 1)) * 8 + 2 * quarter;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xsc[m] = xs + (int64_t)srow[m] * 8 + 2 * quarter;
+
+        auto load = [&](int p, uint4 *q, Pair<MT, CT> &s) {
+            uint4 *mine = q + wave * (MT + CT) * 128;
+            int at[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)  // a chunk past K: the pair's first one
+                at[h] = p * kStepBytes + (p * kStepBytes + chunk[h] * 16 < K / 2 ? chunk[h] * 16 : 0);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    __builtin_amdgcn_global_load_lds((global_void *)(xrow[m][h] + at[h]),
+                                                     (lds_void *)(mine + 128 * m + 64 * h), 16, 0, 0);
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    __builtin_amdgcn_global_load_lds((global_void *)(wrow[c][h] + at[h]),
+                                                     (lds_void *)(mine + 128 * (MT + c) + 64 * h), 16, 0,
+                                                     w8a8::kLdsLoadStream);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) s.sx[m] = *reinterpret_cast<const uint16_t *>(xsc[m] + (int64_t)p * grp.T * 8);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) s.sw[c] = *reinterpret_cast<const uint16_t *>(wsc[c] + (int64_t)p * N * 8);
+        };
+        auto multiply = [&](const uint4 *q, const Pair<MT, CT> &s) {
+            const uint4 *mine = q + wave * (MT + CT) * 128;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int slot = (r16 >> 3) * 64 + (r16 & 7) * 8 + ((2 * quarter + u) ^ (r16 & 7) ^ (r16 >> 3));
+                v4i w[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) w[c] = __builtin_bit_cast(v4i, mine[128 * (MT + c) + slot]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const v4i x = __builtin_bit_cast(v4i, mine[128 * m + slot]);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[m][c] = mfma_16x16x128(u, w[c], s.sw[c], x, s.sx[m], acc[m][c]);
+                }
+            }
+        };
+        Pair<MT, CT> s0, s1;
+        int p = wave;
+        if (p < KB) load(p, q0, s0);
+        if (p + WAVES < KB) load(p + WAVES, q1, s1);
+        for (; p < KB; p += 2 * WAVES) {
+            multiply(q0, s0);
+            if (p + 2 * WAVES < KB) load(p + 2 * WAVES, q0, s0);
+            if (p + WAVES < KB) multiply(q1, s1);
+            if (p + 3 * WAVES < KB) load(p + 3 * WAVES, q1, s1);
+        }
+    }
+
+    // acc[m][c], element i of lane l: row 16 m + l % 16, channel 16 c + 4 (l / 16) + i
+    __syncthreads();  // every wavefront has read its last fragments
+    v4f(*red)[MT * CT][kWave] = reinterpret_cast<v4f(*)[MT * CT][kWave]>(q0);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) red[wave][m * CT + c][lane] = acc[m][c];
+    __syncthreads();
+    if constexpr (EP != kSwiglu) {
+        // one thread: 4 channels of a row
+        for (int e = threadIdx.x; e < MT * CT * kWave; e += WAVES * kWave) {
+            const int tile = e / kWave, l = e % kWave;
+            v4f sum = red[0][tile][l];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) {
+                const v4f v = red[w][tile][l];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] += v[i];
+            }
+            const int m = 16 * (tile / CT) + (l & 15), n = n0 + 16 * (tile % CT) + 4 * (l >> 4);
+            if (m >= rows || n >= N) continue;
+            const int64_t at = (int64_t)(t.m0 + m) * N + n;
+            if constexpr (EP == kOutF32)
+                *reinterpret_cast<v4f *>(static_cast<float *>(o.out) + at) = sum;
+            else if constexpr (EP == kOutBf16)
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.out) + at) =
+                    make_uint2(w8a8::pack_bf16x2(sum[0], sum[1]), w8a8::pack_bf16x2(sum[2], sum[3]));
+            else
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.out) + at) =
+                    make_uint2(pack_f16x2(sum[0], sum[1]), pack_f16x2(sum[2], sum[3]));
+        }
+    } else {
+        static_assert(CT == 4 || EP != kSwiglu, "a block of 32 hidden units");
+        // one thread: 4 channels, i.e. hidden units 2 u and 2 u + 1 of the block
+        // with u = 4 c + l / 16; 16 threads share a row's block
+        const int F = N / 2, f0 = n0 / 2;
+        for (int e = threadIdx.x; e < MT * 16 * 16; e += WAVES * kWave) {
+            const int m = e >> 4, u = e & 15;  // row of the tile, pair of hidden units
+            const int l = (m & 15) + 16 * (u & 3), tile = (m >> 4) * CT + (u >> 2);
+            v4f sum = red[0][tile][l];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) {
+                const v4f v = red[w][tile][l];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] += v[i];
+            }
+            const float h0 = swiglu(sum[0], sum[1]), h1 = swiglu(sum[2], sum[3]);
+            uint32_t top = max(__float_as_uint(h0) & 0x7FFFFFFFu, __float_as_uint(h1) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, kWave));
+            const uint32_t code = scale_code(__uint_as_float(top));
+            uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, h0, h1, scale_value(code), 0) & 0xFFu;
+            if (code == 255) c = 0;
+            if (m >= rows || f0 >= F) continue;
+            const int64_t row = t.m0 + m;
+            o.codes[row * (F / 2) + f0 / 2 + u] = (uint8_t)c;
+            if (u == 0) {
+                uint8_t *s = o.scales + ((int64_t)(f0 / kStep) * grp.S + row) * 8;
+                const int b = (f0 / 32) % 8;
+                s[b] = (uint8_t)code;
+                if (f0 + 32 == F)
+                    for (int i = b + 1; i < 8; ++i) s[i] = 0;
+            }
+        }
+    }
+}
+
+template <int MT, int CT, int WAVES, Epilogue EP>
+hipError_t launch_ep(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                     const Groups &g, int N, int K, const Output &o, hipStream_t stream) {
+    const int KB = (K + kStep - 1) / kStep, tiles_n = (N + 16 * CT - 1) / (16 * CT);
+    const int64_t tiles = most_tiles(g.S, g.E, 16 * MT, g.offsets != nullptr) * tiles_n;
+    decode_kernel<MT, CT, WAVES, EP><<<dim3((unsigned)tiles), dim3(WAVES * kWave), 0, stream>>>(
+        xq, xs, wq, ws, g, N, K, KB, tiles_n, o);
+    return hipGetLastError();
+}
+
+template <int MT, int CT, int WAVES>
+hipError_t launch_plain(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                        const Groups &g, int N, int K, int epilogue, const Output &o, hipStream_t stream) {
+    switch (epilogue) {
+        case kOutBf16: return launch_ep<MT, CT, WAVES, kOutBf16>(xq, xs, wq, ws, g, N, K, o, stream);
+        case kOutF16: return launch_ep<MT, CT, WAVES, kOutF16>(xq, xs, wq, ws, g, N, K, o, stream);
+        default: return launch_ep<MT, CT, WAVES, kOutF32>(xq, xs, wq, ws, g, N, K, o, stream);
+    }
+}
+
+// Channels and wavefronts per workgroup. Grouped rows: 64 channels by 2
+// wavefronts (40 KB of LDS: four workgroups of a CU hide each other's start and
+// end; 32 experts' down products of 8 rows, 25.5 us against 28.5 with 4
+// wavefronts), unless there are too few workgroups for that: 4 wavefronts
+// (1 token, 4 experts: gate and up 9.6 against 10.2 us, down 5.6 against 6.1).
+// Dense: 16 channels by 8 wavefronts, as a single weight has few channels.
+template <int MT>
+hipError_t launch_rows(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                       const Groups &g, int N, int K, int epilogue, const Output &o, hipStream_t stream) {
+    if constexpr (MT < 4) {
+        const int64_t quads = most_tiles(g.S, g.E, 16 * MT, true) * ((N + 63) / 64);
+        const bool few = quads <= 2 * w8a8::device_cu_count();
+        if (epilogue == kSwiglu)
+            return few ? launch_ep<MT, 4, 4, kSwiglu>(xq, xs, wq, ws, g, N, K, o, stream)
+                       : launch_ep<MT, 4, 2, kSwiglu>(xq, xs, wq, ws, g, N, K, o, stream);
+        if (g.offsets)
+            return few ? launch_plain<MT, 2, 4>(xq, xs, wq, ws, g, N, K, epilogue, o, stream)
+                       : launch_plain<MT, 4, 2>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
+        return launch_plain<MT, 1, 8>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
+    } else {
+        return launch_plain<MT, 1, 4>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_gemm_decode(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
+                              const uint8_t *ws, const Groups &g, int N, int K, int epilogue,
+                              const Output &o, int row_tiles, hipStream_t stream) {
+    if (row_tiles <= 1) return launch_rows<1>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
+    if (row_tiles <= 2) return launch_rows<2>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
+    return launch_rows<4>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
+}
+
+}  // namespace mxfp4

@@ -47,9 +47,12 @@ __device__ __forceinline__ void store_tile(const v16f &acc, void *out, int64_t m
 // block. A lane holds units 16 jj + 4 g + 2 half + 0..1 of row m (jj: tile);
 // the two halves join their largest magnitudes and swap codes so that each
 // writes 8 consecutive bytes. The activations are never rounded in between.
-__device__ __forceinline__ void store_swiglu(const v16f &lo, const v16f &hi, const Output &o,
-                                             int64_t m, bool live, int n0, int half, int N, int S) {
-    const int F = N / 2, f0 = n0 / 2;  // this block's first hidden unit
+struct Hidden {
+    uint2 codes;    // bytes 8 half .. + 7 of the block's 16
+    uint32_t code;  // its scale
+};
+
+__device__ __forceinline__ Hidden quantize_swiglu(const v16f &lo, const v16f &hi, int half) {
     float h[2][8];
     uint32_t top = 0;
 #pragma unroll
@@ -80,14 +83,22 @@ __device__ __forceinline__ void store_swiglu(const v16f &lo, const v16f &hi, con
     const uint32_t keep = half ? c[1] : c[0], give = half ? c[0] : c[1];
     const uint32_t take = (uint32_t)__shfl_xor((int)give, 32, kWave);
     const uint32_t even = half ? take : keep, odd = half ? keep : take;
-    const uint2 w = make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),
-                               __builtin_amdgcn_perm(odd, even, 0x07030602u));
+    return Hidden{make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),
+                             __builtin_amdgcn_perm(odd, even, 0x07030602u)),
+                  code};
+}
+
+// The block of hidden units of channels n0 .. n0 + 63 of row m; with the last
+// block of a row, the zeros that pad its scales.
+__device__ __forceinline__ void store_hidden(const Hidden &h, const Output &o, int64_t m, bool live,
+                                             int n0, int half, int N, int S) {
+    const int F = N / 2, f0 = n0 / 2;  // this block's first hidden unit
     if (!live || f0 >= F) return;
-    *reinterpret_cast<uint2 *>(o.codes + m * (F / 2) + f0 / 2 + 8 * half) = w;
+    *reinterpret_cast<uint2 *>(o.codes + m * (F / 2) + f0 / 2 + 8 * half) = h.codes;
     if (half == 0) {
         uint8_t *s = o.scales + ((int64_t)(f0 / kStep) * S + m) * 8;
         const int b = (f0 / 32) % 8;
-        s[b] = (uint8_t)code;
+        s[b] = (uint8_t)h.code;
         if (f0 + 32 == F)
             for (int i = b + 1; i < 8; ++i) s[i] = 0;
     }

@@ -6,17 +6,17 @@
 // A workgroup of 4 wavefronts computes a BM x BN tile; each wavefront owns a
 // (BM/2) x (BN/2) part as 32x32 tiles of v_mfma_scale_f32_32x32x64_f8f6f4,
 // which takes two fp4 blocks of 32 per row and their scales and accumulates
-// in fp32. A K stage is 256 elements: 128 bytes of codes and 8 scale bytes per
-// row. Lanes 0-31 take blocks 0-3 of the stage and lanes 32-63 blocks 4-7, for
-// both operands, so the stage's four K steps use the four bytes of one scale
-// register.
+// in fp32. A K stage is CH = 8 chunks of 16 bytes per row (256 elements, 8
+// scale bytes) or CH = 4 (128 elements, 4 scale bytes). Lanes 0-31 take the
+// first half of the stage's blocks and lanes 32-63 the second, for both
+// operands, so the stage's K steps use consecutive bytes of one scale register.
 //
 //  - Codes and scales travel global -> LDS with direct-to-LDS loads (16 and 4
 //    bytes per lane) through a ring of STAGES buffers, loads running STAGES-1
-//    stages ahead of the MFMAs. Rows of codes are 128 bytes; chunk c of row r
-//    sits at slot c ^ (r % 8) ^ ((r / 8) % 2), which keeps the 16-byte fragment
-//    reads free of bank conflicts. Scales lie as one 32-bit word per lane of a
-//    32-row fragment.
+//    stages ahead of the MFMAs. Chunk c of row r sits at slot c ^ swz(r), which
+//    keeps the 16-byte fragment reads free of bank conflicts. Scales lie as
+//    32-bit words: CH = 8, one per lane of a 32-row fragment; CH = 4, one per
+//    row, read by both halves.
 //  - Rows past the group or N are read from the last valid row (their outputs
 //    are never stored). Blocks past K are read from inside the row; both sides'
 //    scale codes there are the storage's padding 0, so that each product is
@@ -27,6 +27,8 @@
 //    of a row. Outputs are staged in the wavefront's own LDS and stored as
 //    16-byte pieces of contiguous rows; SwiGLU joins gate and up in registers
 //    and stores the hidden activations as MXFP4, 17/64 of their bf16 bytes.
+#include <algorithm>
+
 #include "launch.hpp"
 #include "mxfp4_epilogue.hpp"
 
@@ -35,60 +37,103 @@ namespace {
 
 using w8a8::vm_barrier;
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * kWave;
-constexpr int kChunks = 8;    // 16-byte chunks of codes per row and stage
-constexpr int kSteps = 4;     // MFMA K steps per stage
 
 typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(1))) void global_void;
 
-__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+// 8 consecutive rows that read the same chunk meet 8 distinct 16-byte bank groups.
+template <int CH>
+__device__ __forceinline__ int swz(int row) {
+    static_assert(CH == 8 || CH == 4, "128- or 64-byte stage rows");
+    return CH == 8 ? (row & 7) ^ ((row >> 3) & 1) : ((row >> 1) & 3) ^ ((row >> 3) & 1);
+}
 
 struct Operands {
     const uint8_t *xq, *xs, *wq, *ws;
 };
 
-template <int BM, int BN>
+// BM x BN outputs by GM x GN wavefronts, CH chunks per row and stage.
+template <int BM, int BN, int GM, int GN, int CH>
 struct Shape {
-    static constexpr int kA = BM / 32, kB = BN / 32;              // code loads per wavefront and stage
-    static constexpr int kScale = (BM + BN) / 32 / kWaves;        // scale loads per wavefront and stage
-    static constexpr int kLoads = kA + kB + kScale;
-    static constexpr int kCodes = (BM + BN) * kChunks;            // 16-byte slots of codes per stage
-    static constexpr int kStage = kCodes + (BM + BN) / 2;         // and of scales
+    static constexpr int kBM = BM, kBN = BN, kCH = CH, kWaves = GM * GN;
+    static constexpr int kBytes = 16 * CH;                        // of codes per row and stage
+    static constexpr int kSteps = CH / 2;                         // MFMA K steps per stage
+    static constexpr int kRows = 64 / CH;                         // rows per code load of a wavefront
+    static constexpr int kA = BM / kRows / kWaves, kB = BN / kRows / kWaves;  // code loads
+    // scale loads: rows per load, loads of a wavefront per operand (with fewer
+    // loads than wavefronts some repeat another's, so that all wavefronts have
+    // the same number of loads in flight)
+    static constexpr int kScaleRows = CH == 8 ? 32 : 64;
+    static constexpr int kSA = (BM / kScaleRows + kWaves - 1) / kWaves;
+    static constexpr int kSB = (BN / kScaleRows + kWaves - 1) / kWaves;
+    static constexpr int kLoads = kA + kB + kSA + kSB;
+    static constexpr int kCodes = (BM + BN) * CH;                 // 16-byte slots of codes per stage
+    static constexpr int kStage = kCodes + (BM + BN) * CH / 16;   // and of scales
 };
 
+// Raw buffers and their direct-to-LDS loads of 4 or 16 bytes per lane (types and
+// builtins of the device pass; the host pass only parses the kernels).
+#ifdef __HIP_DEVICE_COMPILE__
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+// A buffer of `bytes` bytes (at most 2^32 - 1 can be addressed).
+__device__ __forceinline__ Buffer buffer(const uint8_t *p, int64_t bytes) {
+    const int64_t n = bytes < 0xFFFFFFFFll ? bytes : 0xFFFFFFFFll;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)(uint32_t)n, 0x00027000);
+}
+
+__device__ __forceinline__ void load_lds16(Buffer b, void *dst, uint32_t lane_off, int off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void *)dst, 16, lane_off, off, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(Buffer b, void *dst, uint32_t lane_off, int off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void *)dst, 4, lane_off, off, 0, 0);
+}
+#else
+struct Buffer {};
+__device__ Buffer buffer(const uint8_t *p, int64_t bytes);
+__device__ void load_lds16(Buffer b, void *dst, uint32_t lane_off, int off);
+__device__ void load_lds4(Buffer b, void *dst, uint32_t lane_off, int off);
+#endif
+
 // Where this lane's share of every stage comes from, and what it fills: a
-// uniform address that moves with the stage, plus a 32-bit offset per lane that
-// does not (64-bit addresses per lane would not fit the registers).
-template <int BM, int BN>
+// buffer descriptor per operand, a 32-bit offset per lane that stays, and a
+// uniform offset that moves with the stage. (Addresses in vector registers
+// cost a 64-bit addition per load, which holds up the MFMAs' issue.)
+struct Sources {
+    Buffer a, b, sa, sb;
+};
+
+template <typename Sh>
 struct Loads {
-    using Sh = Shape<BM, BN>;
-    const uint8_t *a, *b, *sa, *sb;   // uniform
-    int64_t sa_step, sb_step;         // bytes from one stage's scales to the next
-    uint32_t aoff[Sh::kA], boff[Sh::kB], soff[Sh::kScale];
+    Sources src, none;                // none: the same buffers with no bytes (loads give 0)
+    int sa_step, sb_step;             // bytes from one 256-element step's scales to the next
+    uint32_t aoff[Sh::kA], boff[Sh::kB], saoff[Sh::kSA], sboff[Sh::kSB];
     int kc;                           // chunk of the row that this lane loads
     int half_k;                       // bytes of a row
     int nk;                           // stages
+
+    __device__ __forceinline__ Sources at(int j) const { return j < nk ? src : none; }
 };
 
 // Load l of stage j: this lane's 16 bytes of codes or 4 bytes of scales.
-template <int BM, int BN, bool KTAIL>
-__device__ __forceinline__ void load_one(const Loads<BM, BN> &g, int l, int j, uint4 *st, int wave) {
-    using Sh = Shape<BM, BN>;
-    static_assert(BM / 32 % kWaves == 0, "a scale load is of one operand in every wavefront");
+template <typename Sh, bool KTAIL>
+__device__ __forceinline__ void load_one(const Loads<Sh> &g, const Sources &src, int l, int j, uint4 *st,
+                                         int wave) {
+    constexpr int BM = Sh::kBM, BN = Sh::kBN, CH = Sh::kCH, kWaves = Sh::kWaves;
     if (l < Sh::kA + Sh::kB) {
-        uint4 *dst = st + 64 * wave + (l < Sh::kA ? 256 * l : BM * kChunks + 256 * (l - Sh::kA));
-        const uint8_t *base = (l < Sh::kA ? g.a : g.b) + (int64_t)j * kStepBytes;
+        uint4 *dst = st + 64 * (wave + kWaves * (l < Sh::kA ? l : l - Sh::kA)) + (l < Sh::kA ? 0 : BM * CH);
         uint32_t off = l < Sh::kA ? g.aoff[l] : g.boff[l - Sh::kA];
         // a chunk past K: the stage's first one instead (it is inside the row)
-        if (KTAIL && g.kc * 16 + j * kStepBytes >= g.half_k) off -= g.kc * 16;
-        __builtin_amdgcn_global_load_lds((global_void *)(base + off), (lds_void *)dst, 16, 0, 0);
+        if (KTAIL && g.kc * 16 + j * Sh::kBytes >= g.half_k) off -= g.kc * 16;
+        load_lds16(l < Sh::kA ? src.a : src.b, dst, off, j * Sh::kBytes);
     } else {
         const int q = l - Sh::kA - Sh::kB;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(st + Sh::kCodes) + 64 * (wave + kWaves * q);
-        const uint8_t *base = q < BM / 32 / kWaves ? g.sa + j * g.sa_step : g.sb + j * g.sb_step;
-        __builtin_amdgcn_global_load_lds((global_void *)(base + g.soff[q]), (lds_void *)dst, 4, 0, 0);
+        const bool is_a = q < Sh::kSA;
+        constexpr int kFragsA = BM / Sh::kScaleRows, kFragsB = BN / Sh::kScaleRows;
+        const int f = is_a ? (wave + kWaves * q) % kFragsA : kFragsA + (wave + kWaves * (q - Sh::kSA)) % kFragsB;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(st + Sh::kCodes) + 64 * f;
+        const int step = CH == 8 ? j : j >> 1, word = CH == 8 ? 0 : 4 * (j & 1);
+        if (is_a) load_lds4(src.sa, dst, g.saoff[q], step * g.sa_step + word);
+        else load_lds4(src.sb, dst, g.sboff[q - Sh::kSA], step * g.sb_step + word);
     }
 }
 
@@ -99,268 +144,361 @@ struct Frags {
     uint32_t sx[TM], sw[TN];
 };
 
-// One K stage: multiply the stage held in `rd` while (AHEAD) loading stage j
-// into `wr`, and (unless LAST) read the first fragments of the next stage from
-// `nx`. The barrier sits before the last K step: by then every wavefront has
-// read all of this stage's fragments, and the next stage's first ones are read
-// while the last step multiplies. Per K step, the next step's fragment reads
-// go out in two bursts after the first two MFMAs and one load follows each
-// further MFMA; the order is pinned, as a burst of loads would hold the MFMAs.
-// The code is one straight line (whole stages are peeled instead of branching
-// around loads): the compiler moves these MFMAs across branches, down to where
-// their sums are used, and then keeps every fragment alive.
-template <int BM, int BN, int STAGES, bool KTAIL, bool AHEAD, bool LAST, int TM, int TN>
-__device__ __forceinline__ void stage(const Loads<BM, BN> &g, const uint4 *__restrict__ rd,
-                                      uint4 *__restrict__ wr, const uint4 *__restrict__ nx, int j_ahead,
-                                      int wave, int a_frag, int b_frag, int a_scale, int b_scale,
+// This lane's scale bytes, in order from byte 0: a word holds them all (CH = 8)
+// or those of both halves (CH = 4).
+template <int CH>
+__device__ __forceinline__ uint32_t lane_scales(uint32_t word, int half) {
+    return CH == 8 ? word : word >> (16 * half);
+}
+
+// One K stage: multiply the stage held in `rd`, read the first fragments of the
+// next stage from `nx`, and load stage s + 2 into `wr`. The barrier before the
+// last K step says that every wavefront has read all of this stage's fragments
+// and that the next stage has landed. With two buffers `wr` is `rd` again, so
+// the loads follow the barrier; with three it is the buffer of the stage
+// before, free since the last barrier, so the loads are spread over all K steps
+// (256 x 128 tiles, 2048 x 4096 x 4096: 22.9 us in one burst, 19.7 spread). One
+// fragment read or load follows an MFMA; the order is pinned, as bursts hold the
+// MFMAs. The code is one straight line, the same for every stage (past the last
+// one, the loads come from buffers of no bytes and the fragments are not used):
+// the compiler moves these MFMAs across branches, down to where their sums are
+// used, and then keeps every fragment alive.
+template <typename Sh, int NB, bool KTAIL, int TM, int TN>
+__device__ __forceinline__ void stage(const Loads<Sh> &g, const uint4 *rd, const uint4 *nx, uint4 *wr,
+                                      int s, int wave, int a_frag, int b_frag, int a_scale, int b_scale,
                                       int half, int fswz, v16f (&acc)[TM][TN], Frags<TM, TN> &f) {
-    using Sh = Shape<BM, BN>;
+    constexpr int CH = Sh::kCH, kSteps = Sh::kSteps;
     constexpr int NMF = TM * TN;
-    // three buffers: the stage being loaded is not the next one read, so its
-    // loads may follow the barrier too and the barrier leaves the last ones in
-    // flight; two buffers: every load precedes the barrier
-    constexpr bool LATE = STAGES == 3;
-    constexpr int LSTEPS = LATE ? kSteps : kSteps - 1;
-    constexpr int LPK = (Sh::kLoads + LSTEPS - 1) / LSTEPS;
-    constexpr int LPRE = LATE ? ((kSteps - 1) * LPK < Sh::kLoads ? (kSteps - 1) * LPK : Sh::kLoads) : 0;
-    constexpr int NSLOT = NMF > 2 + LPK ? NMF : 2 + LPK;
-    const uint4 *next = STAGES == 2 ? wr : nx;
+    constexpr int RPS = (TM + TN + NMF - 1) / NMF;                 // reads per MFMA
+    constexpr int LSTEP0 = NB == 2 ? kSteps - 1 : 0;               // first K step with loads
+    constexpr int LPK = (Sh::kLoads + kSteps - LSTEP0 - 1) / (kSteps - LSTEP0);  // loads per K step
+    constexpr int LPRE = NB == 2 ? 0 : (kSteps - 1) * LPK < Sh::kLoads ? (kSteps - 1) * LPK : Sh::kLoads;
+    // loads follow the last MFMAs of a K step, where no reads are left
+    constexpr int LPS = NMF > 2 ? (LPK + NMF - 3) / (NMF - 2) : LPK;  // loads per MFMA
+    constexpr int LFIRST = NMF - (LPK + LPS - 1) / LPS;
+    constexpr int kSc = CH == 8 ? 64 : 32;                         // scale words per 32-row fragment
+    const Sources src_bufs = g.at(s + 2);
     uint32_t sx[TM], sw[TN];
 #pragma unroll
     for (int kk = 0; kk < kSteps; ++kk) {
         const int p = kk & 1;
-        if (kk == kSteps - 1 && !LAST) vm_barrier<AHEAD ? LPRE : 0>();
-        const uint4 *src = kk + 1 < kSteps ? rd : next;
-        const int ch = (4 * half + (kk + 1) % kSteps) ^ fswz;
+        const bool last_step = kk == kSteps - 1;
+        if (last_step) vm_barrier<LPRE>();  // the loads of this stage may be in flight
+        const uint4 *src = last_step ? nx : rd;
+        const int ch = (kSteps * half + (kk + 1) % kSteps) ^ fswz;
 #pragma unroll
-        for (int q = 0; q < NSLOT; ++q) {
-            if (q < NMF) {
-                const int i = q / TN, j = q % TN;
-                acc[i][j] = mfma_32x32x64(kk, f.w[p][j], f.sw[j], f.x[p][i], f.sx[i], acc[i][j]);
+        for (int q = 0; q < NMF; ++q) {
+            const int i = q / TN, j = q % TN;
+            acc[i][j] = mfma_32x32x64(kk, f.w[p][j], f.sw[j], f.x[p][i], f.sx[i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = q * RPS; r < (q + 1) * RPS && r < TM + TN; ++r) {
+                if (r < TM) f.x[p ^ 1][r] = __builtin_bit_cast(v4i, src[a_frag + r * 32 * CH + ch]);
+                else f.w[p ^ 1][r - TM] = __builtin_bit_cast(v4i, src[b_frag + (r - TM) * 32 * CH + ch]);
+                if (last_step) {
+                    const uint32_t *sc = reinterpret_cast<const uint32_t *>(nx + Sh::kCodes);
+                    if (r < TM) sx[r] = lane_scales<CH>(sc[a_scale + kSc * r], half);
+                    else sw[r - TM] = lane_scales<CH>(sc[b_scale + kSc * (r - TM)], half);
+                }
+            }
+            if (kk >= LSTEP0 && q >= LFIRST) {
+#pragma unroll
+                for (int u = (q - LFIRST) * LPS; u < (q - LFIRST + 1) * LPS && u < LPK; ++u) {
+                    const int l = (kk - LSTEP0) * LPK + u;
+                    if (l < Sh::kLoads) load_one<Sh, KTAIL>(g, src_bufs, l, s + 2, wr, wave);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (q < 2 && !(LAST && kk == kSteps - 1)) {
+        }
+    }
 #pragma unroll
-                for (int r = q; r < TM + TN; r += 2) {
-                    if (r < TM) f.x[p ^ 1][r] = __builtin_bit_cast(v4i, src[a_frag + r * 32 * kChunks + ch]);
-                    else f.w[p ^ 1][r - TM] = __builtin_bit_cast(v4i, src[b_frag + (r - TM) * 32 * kChunks + ch]);
-                }
-                if (kk == kSteps - 1) {
-                    const uint32_t *sc = reinterpret_cast<const uint32_t *>(next + Sh::kCodes);
+    for (int i = 0; i < TM; ++i) f.sx[i] = sx[i];
 #pragma unroll
-                    for (int r = q; r < TM + TN; r += 2) {
-                        if (r < TM) sx[r] = sc[a_scale + 64 * r];
-                        else sw[r - TM] = sc[b_scale + 64 * (r - TM)];
+    for (int j = 0; j < TN; ++j) f.sw[j] = sw[j];
+}
+
+// Where one tile's operands are: the loads' addresses for this lane.
+template <typename Sh>
+__device__ __forceinline__ void aim(Loads<Sh> &g, const Operands &op, const Groups &grp,
+                                    const Tile &tile, int n0, int N, int K, int KB, int lane, int wave) {
+    constexpr int CH = Sh::kCH, kWaves = Sh::kWaves;
+    const int lrow = Sh::kRows * wave + lane / CH;
+    g.kc = (lane % CH) ^ swz<CH>(lrow);
+    g.half_k = K / 2;
+    g.nk = (K / 2 + Sh::kBytes - 1) / Sh::kBytes;
+    const int rows = tile.m1 - tile.m0;
+    // without row_token the tile's own rows, else rows anywhere in xq
+    const int64_t row0 = grp.row_token ? 0 : tile.m0;
+    const int64_t half_k = K / 2, first_n = (int64_t)tile.e * N + n0;
+    const uint8_t *a = op.xq + row0 * half_k, *b = op.wq + first_n * half_k, *sa = op.xs + row0 * 8,
+                  *sb = op.ws + ((int64_t)tile.e * KB * N + n0) * 8;
+    g.src = Sources{buffer(a, (grp.T - row0) * half_k), buffer(b, (N - n0) * half_k),
+                    buffer(sa, ((int64_t)KB * grp.T - row0) * 8), buffer(sb, ((int64_t)KB * N - n0) * 8)};
+    g.none = Sources{buffer(a, 0), buffer(b, 0), buffer(sa, 0), buffer(sb, 0)};
+    g.sa_step = grp.T * 8;
+    g.sb_step = N * 8;
+    auto a_row = [&](int r) -> uint32_t {
+        r = min(r, rows - 1);
+        return grp.row_token ? (uint32_t)source_row(grp, tile.m0 + r) : (uint32_t)r;
+    };
+    auto b_row = [&](int r) { return (uint32_t)min(r, N - n0 - 1); };
+    constexpr int kPass = Sh::kRows * kWaves;  // rows from one code load to the next
+#pragma unroll
+    for (int l = 0; l < Sh::kA; ++l) g.aoff[l] = a_row(lrow + kPass * l) * (uint32_t)(K / 2) + g.kc * 16;
+#pragma unroll
+    for (int l = 0; l < Sh::kB; ++l) g.boff[l] = b_row(lrow + kPass * l) * (uint32_t)(K / 2) + g.kc * 16;
+    // scale words: CH = 8, lane l of a fragment: row l % 32, word l / 32; CH = 4, row l
+    const int srow = CH == 8 ? lane & 31 : lane, sword = CH == 8 ? 4 * (lane >> 5) : 0;
+#pragma unroll
+    for (int q = 0; q < Sh::kSA; ++q)
+        g.saoff[q] = a_row((wave + kWaves * q) % (Sh::kBM / Sh::kScaleRows) * Sh::kScaleRows + srow) * 8 + sword;
+#pragma unroll
+    for (int q = 0; q < Sh::kSB; ++q)
+        g.sboff[q] = b_row((wave + kWaves * q) % (Sh::kBN / Sh::kScaleRows) * Sh::kScaleRows + srow) * 8 + sword;
+}
+
+template <typename Sh, bool KTAIL>
+__device__ __forceinline__ void load_stage(const Loads<Sh> &g, int j, uint4 *st, int wave) {
+    const Sources src = g.at(j);
+#pragma unroll
+    for (int l = 0; l < Sh::kLoads; ++l) load_one<Sh, KTAIL>(g, src, l, j, st, wave);
+}
+
+// Waits for this wavefront's vector-memory operations (vmcnt 0 only).
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));
+    asm volatile("" ::: "memory");
+}
+
+// The wavefront's outputs: piece by piece (32 rows of at most 128 bytes) through
+// its own 4 KB of LDS, 16-byte chunks permuted by the low row bits, so that each
+// store instruction writes 8 whole cache lines. (Stores straight from the
+// accumulators, 32 bytes of a row each: 38400 x 4096 x 1024 118 -> 168 us.)
+constexpr int kPieceSlots = 32 * 8;
+
+template <Epilogue EP, int TM, int TN>
+__device__ __forceinline__ void store_plain(const v16f (&acc)[TM][TN], uint4 *mine, void *out, int m0,
+                                            int m_end, int nw0, int N, int lane) {
+    constexpr int SIZE = EP == kOutF32 ? 4 : 2;
+    constexpr int PJ = SIZE == 4 || TN == 1 ? 1 : 2;    // 32-channel tiles per piece
+    static_assert(TN % PJ == 0, "whole pieces");
+    constexpr int CH = PJ * 32 * SIZE / 16;             // 16-byte chunks per row of a piece
+    const int row = lane & 31, half = lane >> 5;
+    uint4 *mr = mine + row * CH;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; j += PJ) {
+#pragma unroll
+            for (int p = 0; p < PJ; ++p)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const v16f &a = acc[i][j + p];
+                    const float a0 = a[4 * g], a1 = a[4 * g + 1], a2 = a[4 * g + 2], a3 = a[4 * g + 3];
+                    if constexpr (EP == kOutF32) {
+                        mr[(p * 8 + 2 * g + half) ^ (row & (CH - 1))] = __builtin_bit_cast(uint4, v4f{a0, a1, a2, a3});
+                    } else {
+                        const uint2 w = EP == kOutBf16
+                            ? make_uint2(w8a8::pack_bf16x2(a0, a1), w8a8::pack_bf16x2(a2, a3))
+                            : make_uint2(pack_f16x2(a0, a1), pack_f16x2(a2, a3));
+                        reinterpret_cast<uint2 *>(mr + ((p * 4 + g) ^ (row & (CH - 1))))[half] = w;
                     }
                 }
-            }
-            const int l = kk * LPK + (q - 2);
-            if (AHEAD && kk < LSTEPS && q >= 2 && q < 2 + LPK && l < Sh::kLoads)
-                load_one<BM, BN, KTAIL>(g, l, j_ahead, wr, wave);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-    if constexpr (!LAST) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) f.sx[i] = sx[i];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) f.sw[j] = sw[j];
-    }
-}
-
-// The wavefront's 32 x WN outputs of sub-tile row i: staged in its own LDS
-// (16-byte chunks permuted by the low row bits), then stored in whole pieces.
-template <Epilogue EP, int WN, int TN>
-__device__ __forceinline__ void store_rows(const v16f (&acc)[TN], uint4 *mine, void *out, int m0,
-                                           int m_end, int nw0, int N, int lane) {
-    constexpr int SIZE = EP == kOutF32 ? 4 : 2;
-    constexpr int CH = WN * SIZE / 16;   // 16-byte chunks per row
-    const int row = lane & 31, half = lane >> 5;
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const float a0 = acc[j][4 * g], a1 = acc[j][4 * g + 1], a2 = acc[j][4 * g + 2], a3 = acc[j][4 * g + 3];
-            if constexpr (EP == kOutF32) {
-                mine[row * CH + ((j * 8 + 2 * g + half) ^ (row & (CH - 1)))] =
-                    __builtin_bit_cast(uint4, v4f{a0, a1, a2, a3});
-            } else {
-                const uint2 w = EP == kOutBf16
-                    ? make_uint2(w8a8::pack_bf16x2(a0, a1), w8a8::pack_bf16x2(a2, a3))
-                    : make_uint2(pack_f16x2(a0, a1), pack_f16x2(a2, a3));
-                reinterpret_cast<uint2 *>(mine)[2 * (row * CH + ((j * 4 + g) ^ (row & (CH - 1)))) + half] = w;
+            for (int it = 0; it < 32 * CH / kWave; ++it) {
+                const int q = it * kWave + lane, r = q / CH, c = q % CH;
+                const int m = m0 + 32 * i + r, n = nw0 + 32 * j + c * (16 / SIZE);
+                const uint4 v = mine[r * CH + (c ^ (r & (CH - 1)))];
+                if (m < m_end && n < N)
+                    w8a8::store16_nt(static_cast<char *>(out) + ((int64_t)m * N + n) * SIZE, v);
             }
         }
-#pragma unroll
-    for (int it = 0; it < 32 * CH / kWave; ++it) {
-        const int q = it * kWave + lane, r = q / CH, c = q % CH;
-        const uint4 v = mine[r * CH + (c ^ (r & (CH - 1)))];
-        const int m = m0 + r, n = nw0 + c * (16 / SIZE);
-        if (m < m_end && n < N)
-            w8a8::store16_nt(static_cast<char *>(out) + ((int64_t)m * N + n) * SIZE, v);
-    }
 }
 
-template <int BM, int BN, int STAGES, bool KTAIL, Epilogue EP>
-__global__ __launch_bounds__(kThreads, 1) void tiled_kernel(Operands op, Groups grp, int N, int K,
-                                                            int KB, int tiles_m, int tiles_n,
-                                                            Output o) {
-    using Sh = Shape<BM, BN>;
-    constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
-    static_assert(STAGES == 2 || STAGES == 3, "double or triple buffering");
-    __shared__ uint4 lds[STAGES * Sh::kStage];
-    static_assert(kWaves * 32 * WN * 4 <= (int)sizeof(lds), "the staged outputs fit");
-    w8a8::lds_poison(lds);
+// One tile per workgroup, or (PERSIST: SwiGLU, whose stores are few) every
+// gridDim.x-th: then the first stages of the next tile are on their way before
+// the epilogue of a tile. Plain outputs gain nothing from it, as a workgroup
+// would wait for its stores with the next tile's loads (38400 x 4096 x 1024:
+// 118 us a workgroup per tile, 127 persistent).
+template <int BM, int BN, int GM, int GN, int CH, int NB, int OCC, bool KTAIL, Epilogue EP>
+__global__ __launch_bounds__(GM *GN *kWave, OCC *GM *GN / 4) void tiled_kernel(
+    Operands op, Groups grp, int N, int K, int KB, int tiles_m, int tiles_n, Output o) {
+    using Sh = Shape<BM, BN, GM, GN, CH>;
+    constexpr bool PERSIST = EP == kSwiglu;
+    constexpr int WM = BM / GM, WN = BN / GN, TM = WM / 32, TN = WN / 32;
+    // one array per buffer: the compiler then knows that loads into one do not concern
+    // reads of the other
+    static_assert(NB == 2 || NB == 3, "two or three buffers");
+    static_assert(Sh::kWaves * kPieceSlots <= Sh::kStage, "the staged outputs fit a buffer");
+    __shared__ uint4 b0[Sh::kStage], b1[Sh::kStage], b2[NB == 3 ? Sh::kStage : 1];
+    w8a8::lds_poison(b0);
+    w8a8::lds_poison(b1);
+    w8a8::lds_poison(b2);
     w8a8::lds_poison_done();
 
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wm = wave / 2, wn = wave % 2;
+    const int wm = wave / GN, wn = wave % GN;
+    const int frag_row = lane & 31, half = lane >> 5;
+    const int a_frag = (wm * WM + frag_row) * CH;
+    const int b_frag = BM * CH + (wn * WN + frag_row) * CH;
+    constexpr int kSc = CH == 8 ? 64 : 32;  // scale words per 32-row fragment
+    const int sl = CH == 8 ? lane : frag_row;
+    const int a_scale = wm * (WM / 32) * kSc + sl, b_scale = (BM / 32 + wn * (WN / 32)) * kSc + sl;
+    const int fswz = swz<CH>(frag_row);
 
-    // tiles XCD by XCD, in groups of 4 tile rows, so that concurrent tiles
-    // share activation and weight rows in one L2
     if (grp.offsets) tiles_m = count_tiles<BM>(grp);
     const int tiles = tiles_m * tiles_n;
-    if ((int)blockIdx.x >= tiles) return;
-    constexpr int kGroupM = 4;
-    const int t = w8a8::xcd_contiguous(blockIdx.x, tiles);
-    const int per_group = kGroupM * tiles_n;
-    const int first_m = (t / per_group) * kGroupM;
-    const int gsize = min(tiles_m - first_m, kGroupM);
-    const Tile tile = find_tile<BM>(grp, first_m + (t % per_group) % gsize);
-    const int n0 = ((t % per_group) / gsize) * BN;
-    if (tile.e < 0) return;
-
-    v16f acc[TM][TN];
+    // tiles XCD by XCD, in groups of 4 tile rows, so that concurrent tiles
+    // share activation and weight rows in one L2
+    auto locate = [&](int pid, int &n0) {
+        constexpr int kGroupM = 4;
+        const int t = w8a8::xcd_contiguous(pid, tiles);
+        const int per_group = kGroupM * tiles_n;
+        const int first_m = (t / per_group) * kGroupM;
+        const int gsize = min(tiles_m - first_m, kGroupM);
+        n0 = ((t % per_group) / gsize) * BN;
+        return find_tile<BM>(grp, first_m + (t % per_group) % gsize);
+    };
+    int pid = blockIdx.x;
+    if (pid >= tiles) return;
+    int n0;
+    Tile tile = locate(pid, n0);
+    Loads<Sh> g;
+    int first = 0;  // buffer of the first stage
+    auto start = [&] {
+        if (tile.e < 0 || tile.e >= grp.E) return;
+        aim(g, op, grp, tile, n0, N, K, KB, lane, wave);
+        // the last stage is always in the last buffer: the first one is where
+        // the number of stages asks for
+        first = g.nk % NB;
+        if (first == 0) first = NB;
+        first = NB - first;
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+        for (int j = 0; j < 2; ++j) {
+            const int at = (first + j) % NB;
+            load_stage<Sh, KTAIL>(g, j, at == 0 ? b0 : at == 1 ? b1 : b2, wave);
+        }
+    };
+    start();
+    w8a8::vm_barrier<Sh::kLoads>();  // the first stage has landed everywhere
+    while (true) {
+        v16f acc[TM][TN];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = v16f{};
-
-    const int frag_row = lane & 31, half = lane >> 5;
-    if (tile.e < grp.E) {
-        Loads<BM, BN> g;
-        {
-            const int lrow = 8 * wave + lane / kChunks;
-            g.kc = (lane % kChunks) ^ swz(lrow);
-            g.half_k = K / 2;
-            g.nk = KB;
-            const int rows = tile.m1 - tile.m0;
-            // without row_token the tile's own rows, else rows anywhere in xq
-            const int64_t row0 = grp.row_token ? 0 : tile.m0;
-            g.a = op.xq + row0 * (K / 2);
-            g.b = op.wq + ((int64_t)tile.e * N + n0) * (K / 2);
-            g.sa = op.xs + row0 * 8;
-            g.sb = op.ws + ((int64_t)tile.e * KB * N + n0) * 8;
-            g.sa_step = (int64_t)grp.T * 8;
-            g.sb_step = (int64_t)N * 8;
-            auto a_row = [&](int r) -> uint32_t {
-                r = min(r, rows - 1);
-                return grp.row_token ? (uint32_t)source_row(grp, tile.m0 + r) : (uint32_t)r;
-            };
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int l = 0; l < Sh::kA; ++l) g.aoff[l] = a_row(lrow + 32 * l) * (uint32_t)(K / 2) + g.kc * 16;
-#pragma unroll
-            for (int l = 0; l < Sh::kB; ++l)
-                g.boff[l] = (uint32_t)min(lrow + 32 * l, N - n0 - 1) * (uint32_t)(K / 2) + g.kc * 16;
-#pragma unroll
-            for (int q = 0; q < Sh::kScale; ++q) {
-                const int f = wave + kWaves * q;  // 32-row fragment, activations first
-                const uint32_t r = q < BM / 32 / kWaves ? a_row(32 * f + frag_row)
-                                                       : (uint32_t)min(32 * (f - BM / 32) + frag_row, N - n0 - 1);
-                g.soff[q] = r * 8 + 4 * half;
+            for (int j = 0; j < TN; ++j) acc[i][j] = v16f{};
+        if (tile.e < 0 || tile.e >= grp.E) {
+        } else if (tile.m0 + wm * WM >= tile.m1) {
+            // no rows for this wavefront: its share of the loads, and the barriers
+            for (int s = 0; s < g.nk; ++s) {
+                const int at = (first + s + 2) % NB;
+                uint4 *wr = at == 0 ? b0 : at == 1 ? b1 : b2;
+                if constexpr (NB == 3) load_stage<Sh, KTAIL>(g, s + 2, wr, wave);
+                vm_barrier<NB == 3 ? Sh::kLoads : 0>();
+                if constexpr (NB == 2) load_stage<Sh, KTAIL>(g, s + 2, wr, wave);
             }
-        }
-        const int a_frag = (wm * WM + frag_row) * kChunks;
-        const int b_frag = BM * kChunks + (wn * WN + frag_row) * kChunks;
-        const int a_scale = wm * (WM / 32) * 64 + lane, b_scale = (BM / 32 + wn * (WN / 32)) * 64 + lane;
-        const int fswz = swz(frag_row);
-        Frags<TM, TN> f;
-
-        uint4 *rd = lds, *nx = lds + Sh::kStage, *wr = lds + (STAGES - 1) * Sh::kStage;
-#pragma unroll
-        for (int l = 0; l < Sh::kLoads; ++l) load_one<BM, BN, KTAIL>(g, l, 0, rd, wave);
-        if (STAGES == 3 && g.nk > 1) {
-#pragma unroll
-            for (int l = 0; l < Sh::kLoads; ++l) load_one<BM, BN, KTAIL>(g, l, 1, nx, wave);
-            vm_barrier<Sh::kLoads>();
         } else {
-            vm_barrier<0>();
-        }
-        {
-            const int ch = (4 * half) ^ fswz;
-            const uint32_t *sc = reinterpret_cast<const uint32_t *>(rd + Sh::kCodes);
+            Frags<TM, TN> f;
+            const int ch = (Sh::kSteps * half) ^ fswz;
+            const uint4 *b = first == 0 ? b0 : first == 1 ? b1 : b2;
+            const uint32_t *sc = reinterpret_cast<const uint32_t *>(b + Sh::kCodes);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
-                f.x[0][i] = __builtin_bit_cast(v4i, rd[a_frag + i * 32 * kChunks + ch]);
-                f.sx[i] = sc[a_scale + 64 * i];
+                f.x[0][i] = __builtin_bit_cast(v4i, b[a_frag + i * 32 * CH + ch]);
+                f.sx[i] = lane_scales<CH>(sc[a_scale + kSc * i], half);
             }
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                f.w[0][j] = __builtin_bit_cast(v4i, rd[b_frag + j * 32 * kChunks + ch]);
-                f.sw[j] = sc[b_scale + 64 * j];
+                f.w[0][j] = __builtin_bit_cast(v4i, b[b_frag + j * 32 * CH + ch]);
+                f.sw[j] = lane_scales<CH>(sc[b_scale + kSc * j], half);
             }
-        }
-#define MXFP4_STAGE(AHEAD, LAST, J)                                                               \
-    stage<BM, BN, STAGES, KTAIL, AHEAD, LAST>(g, rd, wr, nx, J, wave, a_frag, b_frag, a_scale,    \
-                                              b_scale, half, fswz, acc, f)
-        for (int j = STAGES - 1; j < g.nk; ++j) {
-            MXFP4_STAGE(true, false, j);
-            uint4 *const done = rd;
-            rd = nx;
-            nx = STAGES == 3 ? wr : done;
-            wr = done;
-        }
-        if (STAGES == 3 && g.nk > 1) {
-            MXFP4_STAGE(false, false, 0);
-            rd = nx;
-        }
-        MXFP4_STAGE(false, true, 0);
+#define MXFP4_STAGE(RD, NX, WR, S)                                                                \
+    stage<Sh, NB, KTAIL>(g, RD, NX, WR, S, wave, a_frag, b_frag, a_scale, b_scale, half, fswz, acc, f)
+            int s = 0;
+            if constexpr (NB == 2) {
+                if (first == 1) { MXFP4_STAGE(b1, b0, b1, s); ++s; }
+                for (; s < g.nk; s += 2) {
+                    MXFP4_STAGE(b0, b1, b0, s);
+                    MXFP4_STAGE(b1, b0, b1, s + 1);
+                }
+            } else {
+                if (first == 1) { MXFP4_STAGE(b1, b2, b0, s); ++s; }
+                if (first != 0) { MXFP4_STAGE(b2, b0, b1, s); ++s; }
+                for (; s < g.nk; s += 3) {
+                    MXFP4_STAGE(b0, b1, b2, s);
+                    MXFP4_STAGE(b1, b2, b0, s + 1);
+                    MXFP4_STAGE(b2, b0, b1, s + 2);
+                }
+            }
 #undef MXFP4_STAGE
-        __syncthreads();  // all fragment reads done before the epilogue reuses LDS
-    }
-
-    const int mw0 = tile.m0 + wm * WM, nw0 = n0 + wn * WN;
-    if constexpr (EP == kSwiglu) {
+        }
+        const Tile done = tile;
+        const int mw0 = done.m0 + wm * WM, nw0 = n0 + wn * WN;
+        pid += gridDim.x;
+        const bool more = PERSIST && pid < tiles;
+        // all fragment reads done, and (empty) loads landed: the buffers are free
+        vm_barrier<0>();
+        if (more) {
+            tile = locate(pid, n0);
+            start();
+        }
+        if (done.e >= 0) {
+            if constexpr (EP == kSwiglu) {
+                Hidden h[TM][TN / 2];
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int j = 0; j < TN; j += 2) {
-                const int m = mw0 + i * 32 + frag_row;
-                store_swiglu(acc[i][j], acc[i][j + 1], o, m, m < tile.m1, nw0 + 32 * j, half, N, grp.S);
+                    for (int j = 0; j < TN; j += 2) h[i][j / 2] = quantize_swiglu(acc[i][j], acc[i][j + 1], half);
+                // the next tile's loads have landed before any store is under
+                // way, so that nothing later waits for the stores with them
+                wait_loads();
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; j += 2) {
+                        const int m = mw0 + i * 32 + frag_row;
+                        store_hidden(h[i][j / 2], o, m, m < done.m1, nw0 + 32 * j, half, N, grp.S);
+                    }
+            } else {
+                store_plain<EP, TM, TN>(acc, b0 + wave * kPieceSlots, o.out, mw0, done.m1, nw0, N, lane);
             }
-    } else {
-        constexpr int SIZE = EP == kOutF32 ? 4 : 2;
-        uint4 *mine = lds + wave * (32 * WN * SIZE / 16);
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-            store_rows<EP, WN, TN>(acc[i], mine, o.out, mw0 + i * 32, tile.m1, nw0, N, lane);
+        } else {
+            wait_loads();
+        }
+        if (!more) break;
+        w8a8::lds_barrier();  // every wavefront has waited for its loads
     }
 }
 
-template <int BM, int BN, int STAGES, Epilogue EP>
+template <int BM, int BN, int GM, int GN, int CH, int NB, int OCC, Epilogue EP>
 hipError_t launch_epilogue(const Operands &op, const Groups &g, int N, int K, const Output &o,
                            hipStream_t stream) {
     const int KB = (K + kStep - 1) / kStep;
     const int tiles_n = (N + BN - 1) / BN;
     const int64_t tiles_m = most_tiles(g.S, g.E, BM, g.offsets != nullptr);
-    const dim3 grid((unsigned)(tiles_m * tiles_n)), block(kThreads);
-    if (K % kStep == 0)
-        tiled_kernel<BM, BN, STAGES, false, EP><<<grid, block, 0, stream>>>(op, g, N, K, KB, (int)tiles_m, tiles_n, o);
+    const int64_t resident = EP == kSwiglu ? (int64_t)OCC * w8a8::device_cu_count() : tiles_m * tiles_n;
+    const dim3 grid((unsigned)std::min(tiles_m * tiles_n, resident)), block(GM * GN * kWave);
+    if (K % (32 * CH) == 0)
+        tiled_kernel<BM, BN, GM, GN, CH, NB, OCC, false, EP><<<grid, block, 0, stream>>>(op, g, N, K, KB, (int)tiles_m, tiles_n, o);
     else
-        tiled_kernel<BM, BN, STAGES, true, EP><<<grid, block, 0, stream>>>(op, g, N, K, KB, (int)tiles_m, tiles_n, o);
+        tiled_kernel<BM, BN, GM, GN, CH, NB, OCC, true, EP><<<grid, block, 0, stream>>>(op, g, N, K, KB, (int)tiles_m, tiles_n, o);
     return hipGetLastError();
 }
 
-template <int BM, int BN, int STAGES>
+template <int BM, int BN, int GM, int GN, int CH, int NB, int OCC>
 hipError_t launch_shape(const Operands &op, const Groups &g, int N, int K, int epilogue,
                         const Output &o, hipStream_t stream) {
     switch (epilogue) {
-        case kOutBf16: return launch_epilogue<BM, BN, STAGES, kOutBf16>(op, g, N, K, o, stream);
-        case kOutF16: return launch_epilogue<BM, BN, STAGES, kOutF16>(op, g, N, K, o, stream);
-        case kOutF32: return launch_epilogue<BM, BN, STAGES, kOutF32>(op, g, N, K, o, stream);
-        default: return launch_epilogue<BM, BN, STAGES, kSwiglu>(op, g, N, K, o, stream);
+        case kOutBf16: return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kOutBf16>(op, g, N, K, o, stream);
+        case kOutF16: return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kOutF16>(op, g, N, K, o, stream);
+        case kOutF32: return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kOutF32>(op, g, N, K, o, stream);
+        default:
+            // a wavefront's channels have to hold whole blocks of hidden units
+            if constexpr (BN / GN >= 64)
+                return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kSwiglu>(op, g, N, K, o, stream);
     }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -369,11 +507,22 @@ hipError_t launch_gemm_tiled(const uint8_t *xq, const uint8_t *xs, const uint8_t
                              const uint8_t *ws, const Groups &g, int N, int K, int epilogue,
                              const Output &o, hipStream_t stream) {
     const Operands op{xq, xs, wq, ws};
-    const int64_t t256 = most_tiles(g.S, g.E, 256, g.offsets != nullptr) * ((N + 255) / 256);
-    const int64_t t128 = most_tiles(g.S, g.E, 256, g.offsets != nullptr) * ((N + 127) / 128);
-    if (t256 >= 4 * 256) return launch_shape<256, 256, 2>(op, g, N, K, epilogue, o, stream);
-    if (t128 >= 256) return launch_shape<256, 128, 3>(op, g, N, K, epilogue, o, stream);
-    return launch_shape<128, 128, 3>(op, g, N, K, epilogue, o, stream);
+    // The smallest tile whose tiles all run at once (one workgroup per CU),
+    // else 256 x 256, whose operands' bytes per product are the fewest. Measured
+    // at N = K = 4096 (us; 64x64, 64x128, 128x128, 256x128, 256x256): M = 256
+    // 8.6, 10.0, 11.3, 14.3, 25.3; M = 384 10.9, 10.4, 11.5, 14.4, 25.2; M = 768
+    // 16.4, 14.6, 12.4, 15.3, 26.5; M = 1536 28.1, 23.4, 24.1, 17.5, 27.6; M = 4096
+    // 68.5, 54.4, 49.5, 47.5, 36.1.
+    const int64_t cus = w8a8::device_cu_count();
+    auto tiles = [&](int bm, int bn) {
+        return most_tiles(g.S, g.E, bm, g.offsets != nullptr) * ((N + bn - 1) / bn);
+    };
+    if (tiles(64, 64) <= cus && epilogue != kSwiglu)
+        return launch_shape<64, 64, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
+    if (tiles(64, 128) <= cus) return launch_shape<64, 128, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
+    if (tiles(128, 128) <= cus) return launch_shape<128, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
+    if (tiles(256, 128) <= cus) return launch_shape<256, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
+    return launch_shape<256, 256, 2, 4, 8, 2, 1>(op, g, N, K, epilogue, o, stream);
 }
 
 }  // namespace mxfp4
