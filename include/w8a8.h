@@ -361,11 +361,13 @@ w8a8_status mxfp4_gemm(const uint8_t *xq, const uint8_t *xs, int64_t M, const ui
  * The dynamically quantized layer: mxfp4_quantize_rows of x (type x_dtype,
  * row stride ldx), then mxfp4_gemm to out of out_dtype. The codes and scales
  * go through `workspace` (device, 16-byte aligned, at least
- * mxfp4_linear_workspace(M, K) bytes, free again once the call's work on the
- * stream is done).
+ * mxfp4_linear_workspace(M, N, K) bytes, free again once the call's work on the
+ * stream is done). Up to 4 rows of a weight of up to 8192 channels take one
+ * launch that quantizes inside the product and need no workspace (0 bytes, may
+ * be NULL).
  * Errors: as the two calls; SHAPE when workspace_bytes is too small.
  */
-int64_t mxfp4_linear_workspace(int64_t M, int64_t K);
+int64_t mxfp4_linear_workspace(int64_t M, int64_t N, int64_t K);
 w8a8_status mxfp4_linear(const void *x, int64_t ldx, mxfp4_dtype x_dtype, int64_t M,
                          const uint8_t *wq, const uint8_t *ws, int64_t N, int64_t K,
                          mxfp4_dtype out_dtype, void *out, void *workspace,

@@ -86,7 +86,7 @@ def load():
                "mxfp4_expert_gemm", "mxfp4_expert_swiglu", "mxfp4_moe", "moe_sort", "moe_gather",
                "moe_gather_backward", "moe_combine", "moe_combine_backward"):
         getattr(lib, fn).restype = i32
-    lib.mxfp4_linear_workspace.argtypes = [i64, i64]
+    lib.mxfp4_linear_workspace.argtypes = [i64, i64, i64]
     lib.moe_sort_workspace.argtypes = [i64, i64]
     lib.mxfp4_moe_workspace.argtypes = [i64, i64, i64, i64, i64, i32]
     for fn in ("mxfp4_linear_workspace", "moe_sort_workspace", "mxfp4_moe_workspace"):
@@ -412,50 +412,77 @@ def _float_dtype(dtype, name="dtype") -> int:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}") from None
 
 
+# The entry points below are called once per layer and token while decoding, where the time of a
+# call is the host's: a tensor that is as it should be passes one condition, the others go through
+# _check_tensor for their message.
+
 def _float_rows(t, name):
-    """(dtype code, row stride) of a 2-dim tensor of rows: its rows may lie apart."""
+    """(dtype code, row stride, rows, width) of a 2-dim tensor of rows: its rows may lie apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    code = _float_dtype(t.dtype, name)
+    code = _MXFP4_DTYPES.get(t.dtype)
+    if code is None:
+        code = _float_dtype(t.dtype, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     rows, width = t.shape
+    if t.is_contiguous():
+        return code, width, rows, width
     if width > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return code, t.stride(0) if rows > 1 else width
+    return code, t.stride(0) if rows > 1 else width, rows, width
 
 
-def _result(t, name, shape, dtype, device):
-    """`t` checked, or a new tensor."""
+def _check(t, name, dtype, ndim):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda
+            and t.is_contiguous()):
+        _check_tensor(t, name, dtype, ndim)
+
+
+def _result(t, name, shape, dtype, like):
+    """`t` checked, or a new tensor on `like`'s device."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check_tensor(t, name, dtype, len(shape))
+        return like.new_empty(shape, dtype=dtype)
+    _check(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
 
-def _scratch(workspace, need, device, stream):
+def _scratch(workspace, need, like, stream):
     """(address, bytes) of a workspace of `need` bytes: the caller's, or a new one that the caching
     allocator keeps until `stream` has run what is queued on it."""
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+        workspace = like.new_empty((need,), dtype=torch.uint8)
         if stream is not None:
             workspace.record_stream(stream)
-    _check_tensor(workspace, "workspace", torch.uint8, 1)
+        return workspace.data_ptr(), need
+    _check(workspace, "workspace", torch.uint8, 1)
     return workspace.data_ptr(), workspace.shape[0]
+
+
+def _stream_of(t, stream) -> int:
+    """The handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _done(st, fn):
+    if st != W8A8_OK:
+        raise W8A8Error(st, fn)
 
 
 def _check_mx(codes, scales, names=("codes", "scales"), lead=()):
     """(rows, K) of MXFP4 rows: codes [*lead, rows, K/2], scales [*lead, ceil(K/256), rows, 8]."""
     n = len(lead)
-    _check_tensor(codes, names[0], torch.uint8, 2 + n)
-    _check_tensor(scales, names[1], torch.uint8, 3 + n)
-    rows, K = codes.shape[n], 2 * codes.shape[n + 1]
-    if (tuple(codes.shape[:n]) != lead
-            or tuple(scales.shape) != lead + ((K + 255) // 256, rows, 8)):
+    _check(codes, names[0], torch.uint8, 2 + n)
+    _check(scales, names[1], torch.uint8, 3 + n)
+    shape = codes.shape
+    rows, K = shape[n], 2 * shape[n + 1]
+    if shape[:n] != lead or scales.shape != lead + ((K + 255) // 256, rows, 8):
         raise ValueError(f"{names[1]} must have shape {lead + ((K + 255) // 256, rows, 8)} for "
                          f"{names[0]} {tuple(codes.shape)}, got {tuple(scales.shape)}")
     return rows, K
@@ -464,12 +491,11 @@ def _check_mx(codes, scales, names=("codes", "scales"), lead=()):
 def mxfp4_quantize_rows(x, codes=None, scales=None, stream=None):
     """x [M,K] (bfloat16, float16 or float32; rows may lie apart) -> MXFP4: codes uint8 [M,K/2]
     and scales uint8 [ceil(K/256),M,8], the storage of include/w8a8.h."""
-    dt, ld = _float_rows(x, "x")
-    M, K = x.shape
-    codes = _result(codes, "codes", (M, K // 2), torch.uint8, x.device)
-    scales = _result(scales, "scales", ((K + 255) // 256, M, 8), torch.uint8, x.device)
-    _call("mxfp4_quantize_rows", x.data_ptr(), ld, M, K, dt, codes.data_ptr(), scales.data_ptr(),
-          _stream_handle(stream))
+    dt, ld, M, K = _float_rows(x, "x")
+    codes = _result(codes, "codes", (M, K // 2), torch.uint8, x)
+    scales = _result(scales, "scales", ((K + 255) // 256, M, 8), torch.uint8, x)
+    _done(load().mxfp4_quantize_rows(x.data_ptr(), ld, M, K, dt, codes.data_ptr(), scales.data_ptr(),
+                                     _stream_of(x, stream)), "mxfp4_quantize_rows")
     return codes, scales
 
 
@@ -477,9 +503,9 @@ def mxfp4_dequantize_rows(codes, scales, dtype=torch.bfloat16, out=None, stream=
     """The values [M,K] that MXFP4 rows stand for, in `dtype`."""
     M, K = _check_mx(codes, scales)
     dt = _float_dtype(dtype)
-    out = _result(out, "out", (M, K), dtype, codes.device)
-    _call("mxfp4_dequantize_rows", codes.data_ptr(), scales.data_ptr(), M, K, dt, out.data_ptr(),
-          _stream_handle(stream))
+    out = _result(out, "out", (M, K), dtype, codes)
+    _done(load().mxfp4_dequantize_rows(codes.data_ptr(), scales.data_ptr(), M, K, dt, out.data_ptr(),
+                                       _stream_of(codes, stream)), "mxfp4_dequantize_rows")
     return out
 
 
@@ -490,38 +516,48 @@ def mxfp4_gemm(xq, xs, wq, ws, out=None, out_dtype=torch.bfloat16, stream=None):
     if K2 != K:
         raise ValueError("operand shapes")
     dt = _float_dtype(out_dtype, "out_dtype")
-    out = _result(out, "out", (M, N), out_dtype, xq.device)
-    _call("mxfp4_gemm", xq.data_ptr(), xs.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K, dt,
-          out.data_ptr(), _stream_handle(stream))
+    out = _result(out, "out", (M, N), out_dtype, xq)
+    _done(load().mxfp4_gemm(xq.data_ptr(), xs.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K, dt,
+                            out.data_ptr(), _stream_of(xq, stream)), "mxfp4_gemm")
     return out
 
 
 def mxfp4_linear(x, wq, ws, out=None, out_dtype=None, workspace=None, stream=None):
     """out [M,N] = x [M,K], quantized to MXFP4 at run time, times the MXFP4 weight; out_dtype
-    defaults to x's. workspace: uint8 of at least mxfp4_linear_workspace(M, K) bytes (a new one
-    if None)."""
-    xd, ld = _float_rows(x, "x")
-    M, K = x.shape
+    defaults to x's. workspace: uint8 of at least mxfp4_linear_workspace(M, N, K) bytes (a new
+    one if None)."""
+    xd, ld, M, K = _float_rows(x, "x")
     N, K2 = _check_mx(wq, ws, ("wq", "ws"))
     if K2 != K:
         raise ValueError("operand shapes")
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    od = _float_dtype(out_dtype, "out_dtype")
-    out = _result(out, "out", (M, N), out_dtype, x.device)
-    address, size = _scratch(workspace, mxfp4_linear_workspace(M, K), x.device, stream)
-    _call("mxfp4_linear", x.data_ptr(), ld, xd, M, wq.data_ptr(), ws.data_ptr(), N, K, od,
-          out.data_ptr(), address, size, _stream_handle(stream))
+    if out_dtype is None:
+        out_dtype, od = x.dtype, xd
+    else:
+        od = _float_dtype(out_dtype, "out_dtype")
+    lib = load()
+    out = _result(out, "out", (M, N), out_dtype, x)
+    address = size = 0
+    need = lib.mxfp4_linear_workspace(M, N, K)
+    if need or workspace is not None:
+        address, size = _scratch(workspace, need, x, stream)
+    _done(lib.mxfp4_linear(x.data_ptr(), ld, xd, M, wq.data_ptr(), ws.data_ptr(), N, K, od,
+                           out.data_ptr(), address, size, _stream_of(x, stream)), "mxfp4_linear")
     return out
 
 
-def mxfp4_linear_workspace(M, K) -> int:
-    """Bytes of workspace that mxfp4_linear needs."""
-    return load().mxfp4_linear_workspace(M, K)
+def mxfp4_linear_workspace(M, N, K) -> int:
+    """Bytes of workspace that mxfp4_linear needs (0 for a few rows)."""
+    return load().mxfp4_linear_workspace(M, N, K)
 
 
-def _plan(t, name, ndim=1):
-    _check_tensor(t, name, torch.int32, ndim)
-    return t
+def _expert_ids(expert_ids):
+    """(T, top, bits) of expert ids."""
+    bits = {torch.int32: 32, torch.int64: 64}.get(getattr(expert_ids, "dtype", None))
+    if bits is None:
+        raise TypeError("expert_ids must be an int32 or int64 tensor")
+    _check(expert_ids, "expert_ids", expert_ids.dtype, 2)
+    T, top = expert_ids.shape
+    return T, top, bits
 
 
 def moe_sort(expert_ids, num_experts, offsets=None, slot_pos=None, row_token=None, workspace=None,
@@ -529,21 +565,18 @@ def moe_sort(expert_ids, num_experts, offsets=None, slot_pos=None, row_token=Non
     """Routing plan of expert_ids [T,top] (int32 or int64; ids outside [0, num_experts) are slots
     without an expert): (offsets int32 [num_experts+1], slot_pos int32 [T,top], row_token int32
     [T*top]) -- include/w8a8.h defines them. The order is stable."""
-    if not isinstance(expert_ids, torch.Tensor) or expert_ids.dtype not in (torch.int32, torch.int64):
-        raise TypeError("expert_ids must be an int32 or int64 tensor")
-    _check_tensor(expert_ids, "expert_ids", expert_ids.dtype, 2)
-    T, top = expert_ids.shape
-    dev = expert_ids.device
-    offsets = _result(offsets, "offsets", (max(num_experts, 0) + 1,), torch.int32, dev)
-    slot_pos = _result(slot_pos, "slot_pos", (T, top), torch.int32, dev)
-    row_token = _result(row_token, "row_token", (T * top,), torch.int32, dev)
-    need = moe_sort_workspace(T * top, num_experts)
+    T, top, bits = _expert_ids(expert_ids)
+    offsets = _result(offsets, "offsets", (max(num_experts, 0) + 1,), torch.int32, expert_ids)
+    slot_pos = _result(slot_pos, "slot_pos", (T, top), torch.int32, expert_ids)
+    row_token = _result(row_token, "row_token", (T * top,), torch.int32, expert_ids)
+    lib = load()
+    need = lib.moe_sort_workspace(T * top, num_experts)
     address, size = 0, 0
     if need or workspace is not None:
-        address, size = _scratch(workspace, need, dev, stream)
-    _call("moe_sort", expert_ids.data_ptr(), 8 * expert_ids.element_size(), T, top, num_experts,
-          offsets.data_ptr(), slot_pos.data_ptr(), row_token.data_ptr(), address, size,
-          _stream_handle(stream))
+        address, size = _scratch(workspace, need, expert_ids, stream)
+    _done(lib.moe_sort(expert_ids.data_ptr(), bits, T, top, num_experts, offsets.data_ptr(),
+                       slot_pos.data_ptr(), row_token.data_ptr(), address, size,
+                       _stream_of(expert_ids, stream)), "moe_sort")
     return offsets, slot_pos, row_token
 
 
@@ -554,43 +587,43 @@ def moe_sort_workspace(slots, num_experts) -> int:
 
 def moe_gather(x, slot_pos, out=None, stream=None):
     """Tokens x [T,H] -> rows [T*top,H] in expert order (0 for slots without an expert)."""
-    dt, ld = _float_rows(x, "x")
-    _plan(slot_pos, "slot_pos", 2)
-    T, H = x.shape
+    dt, ld, T, H = _float_rows(x, "x")
+    _check(slot_pos, "slot_pos", torch.int32, 2)
     top = slot_pos.shape[1]
     if slot_pos.shape[0] != T:
         raise ValueError("slot_pos must have a row per token")
-    out = _result(out, "out", (T * top, H), x.dtype, x.device)
-    _call("moe_gather", x.data_ptr(), ld, slot_pos.data_ptr(), T, top, H, dt, out.data_ptr(),
-          _stream_handle(stream))
+    out = _result(out, "out", (T * top, H), x.dtype, x)
+    _done(load().moe_gather(x.data_ptr(), ld, slot_pos.data_ptr(), T, top, H, dt, out.data_ptr(),
+                            _stream_of(x, stream)), "moe_gather")
     return out
 
 
 def _sorted_rows(rows, name, slot_pos):
     """(dtype code, T, top, H) of rows in expert order with their plan."""
-    code = _float_rows(rows, name)[0]
+    code, _, n, H = _float_rows(rows, name)
     if not rows.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    _plan(slot_pos, "slot_pos", 2)
+    _check(slot_pos, "slot_pos", torch.int32, 2)
     T, top = slot_pos.shape
-    if rows.shape[0] != T * top:
+    if n != T * top:
         raise ValueError(f"{name} must have a row per slot")
-    return code, T, top, rows.shape[1]
+    return code, T, top, H
 
 
 def moe_gather_backward(d_rows, slot_pos, out=None, stream=None):
     """Gradient of moe_gather: d_rows [T*top,H] -> d_x [T,H], the sum of each token's rows."""
     dt, T, top, H = _sorted_rows(d_rows, "d_rows", slot_pos)
-    out = _result(out, "out", (T, H), d_rows.dtype, d_rows.device)
-    _call("moe_gather_backward", d_rows.data_ptr(), slot_pos.data_ptr(), T, top, H, dt,
-          out.data_ptr(), _stream_handle(stream))
+    out = _result(out, "out", (T, H), d_rows.dtype, d_rows)
+    _done(load().moe_gather_backward(d_rows.data_ptr(), slot_pos.data_ptr(), T, top, H, dt,
+                                     out.data_ptr(), _stream_of(d_rows, stream)),
+          "moe_gather_backward")
     return out
 
 
 def _routing_weights(weights, T, top):
-    _check_tensor(weights, "weights", torch.float32, 2)
-    if tuple(weights.shape) != (T, top):
-        raise ValueError("weights must have the shape of slot_pos")
+    _check(weights, "weights", torch.float32, 2)
+    if weights.shape != (T, top):
+        raise ValueError("weights must have the shape of the routing")
 
 
 def moe_combine(rows, slot_pos, weights, out=None, stream=None):
@@ -598,9 +631,9 @@ def moe_combine(rows, slot_pos, weights, out=None, stream=None):
     weights [T,top] (float32) and summed."""
     dt, T, top, H = _sorted_rows(rows, "rows", slot_pos)
     _routing_weights(weights, T, top)
-    out = _result(out, "out", (T, H), rows.dtype, rows.device)
-    _call("moe_combine", rows.data_ptr(), slot_pos.data_ptr(), weights.data_ptr(), T, top, H, dt,
-          out.data_ptr(), _stream_handle(stream))
+    out = _result(out, "out", (T, H), rows.dtype, rows)
+    _done(load().moe_combine(rows.data_ptr(), slot_pos.data_ptr(), weights.data_ptr(), T, top, H, dt,
+                             out.data_ptr(), _stream_of(rows, stream)), "moe_combine")
     return out
 
 
@@ -608,14 +641,15 @@ def moe_combine_backward(d_out, rows, slot_pos, weights, d_rows=None, d_weights=
     """Gradients of moe_combine: d_out [T,H] -> (d_rows [T*top,H], d_weights float32 [T,top])."""
     dt, T, top, H = _sorted_rows(rows, "rows", slot_pos)
     _routing_weights(weights, T, top)
-    dd, ld = _float_rows(d_out, "d_out")
-    if dd != dt or tuple(d_out.shape) != (T, H):
+    dd, ld, n, width = _float_rows(d_out, "d_out")
+    if dd != dt or n != T or width != H:
         raise ValueError("d_out must have the dtype of rows and a row per token")
-    d_rows = _result(d_rows, "d_rows", (T * top, H), rows.dtype, rows.device)
-    d_weights = _result(d_weights, "d_weights", (T, top), torch.float32, rows.device)
-    _call("moe_combine_backward", d_out.data_ptr(), ld, rows.data_ptr(), slot_pos.data_ptr(),
-          weights.data_ptr(), T, top, H, dt, d_rows.data_ptr(), d_weights.data_ptr(),
-          _stream_handle(stream))
+    d_rows = _result(d_rows, "d_rows", (T * top, H), rows.dtype, rows)
+    d_weights = _result(d_weights, "d_weights", (T, top), torch.float32, rows)
+    _done(load().moe_combine_backward(d_out.data_ptr(), ld, rows.data_ptr(), slot_pos.data_ptr(),
+                                      weights.data_ptr(), T, top, H, dt, d_rows.data_ptr(),
+                                      d_weights.data_ptr(), _stream_of(rows, stream)),
+          "moe_combine_backward")
     return d_rows, d_weights
 
 
@@ -626,12 +660,13 @@ def _expert_operands(xq, xs, offsets, wq, ws, row_token):
         raise ValueError("wq must be a tensor [E, N, K/2]")
     E = wq.shape[0]
     N, K2 = _check_mx(wq, ws, ("wq", "ws"), (E,))
-    _plan(offsets, "offsets")
+    _check(offsets, "offsets", torch.int32, 1)
     if K2 != K or offsets.shape[0] != E + 1:
         raise ValueError("operand shapes")
-    if row_token is not None:
-        _plan(row_token, "row_token")
-    return T, T if row_token is None else row_token.shape[0], E, N, K
+    if row_token is None:
+        return T, T, E, N, K
+    _check(row_token, "row_token", torch.int32, 1)
+    return T, row_token.shape[0], E, N, K
 
 
 def mxfp4_expert_gemm(xq, xs, offsets, wq, ws, row_token=None, out=None, out_dtype=torch.bfloat16,
@@ -640,10 +675,11 @@ def mxfp4_expert_gemm(xq, xs, offsets, wq, ws, row_token=None, out=None, out_dty
     all MXFP4; rows past offsets[E] are 0. With row_token [S], row r is row row_token[r] of xq."""
     T, S, E, N, K = _expert_operands(xq, xs, offsets, wq, ws, row_token)
     dt = _float_dtype(out_dtype, "out_dtype")
-    out = _result(out, "out", (S, N), out_dtype, xq.device)
-    _call("mxfp4_expert_gemm", xq.data_ptr(), xs.data_ptr(), T,
-          None if row_token is None else row_token.data_ptr(), S, offsets.data_ptr(), E,
-          wq.data_ptr(), ws.data_ptr(), N, K, dt, out.data_ptr(), _stream_handle(stream))
+    out = _result(out, "out", (S, N), out_dtype, xq)
+    _done(load().mxfp4_expert_gemm(xq.data_ptr(), xs.data_ptr(), T,
+                                   None if row_token is None else row_token.data_ptr(), S,
+                                   offsets.data_ptr(), E, wq.data_ptr(), ws.data_ptr(), N, K, dt,
+                                   out.data_ptr(), _stream_of(xq, stream)), "mxfp4_expert_gemm")
     return out
 
 
@@ -654,11 +690,13 @@ def mxfp4_expert_swiglu(xq, xs, offsets, wq, ws, row_token=None, hq=None, hs=Non
     F = N // 2
     if N % 64:
         raise ValueError("wq must have 2F rows per expert, F a multiple of 32")
-    hq = _result(hq, "hq", (S, F // 2), torch.uint8, xq.device)
-    hs = _result(hs, "hs", ((F + 255) // 256, S, 8), torch.uint8, xq.device)
-    _call("mxfp4_expert_swiglu", xq.data_ptr(), xs.data_ptr(), T,
-          None if row_token is None else row_token.data_ptr(), S, offsets.data_ptr(), E,
-          wq.data_ptr(), ws.data_ptr(), F, K, hq.data_ptr(), hs.data_ptr(), _stream_handle(stream))
+    hq = _result(hq, "hq", (S, F // 2), torch.uint8, xq)
+    hs = _result(hs, "hs", ((F + 255) // 256, S, 8), torch.uint8, xq)
+    _done(load().mxfp4_expert_swiglu(xq.data_ptr(), xs.data_ptr(), T,
+                                     None if row_token is None else row_token.data_ptr(), S,
+                                     offsets.data_ptr(), E, wq.data_ptr(), ws.data_ptr(), F, K,
+                                     hq.data_ptr(), hs.data_ptr(), _stream_of(xq, stream)),
+          "mxfp4_expert_swiglu")
     return hq, hs
 
 
@@ -667,27 +705,22 @@ def mxfp4_moe(x, expert_ids, weights, w13q, w13s, w2q, w2s, out=None, workspace=
     through the experts' gate/up weights w13 [E,2F,H] with SwiGLU and down weights w2 [E,H,F]
     (both MXFP4), and summed with the router's weights [T,top] (float32) -> out [T,H] of x's
     dtype. workspace: uint8 of at least mxfp4_moe_workspace(...) bytes (a new one if None)."""
-    dt, ld = _float_rows(x, "x")
-    T, H = x.shape
-    if not isinstance(expert_ids, torch.Tensor) or expert_ids.dtype not in (torch.int32, torch.int64):
-        raise TypeError("expert_ids must be an int32 or int64 tensor")
-    _check_tensor(expert_ids, "expert_ids", expert_ids.dtype, 2)
-    top = expert_ids.shape[1]
+    dt, ld, T, H = _float_rows(x, "x")
+    T2, top, bits = _expert_ids(expert_ids)
     _routing_weights(weights, T, top)
     if not isinstance(w13q, torch.Tensor) or w13q.dim() != 3:
         raise ValueError("w13q must be a tensor [E, 2F, H/2]")
     E = w13q.shape[0]
     N, K = _check_mx(w13q, w13s, ("w13q", "w13s"), (E,))
     N2, F = _check_mx(w2q, w2s, ("w2q", "w2s"), (E,))
-    if expert_ids.shape[0] != T or K != H or N2 != H or N != 2 * F:
+    if T2 != T or K != H or N2 != H or N != 2 * F:
         raise ValueError("operand shapes")
-    out = _result(out, "out", (T, H), x.dtype, x.device)
-    need = load().mxfp4_moe_workspace(T, top, E, H, F, dt)
-    address, size = _scratch(workspace, need, x.device, stream)
-    _call("mxfp4_moe", x.data_ptr(), ld, dt, T, H, expert_ids.data_ptr(),
-          8 * expert_ids.element_size(), weights.data_ptr(), top, E, w13q.data_ptr(),
-          w13s.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), F, out.data_ptr(), address, size,
-          _stream_handle(stream))
+    lib = load()
+    out = _result(out, "out", (T, H), x.dtype, x)
+    address, size = _scratch(workspace, lib.mxfp4_moe_workspace(T, top, E, H, F, dt), x, stream)
+    _done(lib.mxfp4_moe(x.data_ptr(), ld, dt, T, H, expert_ids.data_ptr(), bits, weights.data_ptr(),
+                        top, E, w13q.data_ptr(), w13s.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), F,
+                        out.data_ptr(), address, size, _stream_of(x, stream)), "mxfp4_moe")
     return out
 
 

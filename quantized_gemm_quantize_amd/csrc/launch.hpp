@@ -77,6 +77,17 @@ hipError_t launch_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, 
                        const Groups &g, int N, int K, int epilogue, const Output &o,
                        hipStream_t stream);
 
+// The single-launch layer for a few rows: x is quantized inside the
+// weight-streaming product, by every workgroup for itself. Taken for up to 4
+// rows and 8192 channels. A call then costs the host one launch instead of two
+// (8.3 against 12.6 us) and the GPU no more: 4096 x 4096, M = 1 5.8 us against 6.0
+// in two launches, M = 4 6.1 / 6.2, but M = 8 7.7 / 6.3; M = 1 with 16384 channels
+// 18.5 / 11.1.
+inline bool single_launch_linear(int64_t M, int64_t N) { return M <= 4 && N <= 8192; }
+hipError_t launch_linear_decode(const void *x, int64_t ldx, int x_dtype, int M, const uint8_t *wq,
+                                const uint8_t *ws, int N, int K, int out_dtype, void *out,
+                                hipStream_t stream);
+
 }  // namespace mxfp4
 
 namespace moe {
@@ -85,6 +96,11 @@ namespace moe {
 int64_t sort_workspace(int64_t S, int64_t E);
 hipError_t launch_sort(const void *ids, bool ids64, int64_t S, int top, int E, int32_t *offsets,
                        int32_t *slot_pos, int32_t *row_token, void *workspace, hipStream_t stream);
+// The sort with the quantization of the T tokens x [T,H] in the same launch.
+hipError_t launch_sort_quantize(const void *ids, bool ids64, int64_t S, int top, int E,
+                                int32_t *offsets, int32_t *slot_pos, int32_t *row_token,
+                                void *workspace, const void *x, int64_t ldx, int64_t T, int H,
+                                int dtype, uint8_t *codes, uint8_t *scales, hipStream_t stream);
 hipError_t launch_gather(const void *x, int64_t ldx, const int32_t *slot_pos, int64_t T, int top,
                          int H, int dtype, void *rows, hipStream_t stream);
 // weights null: the plain sum (the gather's gradient)

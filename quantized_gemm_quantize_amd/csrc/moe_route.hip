@@ -16,7 +16,7 @@
 #include <type_traits>
 
 #include "launch.hpp"
-#include "mxfp4.hpp"
+#include "mxfp4_rows.hpp"
 
 namespace moe {
 namespace {
@@ -52,10 +52,27 @@ __device__ __forceinline__ uint64_t same_bin(int bin, int bits) {
     return m;
 }
 
+// Rows that are quantized to MXFP4 by the workgroups after the sort's own, in
+// the same launch (codes null: none).
+struct Rows {
+    const char *x;
+    int64_t ldx, M;
+    int K, KB;
+    uint8_t *codes, *scales;
+};
+
+template <int QD>
+__device__ __forceinline__ void quantize_beside(int64_t block, const Rows &q) {
+    if constexpr (QD >= 0)
+        mxfp4::quantize_steps<(Dtype)QD, 1, kSortThreads>(block, q.x, q.ldx, q.M, q.K, q.KB, q.codes, q.scales);
+}
+
 // Each workgroup counts the bins of its kChunk slots.
-template <typename I>
+template <typename I, int QD>
 __global__ __launch_bounds__(kSortThreads) void count_kernel(const I *__restrict__ ids, int64_t S,
-                                                             int E, int32_t *__restrict__ counts) {
+                                                             int E, int32_t *__restrict__ counts,
+                                                             int chunks, Rows q) {
+    if (QD >= 0 && (int)blockIdx.x >= chunks) return quantize_beside<QD>(blockIdx.x - chunks, q);
     __shared__ int hist[kMaxBins + 3];
     w8a8::lds_poison(hist);
     w8a8::lds_poison_done();
@@ -77,11 +94,12 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(const I *__restrict
 // the bin's slots in earlier chunks (counts), in earlier wavefronts, and
 // before it in its own wavefront (lane order within a match mask): the stable
 // order. With one chunk the counts are this workgroup's own.
-template <typename I>
+template <typename I, int QD>
 __global__ __launch_bounds__(kSortThreads) void place_kernel(
     const I *__restrict__ ids, int64_t S, int top, int E, int bits,
     const int32_t *__restrict__ counts, int chunks, int32_t *__restrict__ offsets,
-    int32_t *__restrict__ slot_pos, int32_t *__restrict__ row_token) {
+    int32_t *__restrict__ slot_pos, int32_t *__restrict__ row_token, Rows q) {
+    if (QD >= 0 && (int)blockIdx.x >= chunks) return quantize_beside<QD>(blockIdx.x - chunks, q);
     extern __shared__ int hist[];  // [kSortWaves][E + 1] counts, then first rows
     __shared__ int wave_sum[kSortWaves];
     const int bins = E + 1;
@@ -155,46 +173,58 @@ __global__ __launch_bounds__(kSortThreads) void place_kernel(
 // ------------------------------------------------------------------ rows
 
 constexpr int kThreads = 256;
-
-// V elements of a row as floats. V > 1: one 16-byte access.
-template <Dtype D, int V>
-__device__ __forceinline__ void load_row(const char *p, float (&f)[V]) {
-    if constexpr (V == 1) {
-        if constexpr (D == kF32) f[0] = *reinterpret_cast<const float *>(p);
-        else if constexpr (D == kBf16) f[0] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(p) << 16);
-        else f[0] = (float)*reinterpret_cast<const _Float16 *>(p);
-    } else {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (D == kF32) f[i] = __uint_as_float(w[i]);
-            else if constexpr (D == kBf16) { f[2 * i] = w8a8::bf16_lo(w[i]); f[2 * i + 1] = w8a8::bf16_hi(w[i]); }
-            else { const mxfp4::v2h h = __builtin_bit_cast(mxfp4::v2h, w[i]); f[2 * i] = (float)h[0]; f[2 * i + 1] = (float)h[1]; }
-        }
-    }
-}
-
-template <Dtype D, int V>
-__device__ __forceinline__ void store_row(char *p, const float (&f)[V]) {
-    if constexpr (V == 1) {
-        if constexpr (D == kF32) *reinterpret_cast<float *>(p) = f[0];
-        else if constexpr (D == kBf16) *reinterpret_cast<__bf16 *>(p) = (__bf16)f[0];
-        else *reinterpret_cast<_Float16 *>(p) = (_Float16)f[0];
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (D == kF32) w[i] = __float_as_uint(f[i]);
-            else if constexpr (D == kBf16) w[i] = w8a8::pack_bf16x2(f[2 * i], f[2 * i + 1]);
-            else w[i] = __builtin_bit_cast(uint32_t, mxfp4::v2h{(_Float16)f[2 * i], (_Float16)f[2 * i + 1]});
-        }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
+constexpr int kSlots = 4;  // slots of a token whose rows are in flight together
 
 template <Dtype D>
 constexpr int size_of() { return D == kF32 ? 4 : 2; }
+
+// V elements of a row, as loaded: 16 bytes (V * size = 16), 4 bytes, or one
+// element. Everything here is read once and written once: streaming accesses.
+template <Dtype D, int V>
+struct Vec {
+    static constexpr int kBytes = V * size_of<D>();
+    static_assert(kBytes == 16 || kBytes == 4 || V == 1, "one access");
+    static constexpr int kWords = kBytes >= 4 ? kBytes / 4 : 1;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const char *p) {
+        if constexpr (kBytes == 16) {
+            const uint4 u = w8a8::load16_stream(p);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else if constexpr (kBytes == 4) {
+            w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(p));
+        } else {
+            w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t *>(p));
+        }
+    }
+    __device__ __forceinline__ void store(char *p) const {
+        if constexpr (kBytes == 16) w8a8::store16_nt(p, make_uint4(w[0], w[1], w[2], w[3]));
+        else if constexpr (kBytes == 4) __builtin_nontemporal_store(w[0], reinterpret_cast<uint32_t *>(p));
+        else __builtin_nontemporal_store((uint16_t)w[0], reinterpret_cast<uint16_t *>(p));
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (D == kF32) return __uint_as_float(w[i]);
+        else if constexpr (D == kBf16) return i & 1 ? w8a8::bf16_hi(w[i / 2]) : w8a8::bf16_lo(w[i / 2]);
+        else return (float)__builtin_bit_cast(mxfp4::v2h, w[i / 2])[i & 1];
+    }
+    __device__ __forceinline__ void set(const float (&f)[V]) {
+        if constexpr (D == kF32) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] = __float_as_uint(f[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) {
+                const float lo = f[2 * i], hi = 2 * i + 1 < V ? f[2 * i + 1] : 0.0f;
+                if constexpr (D == kBf16) w[i] = w8a8::pack_bf16x2(lo, hi);
+                else w[i] = __builtin_bit_cast(uint32_t, mxfp4::v2h{(_Float16)lo, (_Float16)hi});
+            }
+        }
+    }
+};
 
 // Row of slot_pos value p, kept or dropped; -1 when a malformed plan points
 // outside the S rows.
@@ -203,125 +233,213 @@ __device__ __forceinline__ int64_t row_of(int p, int64_t S) {
     return r < S ? r : -1;
 }
 
-// One workgroup: a token, kThreads * V of its elements. Each element is read
-// once and written to all of the token's rows.
-template <Dtype D, int V>
+// One workgroup: a token, U pieces of kThreads * V of its elements. Each element
+// is read once and written to all of the token's rows.
+template <Dtype D, int V, int U>
 __global__ __launch_bounds__(kThreads) void gather_kernel(const char *__restrict__ x, int64_t ldx,
                                                           const int32_t *__restrict__ slot_pos,
                                                           int top, int64_t S, int H,
                                                           char *__restrict__ rows) {
     const int64_t t = blockIdx.x;
-    const int h = (blockIdx.y * kThreads + threadIdx.x) * V;
-    if (h >= H) return;
-    float f[V], zero[V] = {};
-    load_row<D, V>(x + (t * ldx + h) * size_of<D>(), f);
+    const int h0 = (blockIdx.y * U * kThreads + threadIdx.x) * V;
+    Vec<D, V> v[U], zero;
+    zero.clear();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (h0 + u * kThreads * V < H) v[u].load(x + (t * ldx + h0 + u * kThreads * V) * size_of<D>());
     for (int j = 0; j < top; ++j) {
         const int p = slot_pos[t * top + j];
         const int64_t r = row_of(p, S);
         if (r < 0) continue;
-        store_row<D, V>(rows + (r * H + h) * size_of<D>(), p < 0 ? zero : f);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (h0 + u * kThreads * V < H)
+                (p < 0 ? zero : v[u]).store(rows + (r * H + h0 + u * kThreads * V) * size_of<D>());
     }
 }
 
-template <Dtype D, int V, bool WEIGHTS>
+// The token's rows, kSlots of them in flight together, summed in the order of
+// its slots.
+template <Dtype D, int V, int U, bool WEIGHTS>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const char *__restrict__ rows,
                                                            const int32_t *__restrict__ slot_pos,
                                                            const float *__restrict__ weights,
                                                            int top, int64_t S, int H,
                                                            char *__restrict__ out) {
     const int64_t t = blockIdx.x;
-    const int h = (blockIdx.y * kThreads + threadIdx.x) * V;
-    if (h >= H) return;
-    float sum[V] = {};
-    for (int j = 0; j < top; ++j) {
-        const int p = slot_pos[t * top + j];
-        if (p < 0 || p >= S) continue;
-        const float w = WEIGHTS ? weights[t * top + j] : 1.0f;
-        float f[V];
-        load_row<D, V>(rows + ((int64_t)p * H + h) * size_of<D>(), f);
+    const int h0 = (blockIdx.y * U * kThreads + threadIdx.x) * V;
+    float sum[U][V] = {};
+    for (int j0 = 0; j0 < top; j0 += kSlots) {
+        Vec<D, V> v[kSlots][U];
+        float w[kSlots];
+        bool kept[kSlots];
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] += WEIGHTS ? w * f[i] : f[i];
+        for (int j = 0; j < kSlots; ++j) {
+            const int64_t s = t * top + min(j0 + j, top - 1);
+            const int p = slot_pos[s];
+            w[j] = WEIGHTS ? weights[s] : 1.0f;
+            kept[j] = j0 + j < top && p >= 0 && p < S;
+            if (kept[j]) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (h0 + u * kThreads * V < H)
+                        v[j][u].load(rows + ((int64_t)p * H + h0 + u * kThreads * V) * size_of<D>());
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            if (!kept[j]) continue;  // uniform
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[u][i] += WEIGHTS ? w[j] * v[j][u].get(i) : v[j][u].get(i);
+        }
     }
-    store_row<D, V>(out + (t * H + h) * size_of<D>(), sum);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (h0 + u * kThreads * V < H) {
+            Vec<D, V> v;
+            v.set(sum[u]);
+            v.store(out + (t * H + h0 + u * kThreads * V) * size_of<D>());
+        }
 }
 
-// One workgroup per token: d_rows, and d_w summed over the row (each thread
-// its elements in order, then lanes, then wavefronts).
+// One workgroup per token: d_rows, and d_weights summed over the row (each
+// thread its elements in order, then lanes, then wavefronts). kSlots slots
+// together: d_out is read once for them, their sums are joined together.
 template <Dtype D, int V>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const char *__restrict__ d_out, int64_t ldd, const char *__restrict__ rows,
     const int32_t *__restrict__ slot_pos, const float *__restrict__ weights, int top, int64_t S,
     int H, char *__restrict__ d_rows, float *__restrict__ d_weights) {
-    __shared__ float part[kThreads / kWave];
+    constexpr int kWaves = kThreads / kWave;
+    __shared__ float part[kSlots][kWaves];
     w8a8::lds_poison(part);
     w8a8::lds_poison_done();
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    for (int j = 0; j < top; ++j) {
-        const int p = slot_pos[t * top + j];
-        const int64_t r = row_of(p, S);
-        const bool kept = p >= 0 && r >= 0;
-        const float w = kept ? weights[t * top + j] : 0.0f;
-        float dot = 0.0f;
-        for (int h = threadIdx.x * V; h < H; h += kThreads * V) {
-            float d[V], g[V] = {};
-            if (kept) {
-                float y[V];
-                load_row<D, V>(d_out + (t * ldd + h) * size_of<D>(), d);
-                load_row<D, V>(rows + (r * H + h) * size_of<D>(), y);
+    for (int j0 = 0; j0 < top; j0 += kSlots) {
+        int64_t row[kSlots];
+        bool kept[kSlots];
+        float w[kSlots], dot[kSlots];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    g[i] = w * d[i];
-                    dot += d[i] * y[i];
+        for (int j = 0; j < kSlots; ++j) {
+            const int64_t s = t * top + min(j0 + j, top - 1);
+            const int p = slot_pos[s];
+            row[j] = j0 + j < top ? row_of(p, S) : -1;
+            kept[j] = p >= 0 && row[j] >= 0;
+            w[j] = weights[s];
+            dot[j] = 0.0f;
+        }
+        for (int h = threadIdx.x * V; h < H; h += kThreads * V) {
+            Vec<D, V> d, y[kSlots];
+            d.load(d_out + (t * ldd + h) * size_of<D>());
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j)
+                if (kept[j]) y[j].load(rows + (row[j] * H + h) * size_of<D>());
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                if (row[j] < 0) continue;  // uniform, as kept
+                float g[V] = {};
+                if (kept[j]) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        g[i] = w[j] * d.get(i);
+                        dot[j] += d.get(i) * y[j].get(i);
+                    }
                 }
+                Vec<D, V> v;
+                v.set(g);
+                v.store(d_rows + (row[j] * H + h) * size_of<D>());
             }
-            if (r >= 0) store_row<D, V>(d_rows + (r * H + h) * size_of<D>(), g);
         }
         if (d_weights) {
 #pragma unroll
-            for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off, kWave);
-            if (lane == 0) part[wave] = dot;
+            for (int j = 0; j < kSlots; ++j) {
+#pragma unroll
+                for (int off = 32; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off, kWave);
+                if (lane == 0) part[j][wave] = dot[j];
+            }
             __syncthreads();
-            if (threadIdx.x == 0) d_weights[t * top + j] = kept ? part[0] + part[1] + part[2] + part[3] : 0.0f;
+            if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < top) {
+                const int j = threadIdx.x;
+                bool k = false;
+#pragma unroll
+                for (int q = 0; q < kSlots; ++q)
+                    if (q == j) k = kept[q];
+                float sum = 0.0f;
+#pragma unroll
+                for (int q = 0; q < kWaves; ++q) sum += part[j][q];
+                d_weights[t * top + j0 + j] = k ? sum : 0.0f;
+            }
             __syncthreads();
         }
     }
 }
 
-// 16-byte accesses when every row starts 16-byte aligned.
-bool wide(const void *a, const void *b, const void *c, int64_t ld, int64_t H, int dtype) {
+// Bytes per access: 16 or 4 when every row starts aligned to that, else one
+// element.
+int access(const void *a, const void *b, const void *c, int64_t ld, int64_t H, int dtype) {
     const int64_t size = dtype == kF32 ? 4 : 2;
-    const uintptr_t p = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
-                        reinterpret_cast<uintptr_t>(c);
-    return (p & 15) == 0 && H * size % 16 == 0 && ld * size % 16 == 0;
+    const uint64_t p = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+                       reinterpret_cast<uintptr_t>(c) | (uint64_t)(H * size) | (uint64_t)(ld * size);
+    return p % 16 == 0 ? 16 : p % 4 == 0 ? 4 : 2;
 }
-
-int segments(int H, int per_thread) { return (H + kThreads * per_thread - 1) / (kThreads * per_thread); }
 
 // f(Dtype constant, elements per access)
 template <typename F>
-void by_type(int dtype, bool w, F f) {
+void by_type(int dtype, int bytes, F f) {
     using std::integral_constant;
-    switch (dtype) {
-        case kBf16: w ? f(integral_constant<Dtype, kBf16>{}, integral_constant<int, 8>{}) : f(integral_constant<Dtype, kBf16>{}, integral_constant<int, 1>{}); break;
-        case kF16: w ? f(integral_constant<Dtype, kF16>{}, integral_constant<int, 8>{}) : f(integral_constant<Dtype, kF16>{}, integral_constant<int, 1>{}); break;
-        default: w ? f(integral_constant<Dtype, kF32>{}, integral_constant<int, 4>{}) : f(integral_constant<Dtype, kF32>{}, integral_constant<int, 1>{});
+    if (dtype == kF32) {
+        const integral_constant<Dtype, kF32> d;
+        bytes == 16 ? f(d, integral_constant<int, 4>{}) : f(d, integral_constant<int, 1>{});
+    } else if (dtype == kBf16) {
+        const integral_constant<Dtype, kBf16> d;
+        bytes == 16 ? f(d, integral_constant<int, 8>{})
+                    : bytes == 4 ? f(d, integral_constant<int, 2>{}) : f(d, integral_constant<int, 1>{});
+    } else {
+        const integral_constant<Dtype, kF16> d;
+        bytes == 16 ? f(d, integral_constant<int, 8>{})
+                    : bytes == 4 ? f(d, integral_constant<int, 2>{}) : f(d, integral_constant<int, 1>{});
     }
 }
 
-template <typename I>
+// Elements per thread: one 16-byte access, or four short ones (fewer bytes in
+// flight per thread would not fill the memory's latency).
+template <typename V>
+constexpr int unroll() { return V::value * 2 >= 8 ? 1 : 4; }
+
+int segments(int H, int per_thread) { return (H + kThreads * per_thread - 1) / (kThreads * per_thread); }
+
+template <typename I, int QD>
 hipError_t sort_ids(const I *ids, int64_t S, int top, int E, int32_t *offsets, int32_t *slot_pos,
-                    int32_t *row_token, int32_t *counts, hipStream_t stream) {
+                    int32_t *row_token, int32_t *counts, const Rows &q, hipStream_t stream) {
     const int chunks = S > 0 ? (int)((S + kChunk - 1) / kChunk) : 1;  // none: offsets only
     int bits = 0;
     while ((1 << bits) <= E) ++bits;
+    const int steps_per_block = kSortThreads / 32;
+    const int beside = QD >= 0 ? (int)((q.M * q.KB + steps_per_block - 1) / steps_per_block) : 0;
+    const size_t lds = kSortWaves * (E + 1) * sizeof(int);
     if (chunks > 1) {
-        count_kernel<I><<<chunks, kSortThreads, 0, stream>>>(ids, S, E, counts);
+        count_kernel<I, QD><<<chunks + beside, kSortThreads, 0, stream>>>(ids, S, E, counts, chunks, q);
         if (hipError_t e = hipGetLastError()) return e;
+        place_kernel<I, -1><<<chunks, kSortThreads, lds, stream>>>(ids, S, top, E, bits, counts, chunks, offsets,
+                                                                   slot_pos, row_token, q);
+    } else {
+        place_kernel<I, QD><<<chunks + beside, kSortThreads, lds, stream>>>(ids, S, top, E, bits, counts, chunks,
+                                                                            offsets, slot_pos, row_token, q);
     }
-    place_kernel<I><<<chunks, kSortThreads, kSortWaves * (E + 1) * sizeof(int), stream>>>(
-        ids, S, top, E, bits, counts, chunks, offsets, slot_pos, row_token);
     return hipGetLastError();
+}
+
+template <int QD>
+hipError_t sort_any(const void *ids, bool ids64, int64_t S, int top, int E, int32_t *offsets,
+                    int32_t *slot_pos, int32_t *row_token, void *workspace, const Rows &q,
+                    hipStream_t stream) {
+    int32_t *counts = static_cast<int32_t *>(workspace);
+    if (ids64)
+        return sort_ids<int64_t, QD>(static_cast<const int64_t *>(ids), S, top, E, offsets, slot_pos, row_token, counts, q, stream);
+    return sort_ids<int32_t, QD>(static_cast<const int32_t *>(ids), S, top, E, offsets, slot_pos, row_token, counts, q, stream);
 }
 
 }  // namespace
@@ -333,34 +451,42 @@ int64_t sort_workspace(int64_t S, int64_t E) {
 
 hipError_t launch_sort(const void *ids, bool ids64, int64_t S, int top, int E, int32_t *offsets,
                        int32_t *slot_pos, int32_t *row_token, void *workspace, hipStream_t stream) {
-    int32_t *counts = static_cast<int32_t *>(workspace);
-    if (ids64)
-        return sort_ids(static_cast<const int64_t *>(ids), S, top, E, offsets, slot_pos, row_token, counts, stream);
-    return sort_ids(static_cast<const int32_t *>(ids), S, top, E, offsets, slot_pos, row_token, counts, stream);
+    return sort_any<-1>(ids, ids64, S, top, E, offsets, slot_pos, row_token, workspace, Rows{}, stream);
+}
+
+hipError_t launch_sort_quantize(const void *ids, bool ids64, int64_t S, int top, int E,
+                                int32_t *offsets, int32_t *slot_pos, int32_t *row_token,
+                                void *workspace, const void *x, int64_t ldx, int64_t T, int H,
+                                int dtype, uint8_t *codes, uint8_t *scales, hipStream_t stream) {
+    const Rows q{static_cast<const char *>(x), ldx, T, H, (H + mxfp4::kStep - 1) / mxfp4::kStep, codes, scales};
+    switch (dtype) {
+        case kBf16: return sort_any<kBf16>(ids, ids64, S, top, E, offsets, slot_pos, row_token, workspace, q, stream);
+        case kF16: return sort_any<kF16>(ids, ids64, S, top, E, offsets, slot_pos, row_token, workspace, q, stream);
+        default: return sort_any<kF32>(ids, ids64, S, top, E, offsets, slot_pos, row_token, workspace, q, stream);
+    }
 }
 
 hipError_t launch_gather(const void *x, int64_t ldx, const int32_t *slot_pos, int64_t T, int top,
                          int H, int dtype, void *rows, hipStream_t stream) {
-    by_type(dtype, wide(x, rows, nullptr, ldx, H, dtype), [&](auto d, auto v) {
-        gather_kernel<decltype(d)::value, decltype(v)::value>
-            <<<dim3((unsigned)T, segments(H, v)), kThreads, 0, stream>>>(
-                static_cast<const char *>(x), ldx, slot_pos, top, T * top, H, static_cast<char *>(rows));
+    by_type(dtype, access(x, rows, nullptr, ldx, H, dtype), [&](auto d, auto v) {
+        constexpr int V = decltype(v)::value, U = unroll<decltype(v)>();
+        gather_kernel<decltype(d)::value, V, U><<<dim3((unsigned)T, segments(H, V * U)), kThreads, 0, stream>>>(
+            static_cast<const char *>(x), ldx, slot_pos, top, T * top, H, static_cast<char *>(rows));
     });
     return hipGetLastError();
 }
 
 hipError_t launch_combine(const void *rows, const int32_t *slot_pos, const float *weights,
                           int64_t T, int top, int H, int dtype, void *out, hipStream_t stream) {
-    by_type(dtype, wide(rows, out, nullptr, H, H, dtype), [&](auto d, auto v) {
-        const dim3 grid((unsigned)T, segments(H, v));
+    by_type(dtype, access(rows, out, nullptr, H, H, dtype), [&](auto d, auto v) {
+        constexpr int V = decltype(v)::value, U = unroll<decltype(v)>();
+        const dim3 grid((unsigned)T, segments(H, V * U));
         const char *r = static_cast<const char *>(rows);
         char *o = static_cast<char *>(out);
         if (weights)
-            combine_kernel<decltype(d)::value, decltype(v)::value, true>
-                <<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
+            combine_kernel<decltype(d)::value, V, U, true><<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
         else
-            combine_kernel<decltype(d)::value, decltype(v)::value, false>
-                <<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
+            combine_kernel<decltype(d)::value, V, U, false><<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
     });
     return hipGetLastError();
 }
@@ -369,11 +495,10 @@ hipError_t launch_combine_backward(const void *d_out, int64_t ldd, const void *r
                                    const int32_t *slot_pos, const float *weights, int64_t T,
                                    int top, int H, int dtype, void *d_rows, float *d_weights,
                                    hipStream_t stream) {
-    by_type(dtype, wide(d_out, rows, d_rows, ldd, H, dtype), [&](auto d, auto v) {
-        combine_backward_kernel<decltype(d)::value, decltype(v)::value>
-            <<<dim3((unsigned)T), kThreads, 0, stream>>>(
-                static_cast<const char *>(d_out), ldd, static_cast<const char *>(rows), slot_pos,
-                weights, top, T * top, H, static_cast<char *>(d_rows), d_weights);
+    by_type(dtype, access(d_out, rows, d_rows, ldd, H, dtype), [&](auto d, auto v) {
+        combine_backward_kernel<decltype(d)::value, decltype(v)::value><<<dim3((unsigned)T), kThreads, 0, stream>>>(
+            static_cast<const char *>(d_out), ldd, static_cast<const char *>(rows), slot_pos, weights,
+            top, T * top, H, static_cast<char *>(d_rows), d_weights);
     });
     return hipGetLastError();
 }

@@ -34,17 +34,86 @@ __device__ __forceinline__ v4f mfma_16x16x128(int sel, v4i a, uint32_t sa, v4i b
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, 1, (int)sa, 1, (int)sb);
 }
 
-// One pair in flight: its scales, and the LDS that its codes fill.
-template <int MT, int CT>
-struct Pair {
-    uint32_t sw[CT], sx[MT];
+// Activations that are quantized on the way (the single-launch layer): 64
+// consecutive elements of a row per lane and pair, its two blocks.
+constexpr int kCodes = -1;  // activations in MXFP4 already
+
+template <int XD>
+struct RawPair {
+    static constexpr int kLoads = XD == kCodes ? 0 : XD == kF32 ? 16 : 8;
+    uint4 u[kLoads > 0 ? kLoads : 1];
+
+    // block t of the two -> its scale code, its elements
+    __device__ __forceinline__ uint32_t quantize(int t, v4i &x) const {
+        uint32_t c[4] = {0, 0, 0, 0};
+        uint32_t code = 0;
+        if constexpr (XD == kF32) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 &v = u[8 * t + i];
+                top = max(top, max(max(v.x & 0x7FFFFFFFu, v.y & 0x7FFFFFFFu), max(v.z & 0x7FFFFFFFu, v.w & 0x7FFFFFFFu)));
+            }
+            code = scale_code(__uint_as_float(top));
+            const float s = scale_value(code);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float *f = reinterpret_cast<const float *>(&u[8 * t + 2 * i]);
+                c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[i], f[0], f[1], s, 0);
+                c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[i], f[2], f[3], s, 1);
+                const float *h = reinterpret_cast<const float *>(&u[8 * t + 2 * i + 1]);
+                c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[i], h[0], h[1], s, 2);
+                c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[i], h[2], h[3], s, 3);
+            }
+        } else if constexpr (XD != kCodes) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 &v = u[4 * t + i];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+            }
+            code = scale_code(XD == kBf16 ? __uint_as_float(top << 16)
+                                          : (float)__builtin_bit_cast(_Float16, (unsigned short)top));
+            const float s = scale_value(code);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 &v = u[4 * t + i];
+                if constexpr (XD == kBf16) {
+                    using w8a8::v2bf;
+                    c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c[i], __builtin_bit_cast(v2bf, v.x), s, 0);
+                    c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c[i], __builtin_bit_cast(v2bf, v.y), s, 1);
+                    c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c[i], __builtin_bit_cast(v2bf, v.z), s, 2);
+                    c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c[i], __builtin_bit_cast(v2bf, v.w), s, 3);
+                } else {
+                    c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c[i], __builtin_bit_cast(v2h, v.x), s, 0);
+                    c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c[i], __builtin_bit_cast(v2h, v.y), s, 1);
+                    c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c[i], __builtin_bit_cast(v2h, v.z), s, 2);
+                    c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c[i], __builtin_bit_cast(v2h, v.w), s, 3);
+                }
+            }
+        }
+        x = code == 255 ? v4i{} : v4i{(int)c[0], (int)c[1], (int)c[2], (int)c[3]};
+        return code;
+    }
 };
 
-template <int MT, int CT, int WAVES, Epilogue EP>
+// One pair in flight: its scales (and activations that have no codes yet).
+template <int MT, int CT, int XD>
+struct Pair {
+    uint32_t sw[CT], sx[MT];
+    RawPair<XD> raw;
+};
+
+template <int MT, int CT, int WAVES, int XD, Epilogue EP>
 __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
     const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xs, const uint8_t *__restrict__ wq,
-    const uint8_t *__restrict__ ws, Groups grp, int N, int K, int KB, int tiles_n, Output o) {
-    constexpr int kSlots = WAVES * (MT + CT) * 128;  // 16-byte slots of one pair, all wavefronts
+    const uint8_t *__restrict__ ws, Groups grp, int N, int K, int KB, int tiles_n, int64_t ldx, Output o) {
+    static_assert(XD == kCodes || MT == 1, "up to 16 rows are quantized on the way");
+    constexpr int XT = XD == kCodes ? MT : 0;        // 16-row tiles of codes in LDS
+    constexpr int kSlots = WAVES * (XT + CT) * 128;  // 16-byte slots of one pair, all wavefronts
     // one array per pair in flight: the compiler then waits for that pair only
     __shared__ uint4 q0[kSlots], q1[kSlots];
     static_assert(WAVES * MT * CT * kWave <= kSlots, "the partial sums fit a pair's place");
@@ -70,7 +139,7 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
         const int lr = lane >> 3, lc = lane & 7;
         int row[MT][2], srow[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int m = 0; m < XT; ++m) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) row[m][h] = source_row(grp, t.m0 + min(16 * m + 8 * h + lr, rows - 1));
             srow[m] = source_row(grp, t.m0 + min(16 * m + r16, rows - 1));
@@ -84,55 +153,73 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
             for (int c = 0; c < CT; ++c)
                 wrow[c][h] = wq + ((int64_t)t.e * N + min(n0 + 16 * c + 8 * h + lr, N - 1)) * (K / 2);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) xrow[m][h] = xq + (int64_t)row[m][h] * (K / 2);
+            for (int m = 0; m < XT; ++m) xrow[m][h] = xq + (int64_t)row[m][h] * (K / 2);
         }
 #pragma unroll
         for (int c = 0; c < CT; ++c)
             wsc[c] = ws + ((int64_t)t.e * KB * N + min(n0 + 16 * c + r16, N - 1)) * 8 + 2 * quarter;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) xsc[m] = xs + (int64_t)srow[m] * 8 + 2 * quarter;
+        for (int m = 0; m < XT; ++m) xsc[m] = xs + (int64_t)srow[m] * 8 + 2 * quarter;
 
-        auto load = [&](int p, uint4 *q, Pair<MT, CT> &s) {
-            uint4 *mine = q + wave * (MT + CT) * 128;
+        auto load = [&](int p, uint4 *q, Pair<MT, CT, XD> &s) {
+            uint4 *mine = q + wave * (XT + CT) * 128;
             int at[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)  // a chunk past K: the pair's first one
                 at[h] = p * kStepBytes + (p * kStepBytes + chunk[h] * 16 < K / 2 ? chunk[h] * 16 : 0);
+            if constexpr (XD == kCodes) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    __builtin_amdgcn_global_load_lds((global_void *)(xrow[m][h] + at[h]),
-                                                     (lds_void *)(mine + 128 * m + 64 * h), 16, 0, 0);
+                    for (int h = 0; h < 2; ++h)
+                        __builtin_amdgcn_global_load_lds((global_void *)(xrow[m][h] + at[h]),
+                                                         (lds_void *)(mine + 128 * m + 64 * h), 16, 0, 0);
+            } else {
+                // before the weights: it lands first, and is quantized while they travel
+                constexpr int kPer = XD == kF32 ? 4 : 8;  // elements per load
+                const int k = p * kStep + 64 * quarter;
+                const char *x = reinterpret_cast<const char *>(xq) + (r16 * ldx + k) * (16 / kPer);
+#pragma unroll
+                for (int i = 0; i < RawPair<XD>::kLoads; ++i)
+                    s.raw.u[i] = r16 < rows && k + kPer * i < K ? *reinterpret_cast<const uint4 *>(x + 16 * i)
+                                                                : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     __builtin_amdgcn_global_load_lds((global_void *)(wrow[c][h] + at[h]),
-                                                     (lds_void *)(mine + 128 * (MT + c) + 64 * h), 16, 0,
+                                                     (lds_void *)(mine + 128 * (XT + c) + 64 * h), 16, 0,
                                                      w8a8::kLdsLoadStream);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) s.sx[m] = *reinterpret_cast<const uint16_t *>(xsc[m] + (int64_t)p * grp.T * 8);
+            for (int m = 0; m < XT; ++m) s.sx[m] = *reinterpret_cast<const uint16_t *>(xsc[m] + (int64_t)p * grp.T * 8);
 #pragma unroll
             for (int c = 0; c < CT; ++c) s.sw[c] = *reinterpret_cast<const uint16_t *>(wsc[c] + (int64_t)p * N * 8);
         };
-        auto multiply = [&](const uint4 *q, const Pair<MT, CT> &s) {
-            const uint4 *mine = q + wave * (MT + CT) * 128;
+        auto multiply = [&](const uint4 *q, const Pair<MT, CT, XD> &s) {
+            const uint4 *mine = q + wave * (XT + CT) * 128;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int slot = (r16 >> 3) * 64 + (r16 & 7) * 8 + ((2 * quarter + u) ^ (r16 & 7) ^ (r16 >> 3));
                 v4i w[CT];
 #pragma unroll
-                for (int c = 0; c < CT; ++c) w[c] = __builtin_bit_cast(v4i, mine[128 * (MT + c) + slot]);
+                for (int c = 0; c < CT; ++c) w[c] = __builtin_bit_cast(v4i, mine[128 * (XT + c) + slot]);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    const v4i x = __builtin_bit_cast(v4i, mine[128 * m + slot]);
+                    v4i x;
+                    uint32_t sx;
+                    if constexpr (XD == kCodes) {
+                        x = __builtin_bit_cast(v4i, mine[128 * m + slot]);
+                        sx = s.sx[m];
+                    } else {
+                        sx = s.raw.quantize(u, x) << (8 * u);
+                    }
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) acc[m][c] = mfma_16x16x128(u, w[c], s.sw[c], x, s.sx[m], acc[m][c]);
+                    for (int c = 0; c < CT; ++c) acc[m][c] = mfma_16x16x128(u, w[c], s.sw[c], x, sx, acc[m][c]);
                 }
             }
         };
-        Pair<MT, CT> s0, s1;
+        Pair<MT, CT, XD> s0, s1;
         int p = wave;
         if (p < KB) load(p, q0, s0);
         if (p + WAVES < KB) load(p + WAVES, q1, s1);
@@ -216,8 +303,8 @@ hipError_t launch_ep(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, co
                      const Groups &g, int N, int K, const Output &o, hipStream_t stream) {
     const int KB = (K + kStep - 1) / kStep, tiles_n = (N + 16 * CT - 1) / (16 * CT);
     const int64_t tiles = most_tiles(g.S, g.E, 16 * MT, g.offsets != nullptr) * tiles_n;
-    decode_kernel<MT, CT, WAVES, EP><<<dim3((unsigned)tiles), dim3(WAVES * kWave), 0, stream>>>(
-        xq, xs, wq, ws, g, N, K, KB, tiles_n, o);
+    decode_kernel<MT, CT, WAVES, kCodes, EP><<<dim3((unsigned)tiles), dim3(WAVES * kWave), 0, stream>>>(
+        xq, xs, wq, ws, g, N, K, KB, tiles_n, 0, o);
     return hipGetLastError();
 }
 
@@ -255,7 +342,38 @@ hipError_t launch_rows(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, 
     }
 }
 
+template <int XD, Epilogue EP>
+hipError_t launch_fused(const void *x, int64_t ldx, const uint8_t *wq, const uint8_t *ws, int M, int N,
+                        int K, const Output &o, hipStream_t stream) {
+    const int tiles_n = (N + 15) / 16;
+    decode_kernel<1, 1, 8, XD, EP><<<dim3((unsigned)tiles_n), dim3(8 * kWave), 0, stream>>>(
+        static_cast<const uint8_t *>(x), nullptr, wq, ws, Groups{nullptr, nullptr, 1, M, M}, N, K,
+        (K + kStep - 1) / kStep, tiles_n, ldx, o);
+    return hipGetLastError();
+}
+
+template <int XD>
+hipError_t launch_fused(const void *x, int64_t ldx, const uint8_t *wq, const uint8_t *ws, int M, int N,
+                        int K, int out_dtype, const Output &o, hipStream_t stream) {
+    switch (out_dtype) {
+        case kBf16: return launch_fused<XD, kOutBf16>(x, ldx, wq, ws, M, N, K, o, stream);
+        case kF16: return launch_fused<XD, kOutF16>(x, ldx, wq, ws, M, N, K, o, stream);
+        default: return launch_fused<XD, kOutF32>(x, ldx, wq, ws, M, N, K, o, stream);
+    }
+}
+
 }  // namespace
+
+hipError_t launch_linear_decode(const void *x, int64_t ldx, int x_dtype, int M, const uint8_t *wq,
+                                const uint8_t *ws, int N, int K, int out_dtype, void *out,
+                                hipStream_t stream) {
+    const Output o{out, nullptr, nullptr};
+    switch (x_dtype) {
+        case kBf16: return launch_fused<kBf16>(x, ldx, wq, ws, M, N, K, out_dtype, o, stream);
+        case kF16: return launch_fused<kF16>(x, ldx, wq, ws, M, N, K, out_dtype, o, stream);
+        default: return launch_fused<kF32>(x, ldx, wq, ws, M, N, K, out_dtype, o, stream);
+    }
+}
 
 hipError_t launch_gemm_decode(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
                               const uint8_t *ws, const Groups &g, int N, int K, int epilogue,

@@ -347,8 +347,8 @@ w8a8_status mxfp4_gemm(const uint8_t *xq, const uint8_t *xs, int64_t M, const ui
                                          static_cast<hipStream_t>(stream)));
 }
 
-int64_t mxfp4_linear_workspace(int64_t M, int64_t K) {
-    if (M <= 0 || mx_shape(M, K) != W8A8_OK) return 0;
+int64_t mxfp4_linear_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || mx_shape(M, K) != W8A8_OK || mxfp4::single_launch_linear(M, N)) return 0;
     return mx_codes(M, K) + mx_scales(M, K);
 }
 
@@ -360,13 +360,17 @@ w8a8_status mxfp4_linear(const void *x, int64_t ldx, mxfp4_dtype x_dtype, int64_
     if (w8a8_status s = mx_weight(N, K)) return s;
     const int xd = selector(&x_dtype), od = selector(&out_dtype);
     if (!mx_dtype_ok(xd) || !mx_dtype_ok(od)) return W8A8_ERR_DTYPE;
-    if (ldx < K || ldx > INT_MAX || workspace_bytes < mxfp4_linear_workspace(M, K))
+    if (ldx < K || ldx > INT_MAX || workspace_bytes < mxfp4_linear_workspace(M, N, K))
         return W8A8_ERR_SHAPE;
     if (M == 0) return W8A8_OK;
-    if (!x || !wq || !ws || !out || !workspace) return W8A8_ERR_NULL;
+    const bool fused = mxfp4::single_launch_linear(M, N);
+    if (!x || !wq || !ws || !out || (!fused && !workspace)) return W8A8_ERR_NULL;
     if (misaligned(x) || misaligned(wq) || misaligned(ws) || misaligned(out) ||
         misaligned(workspace) || ldx * dtype_size(xd) % 16 != 0)
         return W8A8_ERR_ALIGN;
+    if (fused)
+        return hip_status(mxfp4::launch_linear_decode(x, ldx, xd, (int)M, wq, ws, (int)N, (int)K, od,
+                                                      out, static_cast<hipStream_t>(stream)));
     uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + mx_codes(M, K);
     if (w8a8_status s = mxfp4_quantize_rows(x, ldx, M, K, x_dtype, codes, scales, stream)) return s;
     return mxfp4_gemm(codes, scales, M, wq, ws, N, K, out_dtype, out, stream);
@@ -575,10 +579,11 @@ w8a8_status mxfp4_moe(const void *x, int64_t ldx, mxfp4_dtype dtype, int64_t T, 
     int32_t *slot_pos = reinterpret_cast<int32_t *>(ws + p.slot_pos);
     int32_t *row_token = reinterpret_cast<int32_t *>(ws + p.row_token);
     const int64_t S = T * top;
-    if (w8a8_status s = moe_sort(expert_ids, ids_bits, T, top, E, offsets, slot_pos, row_token,
-                                 ws + p.sort, p.sort_bytes, stream))
+    if (w8a8_status s = hip_status(moe::launch_sort_quantize(
+            expert_ids, ids_bits == 64, S, (int)top, (int)E, offsets, slot_pos, row_token,
+            ws + p.sort, x, ldx, T, (int)H, dt, ws + p.xq, ws + p.xs,
+            static_cast<hipStream_t>(stream))))
         return s;
-    if (w8a8_status s = mxfp4_quantize_rows(x, ldx, T, H, dtype, ws + p.xq, ws + p.xs, stream)) return s;
     if (w8a8_status s = mxfp4_expert_swiglu(ws + p.xq, ws + p.xs, T, row_token, S, offsets, E, w13q,
                                             w13s, F, H, ws + p.hq, ws + p.hs, stream))
         return s;

@@ -166,15 +166,28 @@ def test_gemm_nan_rows(m):
 
 
 @pytest.mark.parametrize("x_dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("m,n,k", [(1, 512, 4096), (37, 272, 352), (300, 640, 1312)])
+@pytest.mark.parametrize("m,n,k", [(1, 512, 4096), (3, 48, 32), (4, 272, 1312), (5, 1040, 96), (1, 8208, 96),
+                                   (37, 272, 352), (300, 640, 1312)])
 def test_linear(m, n, k, x_dtype):
     x, x64 = rows(m, k, x_dtype, seed=m, spread=1.0)
     wq, ws, w = packed(n, k, seed=n, lo=112, hi=120)
     got = b.mxfp4_linear(x, wq, ws, out_dtype=torch.float32)
     check_product(got, ref.values(*ref.quantize(x64)), w, "f32")
     assert torch.equal(b.mxfp4_linear(x, wq, ws), got.to(TYPES[x_dtype]))
-    work = torch.empty(b.mxfp4_linear_workspace(m, k), dtype=torch.uint8, device=DEV)
+    work = torch.empty(b.mxfp4_linear_workspace(m, n, k), dtype=torch.uint8, device=DEV)
     assert torch.equal(b.mxfp4_linear(x, wq, ws, out_dtype=torch.float32, workspace=work), got)
+
+
+@pytest.mark.parametrize("m", [2, 40])
+def test_linear_non_finite_and_apart(m):
+    """A row with an infinity or NaN gives a NaN row and leaves the others; rows may lie apart."""
+    base, _ = rows(m, 512, "bf16", seed=8)
+    x = base[:, 64:64 + 352]
+    x[1, 40] = float("nan")
+    wq, ws, _ = packed(64, 352, seed=9)
+    out = b.mxfp4_linear(x, wq, ws)
+    assert torch.isnan(out[1]).all() and torch.isfinite(out[:1]).all() and torch.isfinite(out[2:]).all()
+    assert torch.equal(out.nan_to_num(), b.mxfp4_linear(x.contiguous(), wq, ws).nan_to_num())
 
 
 def test_empty():
@@ -211,4 +224,5 @@ def test_refusals():
     with pytest.raises(TypeError):
         b.mxfp4_gemm(wq, ws, wq, ws, out_dtype=torch.float64)
     with pytest.raises(b.W8A8Error):
-        b.mxfp4_linear(x, wq, ws, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+        b.mxfp4_linear(rows(12, 64, "bf16", seed=1)[0], wq, ws,
+                       workspace=torch.empty(8, dtype=torch.uint8, device=DEV))

@@ -78,10 +78,15 @@ def test_gemm(lib):
 
 
 def test_linear(lib):
-    base = dict(x=P, ldx=64, xd=0, M=4, wq=P, ws=P, N=32, K=64, od=0, out=P, work=P, size=1 << 20, stream=None)
+    base = dict(x=P, ldx=64, xd=0, M=40, wq=P, ws=P, N=32, K=64, od=0, out=P, work=P, size=1 << 20, stream=None)
     c = caller(lib.mxfp4_linear, list(base), base)
-    need = lib.mxfp4_linear_workspace(4, 64)
-    assert need >= 4 * 32 + 4 * 8 and lib.mxfp4_linear_workspace(0, 64) == 0 and lib.mxfp4_linear_workspace(4, 60) == 0
+    need = lib.mxfp4_linear_workspace(40, 32, 64)
+    assert need >= 40 * 32 + 40 * 8 and lib.mxfp4_linear_workspace(0, 32, 64) == 0
+    assert lib.mxfp4_linear_workspace(40, 32, 60) == 0
+    # a few rows: no workspace, one may be given all the same
+    assert lib.mxfp4_linear_workspace(4, 32, 64) == 0 and lib.mxfp4_linear_workspace(5, 32, 64) > 0
+    assert lib.mxfp4_linear_workspace(1, 8208, 64) > 0
+    assert c(M=4, work=0, size=0, out=0) == NULL and c(M=5, size=0) == SHAPE and c(M=4, work=P + 8) == ALIGN
     assert c(size=need - 1) == SHAPE and c(M=-1) == SHAPE and c(N=8) == SHAPE and c(ldx=63) == SHAPE
     assert c(xd=4) == DTYPE and c(od=-2) == DTYPE
     for n in ("x", "wq", "ws", "out", "work"):
