@@ -350,7 +350,7 @@ w8a8_status mxfp4_dequantize_rows(const uint8_t *codes, const uint8_t *scales, i
 /*
  * out[m][n] = sum_k x[m][k] * w[n][k] for MXFP4 x [M,K] and w [N,K]: products
  * and scales exact, accumulated in fp32, rounded once to dtype. M >= 0, N a
- * positive multiple of 16, K as above.
+ * positive multiple of 16 with the same bound as M, M * N <= 2^36, K as above.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, HIP.
  */
 w8a8_status mxfp4_gemm(const uint8_t *xq, const uint8_t *xs, int64_t M, const uint8_t *wq,
@@ -441,7 +441,8 @@ w8a8_status moe_combine_backward(const void *d_out, int64_t ldd, const void *row
  *   xq, xs     MXFP4 [T,K]; offsets [E+1], row_token [S] from moe_sort
  *   wq         [E][N, K/2], ws [E][ceil(K/256), N, 8]
  *   out        [S,N] of dtype
- * S >= 0 rows, N a positive multiple of 16, K as for mxfp4_gemm.
+ * S >= 0 rows, N and K as for mxfp4_gemm; with row_token, x's codes hold less
+ * than 2^32 bytes.
  * mxfp4_expert_swiglu: N = 2F, rows 2f and 2f+1 of a weight are the gate and
  * the up projection of hidden unit f (F a positive multiple of 32); writes the
  * hidden activations gate / (1 + exp(-gate)) * up, computed in fp32 from the

@@ -487,18 +487,22 @@ hipError_t launch_epilogue(const Operands &op, const Groups &g, int N, int K, co
 }
 
 template <int BM, int BN, int GM, int GN, int CH, int NB, int OCC>
-hipError_t launch_shape(const Operands &op, const Groups &g, int N, int K, int epilogue,
+hipError_t launch_plain(const Operands &op, const Groups &g, int N, int K, int epilogue,
                         const Output &o, hipStream_t stream) {
     switch (epilogue) {
         case kOutBf16: return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kOutBf16>(op, g, N, K, o, stream);
         case kOutF16: return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kOutF16>(op, g, N, K, o, stream);
-        case kOutF32: return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kOutF32>(op, g, N, K, o, stream);
-        default:
-            // a wavefront's channels have to hold whole blocks of hidden units
-            if constexpr (BN / GN >= 64)
-                return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kSwiglu>(op, g, N, K, o, stream);
+        default: return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kOutF32>(op, g, N, K, o, stream);
     }
-    return hipErrorInvalidValue;
+}
+
+template <int BM, int BN, int GM, int GN, int CH, int NB, int OCC>
+hipError_t launch_shape(const Operands &op, const Groups &g, int N, int K, int epilogue,
+                        const Output &o, hipStream_t stream) {
+    static_assert(BN / GN >= 64, "a wavefront's channels hold whole blocks of hidden units");
+    if (epilogue == kSwiglu)
+        return launch_epilogue<BM, BN, GM, GN, CH, NB, OCC, kSwiglu>(op, g, N, K, o, stream);
+    return launch_plain<BM, BN, GM, GN, CH, NB, OCC>(op, g, N, K, epilogue, o, stream);
 }
 
 }  // namespace
@@ -513,15 +517,20 @@ hipError_t launch_gemm_tiled(const uint8_t *xq, const uint8_t *xs, const uint8_t
     // 8.6, 10.0, 11.3, 14.3, 25.3; M = 384 10.9, 10.4, 11.5, 14.4, 25.2; M = 768
     // 16.4, 14.6, 12.4, 15.3, 26.5; M = 1536 28.1, 23.4, 24.1, 17.5, 27.6; M = 4096
     // 68.5, 54.4, 49.5, 47.5, 36.1.
+    // Short K: two workgroups of 256 x 128 per CU with 128-element stages, whose
+    // starts and stores overlap each other's products (8192 x 8192, K = 512 47.6 ->
+    // 44.1 us, K = 1024 61.3 -> 56.2, K = 2048 86.6 -> 90.5).
     const int64_t cus = w8a8::device_cu_count();
     auto tiles = [&](int bm, int bn) {
         return most_tiles(g.S, g.E, bm, g.offsets != nullptr) * ((N + bn - 1) / bn);
     };
     if (tiles(64, 64) <= cus && epilogue != kSwiglu)
-        return launch_shape<64, 64, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
+        return launch_plain<64, 64, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
     if (tiles(64, 128) <= cus) return launch_shape<64, 128, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
     if (tiles(128, 128) <= cus) return launch_shape<128, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
     if (tiles(256, 128) <= cus) return launch_shape<256, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
+    if (K <= 1024 && epilogue != kSwiglu)
+        return launch_plain<256, 128, 2, 2, 4, 3, 2>(op, g, N, K, epilogue, o, stream);
     return launch_shape<256, 256, 2, 4, 8, 2, 1>(op, g, N, K, epilogue, o, stream);
 }
 

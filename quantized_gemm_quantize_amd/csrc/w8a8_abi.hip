@@ -300,6 +300,16 @@ static w8a8_status mx_weight(int64_t N, int64_t K) {
     return mx_shape(N, K);
 }
 
+// Outputs of a product: at most 2^36 (the kernels count tiles in 32 bits).
+static w8a8_status mx_out(int64_t rows, int64_t N) {
+    return rows > 0 && N > ((int64_t)1 << 36) / rows ? W8A8_ERR_SHAPE : W8A8_OK;
+}
+
+// Activation rows that are read through row_token lie within 32-bit offsets.
+static w8a8_status mx_tokens(int64_t T, int64_t K) {
+    return T * (K / 2) > (int64_t)UINT_MAX ? W8A8_ERR_SHAPE : W8A8_OK;
+}
+
 static int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 static int64_t mx_codes(int64_t rows, int64_t K) { return align256(rows * (K / 2)); }
 static int64_t mx_scales(int64_t rows, int64_t K) { return align256((K + 255) / 256 * rows * 8); }
@@ -335,6 +345,7 @@ w8a8_status mxfp4_gemm(const uint8_t *xq, const uint8_t *xs, int64_t M, const ui
                        void *stream) {
     if (w8a8_status s = mx_shape(M, K)) return s;
     if (w8a8_status s = mx_weight(N, K)) return s;
+    if (w8a8_status s = mx_out(M, N)) return s;
     const int dt = selector(&dtype);
     if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
     if (M == 0) return W8A8_OK;
@@ -358,6 +369,7 @@ w8a8_status mxfp4_linear(const void *x, int64_t ldx, mxfp4_dtype x_dtype, int64_
                          int64_t workspace_bytes, void *stream) {
     if (w8a8_status s = mx_shape(M, K)) return s;
     if (w8a8_status s = mx_weight(N, K)) return s;
+    if (w8a8_status s = mx_out(M, N)) return s;
     const int xd = selector(&x_dtype), od = selector(&out_dtype);
     if (!mx_dtype_ok(xd) || !mx_dtype_ok(od)) return W8A8_ERR_DTYPE;
     if (ldx < K || ldx > INT_MAX || workspace_bytes < mxfp4_linear_workspace(M, N, K))
@@ -485,8 +497,11 @@ static w8a8_status expert_entry(const uint8_t *xq, const uint8_t *xs, int64_t T,
     if (w8a8_status s = mx_shape(S, K)) return s;
     if (w8a8_status s = mx_shape(T, K)) return s;
     if (w8a8_status s = mx_weight(N, K)) return s;
+    if (w8a8_status s = mx_out(S, N)) return s;
     if (E <= 0 || E > MOE_MAX_EXPERTS || (!row_token && T != S) || (S > 0 && T == 0))
         return W8A8_ERR_SHAPE;
+    if (row_token)
+        if (w8a8_status s = mx_tokens(T, K)) return s;
     if (S == 0) return W8A8_OK;
     if (!xq || !xs || !offsets || !wq || !ws) return W8A8_ERR_NULL;
     if (epilogue == mxfp4::kSwiglu ? !o.codes || !o.scales : !o.out) return W8A8_ERR_NULL;
@@ -531,6 +546,9 @@ static w8a8_status moe_parts(int64_t T, int64_t top, int64_t E, int64_t H, int64
     if (w8a8_status s = mx_shape(S, F)) return s;
     if (w8a8_status s = mx_weight(H, F)) return s;
     if (w8a8_status s = mx_weight(2 * F, H)) return s;
+    if (w8a8_status s = mx_out(S, 2 * F)) return s;
+    if (w8a8_status s = mx_out(S, H)) return s;
+    if (w8a8_status s = mx_tokens(T, H)) return s;
     int64_t at = 0;
     auto take = [&](int64_t bytes) { const int64_t b = at; at += align256(bytes); return b; };
     p.offsets = take((E + 1) * 4);
