@@ -79,6 +79,19 @@ struct Groups {
     int E, S, T;
 };
 
+// Expert ids of slots, `top` per token, 32 or 64 bits each.
+struct Ids {
+    const void *ids;
+    int bits, top;
+};
+
+// Expert of a slot, E when its id names none.
+__device__ __forceinline__ int expert_of(const Ids &s, int64_t slot, int E) {
+    const int64_t id = s.bits == 64 ? static_cast<const int64_t *>(s.ids)[slot]
+                                    : static_cast<const int32_t *>(s.ids)[slot];
+    return id >= 0 && id < E ? (int)id : E;
+}
+
 struct Tile {
     int e;       // group, E for the rows without a weight, -1 past the last tile
     int m0, m1;  // its rows: m0 .. m1-1 with m1 the end of the group

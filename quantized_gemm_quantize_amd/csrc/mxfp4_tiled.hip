@@ -519,7 +519,11 @@ hipError_t launch_gemm_tiled(const uint8_t *xq, const uint8_t *xs, const uint8_t
     // 68.5, 54.4, 49.5, 47.5, 36.1.
     // Short K: two workgroups of 256 x 128 per CU with 128-element stages, whose
     // starts and stores overlap each other's products (8192 x 8192, K = 512 47.6 ->
-    // 44.1 us, K = 1024 61.3 -> 56.2, K = 2048 86.6 -> 90.5).
+    // 44.1 us, K = 1024 61.3 -> 56.2, K = 2048 86.6 -> 90.5; 32 experts' gate and up
+    // [2944, 960] with 285 rows each 42.1 -> 36.4).
+    // Small groups: 64 rows, as a taller tile is mostly empty (32 experts with 64
+    // rows each: gate and up [4096, 4096] 82.1 -> 77.5, down [4096, 2048] 45.1 -> 38.9;
+    // with 256 rows 111 -> 152 and 63 -> 82).
     const int64_t cus = w8a8::device_cu_count();
     auto tiles = [&](int bm, int bn) {
         return most_tiles(g.S, g.E, bm, g.offsets != nullptr) * ((N + bn - 1) / bn);
@@ -527,10 +531,11 @@ hipError_t launch_gemm_tiled(const uint8_t *xq, const uint8_t *xs, const uint8_t
     if (tiles(64, 64) <= cus && epilogue != kSwiglu)
         return launch_plain<64, 64, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
     if (tiles(64, 128) <= cus) return launch_shape<64, 128, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
+    if (g.offsets && g.S < 96ll * g.E)
+        return launch_shape<64, 128, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
     if (tiles(128, 128) <= cus) return launch_shape<128, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
     if (tiles(256, 128) <= cus) return launch_shape<256, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
-    if (K <= 1024 && epilogue != kSwiglu)
-        return launch_plain<256, 128, 2, 2, 4, 3, 2>(op, g, N, K, epilogue, o, stream);
+    if (K <= 1024) return launch_shape<256, 128, 2, 2, 4, 3, 2>(op, g, N, K, epilogue, o, stream);
     return launch_shape<256, 256, 2, 4, 8, 2, 1>(op, g, N, K, epilogue, o, stream);
 }
 

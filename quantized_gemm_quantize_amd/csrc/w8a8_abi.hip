@@ -597,6 +597,15 @@ w8a8_status mxfp4_moe(const void *x, int64_t ldx, mxfp4_dtype dtype, int64_t T, 
     int32_t *slot_pos = reinterpret_cast<int32_t *>(ws + p.slot_pos);
     int32_t *row_token = reinterpret_cast<int32_t *>(ws + p.row_token);
     const int64_t S = T * top;
+    if (mxfp4::few_slots(S, H, F)) {
+        const mxfp4::Ids slots{expert_ids, ids_bits, (int)top};
+        hipStream_t st = static_cast<hipStream_t>(stream);
+        if (w8a8_status s = hip_status(mxfp4::launch_moe_up(x, ldx, dt, slots, (int)S, (int)E, w13q, w13s, (int)F,
+                                                            (int)H, ws + p.hq, ws + p.hs, st)))
+            return s;
+        return hip_status(mxfp4::launch_moe_down(ws + p.hq, ws + p.hs, slots, weights, (int)T, (int)E, w2q, w2s,
+                                                 (int)H, (int)F, dt, out, st));
+    }
     if (w8a8_status s = hip_status(moe::launch_sort_quantize(
             expert_ids, ids_bits == 64, S, (int)top, (int)E, offsets, slot_pos, row_token,
             ws + p.sort, x, ldx, T, (int)H, dt, ws + p.xq, ws + p.xs,

@@ -278,10 +278,14 @@ def test_swiglu_saturated_gates():
     check_hidden(hq, hs, h, np.abs(h) * 2.0 ** -20 + 1e-38)
 
 
-@pytest.mark.parametrize("T,top,E,H,F,dtype,drop", [(1, 2, 4, 256, 96, "bf16", 0.0), (70, 2, 6, 288, 160, "f16", 0.1),
-                                                    (600, 4, 4, 512, 288, "f32", 0.0)])
+@pytest.mark.parametrize("T,top,E,H,F,dtype,drop", [(1, 2, 4, 256, 96, "bf16", 0.0), (1, 1, 1, 32, 32, "f32", 0.0),
+                                                    (3, 2, 5, 288, 160, "f16", 0.3), (2, 3, 8, 1312, 736, "f32", 0.0),
+                                                    (1, 4, 16, 4096, 2048, "bf16", 0.0), (8, 8, 16, 256, 96, "bf16", 0.1),
+                                                    (70, 2, 6, 288, 160, "f16", 0.1), (600, 4, 4, 512, 288, "f32", 0.0)])
 def test_layer_is_its_parts(T, top, E, H, F, dtype, drop):
-    """mxfp4_moe gives bit for bit what its parts give, and is close to the layer in 64 bits."""
+    """mxfp4_moe is close to the layer in 64 bits; with more slots than the two-launch form takes, it
+    gives bit for bit what its parts give (that form sums in another order and does not round the
+    experts' outputs)."""
     ids = torch.from_numpy(routing(T, top, E, seed=T, drop=drop)).to(DEV)
     weights = torch.rand((T, top), generator=torch.Generator().manual_seed(1)).to(DEV)
     x, x64 = rows(T, H, dtype, seed=2, spread=0.5)
@@ -294,7 +298,8 @@ def test_layer_is_its_parts(T, top, E, H, F, dtype, drop):
     xq, xs = b.mxfp4_quantize_rows(x)
     hq, hs = b.mxfp4_expert_swiglu(xq, xs, offsets, w13q, w13s, row_token=row_token)
     y = b.mxfp4_expert_gemm(hq, hs, offsets, w2q, w2s, out_dtype=x.dtype)
-    assert torch.equal(out, b.moe_combine(y, slot_pos, weights))
+    if T * top > 64:
+        assert torch.equal(out, b.moe_combine(y, slot_pos, weights))
     off, pos, tok = ref.sort(ids.cpu().numpy(), E)
     xv = ref.values(*ref.quantize(x64))
     y64 = np.zeros((T * top, H))
@@ -308,6 +313,29 @@ def test_layer_is_its_parts(T, top, E, H, F, dtype, drop):
     # norm; the outputs' type adds its own roundings (of y and of out)
     err = np.linalg.norm(out.double().cpu().numpy() - want) / np.linalg.norm(want)
     assert err <= 2.0 ** -8 + 3 * HALF_ULP[dtype]
+
+
+@pytest.mark.parametrize("T", [2, 50])
+def test_layer_dropped_slots(T):
+    """Dropped slots add nothing, whatever their weights hold and however their ids are out of range;
+    a token without any other slot gets 0."""
+    E, H, F = 4, 288, 96
+    x, _ = rows(T, H, "bf16", seed=3, spread=0.5)
+    w13 = [packed(2 * F, H, seed=10 + e, lo=119, hi=123) for e in range(E)]
+    w2 = [packed(H, F, seed=50 + e, lo=119, hi=123) for e in range(E)]
+    stacks = [torch.stack([w[i] for w in ws]) for ws in (w13, w2) for i in (0, 1)]
+    ids = torch.full((T, 2), 1, dtype=torch.int64, device=DEV)
+    ids[0, 1], ids[1] = 2 ** 32 + 1, torch.tensor([-1, E])
+    w = torch.full((T, 2), 0.5, device=DEV)
+    w[0, 1], w[1] = float("nan"), torch.tensor([float("inf"), float("nan")])
+    out = b.mxfp4_moe(x, ids, w, *stacks)
+    assert (out[1] == 0).all() and torch.isfinite(out).all()
+    one = b.mxfp4_moe(x[:1], ids[:1, :1].contiguous(), w[:1, :1].contiguous(), *stacks)
+    # the same sum but for the order of its parts (and the rounding of the experts' outputs)
+    assert torch.allclose(out[:1].float(), one.float(), rtol=2.0 ** -6, atol=2.0 ** -8 * one.abs().max().item())
+    wide = torch.zeros((T, 400), dtype=torch.bfloat16, device=DEV)
+    wide[:, 64:64 + H] = x
+    assert torch.equal(b.mxfp4_moe(wide[:, 64:64 + H], ids.to(torch.int32).masked_fill(ids > E, -5), w, *stacks), out)
 
 
 def test_refusals():
