@@ -12,7 +12,11 @@
 //   d_w[t, j] = <d_out[t], rows[p]>.
 //
 // Sums run in fp32 in the order of j (and a fixed tree over the row), so
-// results do not depend on how the work is spread. All of it is bound by HBM.
+// results do not depend on how the work is spread. The rows' kernels are bound
+// by HBM and go token by token, so that each token is read once. Measured, 16448
+// tokens x 4 slots x 4096 bf16: gather 121 us (674 MB, 5.6 TB/s), combine 111 (6.1),
+// its backward 230 (1.21 GB, 5.3), the gather's 110; the sort of the 65792 slots,
+// bound by the latency of its two launches, 16.
 #include <type_traits>
 
 #include "launch.hpp"

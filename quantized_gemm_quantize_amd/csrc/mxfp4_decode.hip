@@ -5,7 +5,11 @@
 // once. A workgroup owns 16 CT channels of one group's weight and up to 16 MT
 // of its rows; its WAVES wavefronts split K in pairs of 128 bytes of codes (256
 // elements), wavefront w taking pairs w, w + WAVES, ..., so that neighbouring
-// wavefronts read neighbouring cache lines.
+// wavefronts read neighbouring cache lines. Measured,
+// least and median of 15: 1 x 4096 x 4096 (8.9 MB) 5.6 and 6.6 us; 32 experts' gate and
+// up [4096, 4096] for 64 tokens (285 MB) 44 and 56 us, 6.5 and 5.1 TB/s; their down
+// products (142 MB) 24.5 and 29 us; one token's four experts 9.2 and 6.5 us (36 and 18
+// MB), where the start and the end of one workgroup per CU show.
 //
 //  - Codes of weights and activations travel global -> LDS with 16-byte
 //    direct-to-LDS loads of 8 whole lines each, two pairs in flight per

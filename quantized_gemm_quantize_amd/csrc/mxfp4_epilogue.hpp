@@ -18,30 +18,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v2h{(_Float16)lo, (_Float16)hi});
 }
 
-// One 32x32 tile of a product whose first MFMA operand was the weight: this
-// lane's row m, channels n0 + 8g + 4 half + 0..3.
-template <Epilogue EP>
-__device__ __forceinline__ void store_tile(const v16f &acc, void *out, int64_t m, bool live, int n0,
-                                           int half, int N) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int n = n0 + 8 * g + 4 * half;
-        if (!live || n >= N) continue;
-        const int64_t at = m * N + n;
-        if constexpr (EP == kOutF32)
-            *reinterpret_cast<v4f *>(static_cast<float *>(out) + at) =
-                v4f{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
-        else if constexpr (EP == kOutBf16)
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) =
-                make_uint2(w8a8::pack_bf16x2(acc[4 * g], acc[4 * g + 1]),
-                           w8a8::pack_bf16x2(acc[4 * g + 2], acc[4 * g + 3]));
-        else
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) =
-                make_uint2(pack_f16x2(acc[4 * g], acc[4 * g + 1]),
-                           pack_f16x2(acc[4 * g + 2], acc[4 * g + 3]));
-    }
-}
-
 // SwiGLU of two neighbouring 32-channel tiles (64 channels: gate and up rows
 // alternate, so 32 hidden units, one MXFP4 block) and the quantization of the
 // block. A lane holds units 16 jj + 4 g + 2 half + 0..1 of row m (jj: tile);

@@ -3,8 +3,8 @@
 //
 //   out[m, n] = sum over blocks b of 2^(ex[m,b] + ew[n,b]) * sum_{k in b} qx[m,k] qw[n,k]
 //
-// A workgroup of 4 wavefronts computes a BM x BN tile; each wavefront owns a
-// (BM/2) x (BN/2) part as 32x32 tiles of v_mfma_scale_f32_32x32x64_f8f6f4,
+// A workgroup of GM x GN wavefronts computes a BM x BN tile; each wavefront owns
+// a (BM/GM) x (BN/GN) part as 32x32 tiles of v_mfma_scale_f32_32x32x64_f8f6f4,
 // which takes two fp4 blocks of 32 per row and their scales and accumulates
 // in fp32. A K stage is CH = 8 chunks of 16 bytes per row (256 elements, 8
 // scale bytes) or CH = 4 (128 elements, 4 scale bytes). Lanes 0-31 take the
@@ -12,21 +12,30 @@
 // operands, so the stage's K steps use consecutive bytes of one scale register.
 //
 //  - Codes and scales travel global -> LDS with direct-to-LDS loads (16 and 4
-//    bytes per lane) through a ring of STAGES buffers, loads running STAGES-1
-//    stages ahead of the MFMAs. Chunk c of row r sits at slot c ^ swz(r), which
-//    keeps the 16-byte fragment reads free of bank conflicts. Scales lie as
-//    32-bit words: CH = 8, one per lane of a 32-row fragment; CH = 4, one per
-//    row, read by both halves.
+//    bytes per lane) through NB buffers, two stages ahead of the MFMAs. Chunk c
+//    of row r sits at slot c ^ swz(r), which keeps the 16-byte fragment reads
+//    free of bank conflicts. Scales lie as 32-bit words: CH = 8, one per lane of a
+//    32-row fragment; CH = 4, one per row, read by both halves.
 //  - Rows past the group or N are read from the last valid row (their outputs
 //    are never stored). Blocks past K are read from inside the row; both sides'
 //    scale codes there are the storage's padding 0, so that each product is
 //    below 2^-240 and adds nothing in fp32.
 //  - Rows grouped by expert read their activation row through row_token, so no
-//    sorted copy of the activations exists.
+//    sorted copy of the activations exists. A wavefront whose rows lie past the
+//    group's end only loads.
 //  - The MFMA takes the weight first: a lane ends with 4 consecutive channels
 //    of a row. Outputs are staged in the wavefront's own LDS and stored as
 //    16-byte pieces of contiguous rows; SwiGLU joins gate and up in registers
 //    and stores the hidden activations as MXFP4, 17/64 of their bf16 bytes.
+//
+// What bounds it (8192 x 8192, by K): a 256 x 256 tile's K stage takes 1.6 us,
+// 5.3 PFLOP/s over the chip, where the MFMA loop alone reaches 5.3-6.5 (its clock
+// falls under the load). Alone, a stage's 68 KB of operands take 1.27 us: 64
+// reads of 128 bytes in flight per CU at a latency of about 300 clocks, 27 bytes
+// per clock, whatever the address pattern; so a tile with more products per byte
+// is faster until too few tiles are left (see the choice at the end). Around its
+// stages a tile costs about 8 us more: its first loads, and the stores of a
+// plain output or the exponentials of SwiGLU.
 #include <algorithm>
 
 #include "launch.hpp"
@@ -36,7 +45,6 @@ namespace mxfp4 {
 namespace {
 
 using w8a8::vm_barrier;
-
 
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -94,13 +102,15 @@ __device__ void load_lds16(Buffer b, void *dst, uint32_t lane_off, int off);
 __device__ void load_lds4(Buffer b, void *dst, uint32_t lane_off, int off);
 #endif
 
-// Where this lane's share of every stage comes from, and what it fills: a
-// buffer descriptor per operand, a 32-bit offset per lane that stays, and a
-// uniform offset that moves with the stage. (Addresses in vector registers
-// cost a 64-bit addition per load, which holds up the MFMAs' issue.)
+// Codes and scales of activations (a, sa) and weights (b, sb).
 struct Sources {
     Buffer a, b, sa, sb;
 };
+
+// Where this lane's share of every stage comes from: a buffer per operand, a
+// 32-bit offset per lane that stays, and a uniform offset that moves with the
+// stage. (Addresses in vector registers cost a 64-bit addition per load, which
+// holds up the MFMAs' issue.)
 
 template <typename Sh>
 struct Loads {
@@ -319,7 +329,8 @@ __device__ __forceinline__ void store_plain(const v16f (&acc)[TM][TN], uint4 *mi
 // gridDim.x-th: then the first stages of the next tile are on their way before
 // the epilogue of a tile. Plain outputs gain nothing from it, as a workgroup
 // would wait for its stores with the next tile's loads (38400 x 4096 x 1024:
-// 118 us a workgroup per tile, 127 persistent).
+// 118 us a workgroup per tile, 127 persistent); SwiGLU does (32 experts' gate and
+// up of 8192 tokens: 348 -> 335 us).
 template <int BM, int BN, int GM, int GN, int CH, int NB, int OCC, bool KTAIL, Epilogue EP>
 __global__ __launch_bounds__(GM *GN *kWave, OCC *GM *GN / 4) void tiled_kernel(
     Operands op, Groups grp, int N, int K, int KB, int tiles_m, int tiles_n, Output o) {
