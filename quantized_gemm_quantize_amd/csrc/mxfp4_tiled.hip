@@ -333,7 +333,7 @@ __device__ __forceinline__ void store_plain(const v16f (&acc)[TM][TN], uint4 *mi
 // up of 8192 tokens: 348 -> 335 us).
 template <int BM, int BN, int GM, int GN, int CH, int NB, int OCC, bool KTAIL, Epilogue EP>
 __global__ __launch_bounds__(GM *GN *kWave, OCC *GM *GN / 4) void tiled_kernel(
-    Operands op, Groups grp, int N, int K, int KB, int tiles_m, int tiles_n, Output o) {
+    Operands op, Groups grp, int N, int K, int KB, int tiles_m, int tiles_n, int slots, Output o) {
     using Sh = Shape<BM, BN, GM, GN, CH>;
     constexpr bool PERSIST = EP == kSwiglu;
     constexpr int WM = BM / GM, WN = BN / GN, TM = WM / 32, TN = WN / 32;
@@ -373,6 +373,13 @@ __global__ __launch_bounds__(GM *GN *kWave, OCC *GM *GN / 4) void tiled_kernel(
     };
     int pid = blockIdx.x;
     if (pid >= tiles) return;
+    // Several tiles per CU of the same length: without this all CUs compute, then
+    // all store (57-75 GB/s for a CU among few, 21 when all store). The first
+    // workgroups start up to 8 us apart within an XCD, the later ones follow them
+    // (us: 8192 x 8192, K = 512 47.0 -> 41.4, 2048 89.6 -> 84.1, 4096 145 -> 139; 32
+    // experts' down products of 8192 tokens 197 -> 186). SwiGLU's stores are few.
+    if (!PERSIST && pid < slots && tiles > 2 * slots)
+        for (int wait = pid / 8 % 32; wait > 0; --wait) __builtin_amdgcn_s_sleep(8);
     int n0;
     Tile tile = locate(pid, n0);
     Loads<Sh> g;
@@ -488,12 +495,12 @@ hipError_t launch_epilogue(const Operands &op, const Groups &g, int N, int K, co
     const int KB = (K + kStep - 1) / kStep;
     const int tiles_n = (N + BN - 1) / BN;
     const int64_t tiles_m = most_tiles(g.S, g.E, BM, g.offsets != nullptr);
-    const int64_t resident = EP == kSwiglu ? (int64_t)OCC * w8a8::device_cu_count() : tiles_m * tiles_n;
-    const dim3 grid((unsigned)std::min(tiles_m * tiles_n, resident)), block(GM * GN * kWave);
+    const int slots = OCC * w8a8::device_cu_count();  // workgroups that run at once
+    const dim3 grid((unsigned)(EP == kSwiglu ? std::min<int64_t>(tiles_m * tiles_n, slots) : tiles_m * tiles_n)), block(GM * GN * kWave);
     if (K % (32 * CH) == 0)
-        tiled_kernel<BM, BN, GM, GN, CH, NB, OCC, false, EP><<<grid, block, 0, stream>>>(op, g, N, K, KB, (int)tiles_m, tiles_n, o);
+        tiled_kernel<BM, BN, GM, GN, CH, NB, OCC, false, EP><<<grid, block, 0, stream>>>(op, g, N, K, KB, (int)tiles_m, tiles_n, slots, o);
     else
-        tiled_kernel<BM, BN, GM, GN, CH, NB, OCC, true, EP><<<grid, block, 0, stream>>>(op, g, N, K, KB, (int)tiles_m, tiles_n, o);
+        tiled_kernel<BM, BN, GM, GN, CH, NB, OCC, true, EP><<<grid, block, 0, stream>>>(op, g, N, K, KB, (int)tiles_m, tiles_n, slots, o);
     return hipGetLastError();
 }
 
