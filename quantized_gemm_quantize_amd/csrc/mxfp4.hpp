@@ -110,45 +110,54 @@ __device__ __forceinline__ int scan_lanes(int v) {
     return v;
 }
 
-// Group `e` of 64 consecutive ones, one per lane: its first row and rows (none
-// past group E, which holds the rows without a weight). Bounds that a malformed
-// offsets array could break are clamped, so rows stay inside [0, S).
-__device__ __forceinline__ void group_rows(const Groups &g, int e, int &lo, int &n) {
-    const int a = g.offsets[min(e, g.E)], b = g.offsets[min(e + 1, g.E)];
-    lo = min(max(a, 0), g.S);
-    n = e < g.E ? min(max(b, lo), g.S) - lo : e == g.E ? g.S - lo : 0;
+// 64 consecutive groups from `base` on, one per lane: the group's first row and
+// rows (none past group E, which holds the rows without a weight), and the tiles
+// of these groups up to and including it. Bounds that a malformed offsets array
+// could break are clamped, so rows stay inside [0, S).
+struct GroupScan {
+    int lo, n, upto;
+};
+
+template <int BM>
+__device__ __forceinline__ GroupScan scan_groups(const Groups &g, int base) {
+    int e = base + (threadIdx.x & (kWave - 1));
+    asm volatile("" : "+v"(e));  // or a persistent kernel keeps the addresses in registers
+    int a = g.offsets[min(e, g.E)], b = g.offsets[min(e + 1, g.E)];
+    asm volatile("" : "+v"(a), "+v"(b));  // both under way together, not the second one in a branch
+    GroupScan s;
+    s.lo = min(max(a, 0), g.S);
+    s.n = e < g.E ? min(max(b, s.lo), g.S) - s.lo : e == g.E ? g.S - s.lo : 0;
+    s.upto = scan_lanes((s.n + BM - 1) / BM);
+    return s;
 }
 
-// All tiles of BM rows, found by every wavefront for itself.
+// All tiles of BM rows, found by every wavefront for itself (first: the scan
+// from group 0 on).
 template <int BM>
-__device__ __forceinline__ int count_tiles(const Groups &g) {
-    int own = 0;
-    for (int base = 0; base <= g.E; base += kWave) {
-        int lo, n;
-        group_rows(g, base + (threadIdx.x & (kWave - 1)), lo, n);
-        own += (n + BM - 1) / BM;
-    }
-    return __builtin_amdgcn_readlane(scan_lanes(own), kWave - 1);
+__device__ __forceinline__ int count_tiles(const Groups &g, const GroupScan &first) {
+    int total = __builtin_amdgcn_readlane(first.upto, kWave - 1);
+    for (int base = kWave; base <= g.E; base += kWave)
+        total += __builtin_amdgcn_readlane(scan_groups<BM>(g, base).upto, kWave - 1);
+    return total;
 }
 
 // Tile t of the groups' rows cut into tiles of BM rows, group after group, 64
 // groups at a time.
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const Groups &g, int t) {
+__device__ __forceinline__ Tile find_tile(const Groups &g, const GroupScan &first, int t) {
     if (!g.offsets) return Tile{t * BM < g.S ? 0 : -1, t * BM, g.S};
+    GroupScan s = first;
     int before = 0;
     for (int base = 0; base <= g.E; base += kWave) {
-        int lo, n;
-        group_rows(g, base + (threadIdx.x & (kWave - 1)), lo, n);
-        const int own = (n + BM - 1) / BM, upto = scan_lanes(own);
-        const uint64_t hit = __builtin_amdgcn_ballot_w64(before + upto > t);
+        if (base > 0) s = scan_groups<BM>(g, base);
+        const uint64_t hit = __builtin_amdgcn_ballot_w64(before + s.upto > t);
         if (hit) {
             const int l = __builtin_ctzll(hit);
-            const int first = before + __builtin_amdgcn_readlane(upto - own, l);
-            const int glo = __builtin_amdgcn_readlane(lo, l), gn = __builtin_amdgcn_readlane(n, l);
-            return Tile{base + l, glo + (t - first) * BM, glo + gn};
+            const int lo = __builtin_amdgcn_readlane(s.lo, l), n = __builtin_amdgcn_readlane(s.n, l);
+            const int first_t = before + __builtin_amdgcn_readlane(s.upto, l) - (n + BM - 1) / BM;
+            return Tile{base + l, lo + (t - first_t) * BM, lo + n};
         }
-        before += __builtin_amdgcn_readlane(upto, kWave - 1);
+        before += __builtin_amdgcn_readlane(s.upto, kWave - 1);
     }
     return Tile{-1, 0, 0};
 }
@@ -163,9 +172,15 @@ inline int64_t most_tiles(int64_t S, int64_t E, int BM, bool grouped) {
     return split < S ? split : S;
 }
 
-// Activation row of product row r.
-__device__ __forceinline__ int source_row(const Groups &g, int r) {
-    return g.row_token ? min(max(g.row_token[r], 0), g.T - 1) : r;
+// Activation rows of N product rows: r[i] -> row_token[r[i]], all loads under way
+// together.
+template <int N>
+__device__ __forceinline__ void source_rows(const Groups &g, int (&r)[N]) {
+    if (!g.row_token) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = g.row_token[r[i]];
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = min(max(r[i], 0), g.T - 1);
 }
 
 // Gate and up projections of one hidden unit -> its activation, gate / (1 +

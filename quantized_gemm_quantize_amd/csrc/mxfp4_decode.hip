@@ -104,6 +104,11 @@ struct RawPair {
     }
 };
 
+// Waits for a register's load, and with it for the direct-to-LDS loads issued
+// before (loads return in order). The compiler's own wait for those is not
+// enough where some of the loads in flight are behind a branch.
+__device__ __forceinline__ void landed(uint32_t &v) { asm volatile("" : "+v"(v)::"memory"); }
+
 // One pair in flight: its scales (and activations that have no codes yet).
 template <int MT, int CT, int XD>
 struct Pair {
@@ -135,7 +140,7 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
         t = Tile{expert_of(slots, slot, grp.E), slot, slot + 1};
         xbase = slot / slots.top;
     } else {
-        t = find_tile<16 * MT>(grp, blockIdx.x / tiles_n);
+        t = find_tile<16 * MT>(grp, grp.offsets ? scan_groups<16 * MT>(grp, 0) : GroupScan{}, blockIdx.x / tiles_n);
     }
     if (t.e < 0) return;
     const int n0 = (blockIdx.x % tiles_n) * 16 * CT;
@@ -150,13 +155,14 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
     const int r16 = lane & 15, quarter = lane >> 4;
     if (weight) {
         const int lr = lane >> 3, lc = lane & 7;
-        int row[MT][2], srow[MT];
+        int row[3 * MT];  // per 16-row tile: the rows of this lane's two code loads, of its scales
 #pragma unroll
-        for (int m = 0; m < XT; ++m) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) row[m][h] = source_row(grp, t.m0 + min(16 * m + 8 * h + lr, rows - 1));
-            srow[m] = source_row(grp, t.m0 + min(16 * m + r16, rows - 1));
+        for (int m = 0; m < MT; ++m) {
+            row[3 * m] = t.m0 + min(16 * m + lr, rows - 1);
+            row[3 * m + 1] = t.m0 + min(16 * m + 8 + lr, rows - 1);
+            row[3 * m + 2] = t.m0 + min(16 * m + r16, rows - 1);
         }
+        if constexpr (XD == kCodes) source_rows(grp, row);
         const uint8_t *wrow[CT][2], *xrow[MT][2], *wsc[CT], *xsc[MT];
         int chunk[2];
 #pragma unroll
@@ -166,13 +172,13 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
             for (int c = 0; c < CT; ++c)
                 wrow[c][h] = wq + ((int64_t)t.e * N + min(n0 + 16 * c + 8 * h + lr, N - 1)) * (K / 2);
 #pragma unroll
-            for (int m = 0; m < XT; ++m) xrow[m][h] = xq + (int64_t)row[m][h] * (K / 2);
+            for (int m = 0; m < XT; ++m) xrow[m][h] = xq + (int64_t)row[3 * m + h] * (K / 2);
         }
 #pragma unroll
         for (int c = 0; c < CT; ++c)
             wsc[c] = ws + ((int64_t)t.e * KB * N + min(n0 + 16 * c + r16, N - 1)) * 8 + 2 * quarter;
 #pragma unroll
-        for (int m = 0; m < XT; ++m) xsc[m] = xs + (int64_t)srow[m] * 8 + 2 * quarter;
+        for (int m = 0; m < XT; ++m) xsc[m] = xs + (int64_t)row[3 * m + 2] * 8 + 2 * quarter;
 
         auto load = [&](int p, uint4 *q, Pair<MT, CT, XD> &s) {
             uint4 *mine = q + wave * (XT + CT) * 128;
@@ -180,14 +186,7 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
 #pragma unroll
             for (int h = 0; h < 2; ++h)  // a chunk past K: the pair's first one
                 at[h] = p * kStepBytes + (p * kStepBytes + chunk[h] * 16 < K / 2 ? chunk[h] * 16 : 0);
-            if constexpr (XD == kCodes) {
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        __builtin_amdgcn_global_load_lds((global_void *)(xrow[m][h] + at[h]),
-                                                         (lds_void *)(mine + 128 * m + 64 * h), 16, 0, 0);
-            } else {
+            if constexpr (XD != kCodes) {
                 // before the weights: it lands first, and is quantized while they travel
                 constexpr int kPer = XD == kF32 ? 4 : 8;  // elements per load
                 const int k = p * kStep + 64 * quarter;
@@ -205,12 +204,21 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
                                                      (lds_void *)(mine + 128 * (XT + c) + 64 * h), 16, 0,
                                                      w8a8::kLdsLoadStream);
 #pragma unroll
+            for (int m = 0; m < XT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    __builtin_amdgcn_global_load_lds((global_void *)(xrow[m][h] + at[h]),
+                                                     (lds_void *)(mine + 128 * m + 64 * h), 16, 0, 0);
+            asm volatile("" ::: "memory");  // the scales' loads stay behind these
+#pragma unroll
             for (int m = 0; m < XT; ++m) s.sx[m] = *reinterpret_cast<const uint16_t *>(xsc[m] + (int64_t)p * grp.T * 8);
 #pragma unroll
             for (int c = 0; c < CT; ++c) s.sw[c] = *reinterpret_cast<const uint16_t *>(wsc[c] + (int64_t)p * N * 8);
         };
-        auto multiply = [&](const uint4 *q, const Pair<MT, CT, XD> &s) {
+        auto multiply = [&](const uint4 *q, Pair<MT, CT, XD> &s) {
             const uint4 *mine = q + wave * (XT + CT) * 128;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) landed(s.sw[c]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int slot = (r16 >> 3) * 64 + (r16 & 7) * 8 + ((2 * quarter + u) ^ (r16 & 7) ^ (r16 >> 3));
@@ -322,9 +330,11 @@ __global__ __launch_bounds__(kDownWaves *kWave) void down_combine_kernel(
     const uint8_t *__restrict__ hq, const uint8_t *__restrict__ hs, const uint8_t *__restrict__ wq,
     const uint8_t *__restrict__ ws, Ids slots, const float *__restrict__ weights, int S, int E, int N,
     int K, int KB, int tiles_n, void *__restrict__ out) {
-    __shared__ uint4 q0[kDownWaves * 128], q1[kDownWaves * 128];
+    __shared__ uint4 q0[kDownWaves * 128], q1[kDownWaves * 128], q2[kDownWaves * 128], q3[kDownWaves * 128];
     w8a8::lds_poison(q0);
     w8a8::lds_poison(q1);
+    w8a8::lds_poison(q2);
+    w8a8::lds_poison(q3);
     w8a8::lds_poison_done();
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -332,6 +342,12 @@ __global__ __launch_bounds__(kDownWaves *kWave) void down_combine_kernel(
     const int n0 = (blockIdx.x % tiles_n) * 16;  // N is a multiple of 16
     const int r16 = lane & 15, quarter = lane >> 4, lr = lane >> 3, lc = lane & 7;
 
+    // lane j: slot j's expert and weight (a load of its own in each item's chain
+    // would wait for all loads before it)
+    const int64_t own = token * slots.top + min(lane, slots.top - 1);
+    uint32_t slot_weight = __float_as_uint(weights[own]);
+    const int slot_expert = expert_of(slots, own, E);
+    landed(slot_weight);
     struct Item {
         uint32_t sw, sx;
         uint4 x[2];
@@ -341,16 +357,14 @@ __global__ __launch_bounds__(kDownWaves *kWave) void down_combine_kernel(
     auto load = [&](int item, uint4 *q, Item &s) {
         const int j = item / KB, p = item % KB;
         const int64_t slot = token * slots.top + j;
-        const int e = __builtin_amdgcn_readfirstlane(expert_of(slots, slot, E));
+        const int e = __builtin_amdgcn_readlane(slot_expert, j);
         s.live = e < E;
         if (!s.live) return;
-        s.weight = weights[slot];
-        // one row of activations: the lanes of the other fifteen hold zeros
-        const int k16 = p * 8 + 2 * quarter;  // 16-byte chunks along K
-        const uint4 *x = reinterpret_cast<const uint4 *>(hq + slot * (K / 2)) + k16;
+        s.weight = __uint_as_float(__builtin_amdgcn_readlane(slot_weight, j));
+        const int k16 = p * 8 + 2 * quarter;  // 16-byte chunks along K; one past K: the row's first
+        const uint4 *x = reinterpret_cast<const uint4 *>(hq + slot * (K / 2));
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-            s.x[u] = r16 == 0 && (k16 + u) * 16 < K / 2 ? x[u] : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < 2; ++u) s.x[u] = x[(k16 + u) * 16 < K / 2 ? k16 + u : 0];
         s.sx = *reinterpret_cast<const uint16_t *>(hs + ((int64_t)p * S + slot) * 8 + 2 * quarter);
         uint4 *mine = q + wave * 128;
 #pragma unroll
@@ -360,31 +374,41 @@ __global__ __launch_bounds__(kDownWaves *kWave) void down_combine_kernel(
             __builtin_amdgcn_global_load_lds((global_void *)(wq + ((int64_t)e * N + n0 + 8 * h + lr) * (K / 2) + at),
                                              (lds_void *)(mine + 64 * h), 16, 0, w8a8::kLdsLoadStream);
         }
+        asm volatile("" ::: "memory");  // the scale's load stays behind these
         s.sw = *reinterpret_cast<const uint16_t *>(ws + (((int64_t)e * KB + p) * N + n0 + r16) * 8 + 2 * quarter);
     };
     v4f sum = {};
-    auto multiply = [&](const uint4 *q, const Item &s) {
+    auto multiply = [&](const uint4 *q, Item &s) {
         if (!s.live) return;
         const uint4 *mine = q + wave * 128;
+        landed(s.sw);
         v4f acc = {};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int slot = (r16 >> 3) * 64 + (r16 & 7) * 8 + ((2 * quarter + u) ^ (r16 & 7) ^ (r16 >> 3));
-            acc = mfma_16x16x128(u, __builtin_bit_cast(v4i, mine[slot]), s.sw, __builtin_bit_cast(v4i, s.x[u]), s.sx, acc);
+            // one row of activations: the lanes of the other fifteen hold zeros
+            const v4i x = r16 == 0 ? __builtin_bit_cast(v4i, s.x[u]) : v4i{};
+            acc = mfma_16x16x128(u, __builtin_bit_cast(v4i, mine[slot]), s.sw, x, s.sx, acc);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] += s.weight * acc[i];
     };
     const int items = slots.top * KB;
-    Item s0{}, s1{};
+    Item s0{}, s1{}, s2{}, s3{};
     int i = wave;
     if (i < items) load(i, q0, s0);
     if (i + kDownWaves < items) load(i + kDownWaves, q1, s1);
-    for (; i < items; i += 2 * kDownWaves) {
+    if (i + 2 * kDownWaves < items) load(i + 2 * kDownWaves, q2, s2);
+    if (i + 3 * kDownWaves < items) load(i + 3 * kDownWaves, q3, s3);
+    for (; i < items; i += 4 * kDownWaves) {
         multiply(q0, s0);
-        if (i + 2 * kDownWaves < items) load(i + 2 * kDownWaves, q0, s0);
+        if (i + 4 * kDownWaves < items) load(i + 4 * kDownWaves, q0, s0);
         if (i + kDownWaves < items) multiply(q1, s1);
-        if (i + 3 * kDownWaves < items) load(i + 3 * kDownWaves, q1, s1);
+        if (i + 5 * kDownWaves < items) load(i + 5 * kDownWaves, q1, s1);
+        if (i + 2 * kDownWaves < items) multiply(q2, s2);
+        if (i + 6 * kDownWaves < items) load(i + 6 * kDownWaves, q2, s2);
+        if (i + 3 * kDownWaves < items) multiply(q3, s3);
+        if (i + 7 * kDownWaves < items) load(i + 7 * kDownWaves, q3, s3);
     }
     __syncthreads();  // every wavefront has read its last fragments
     v4f(*red)[4] = reinterpret_cast<v4f(*)[4]>(q0);

@@ -247,21 +247,25 @@ __device__ __forceinline__ void aim(Loads<Sh> &g, const Operands &op, const Grou
     g.none = Sources{buffer(a, 0), buffer(b, 0), buffer(sa, 0), buffer(sb, 0)};
     g.sa_step = grp.T * 8;
     g.sb_step = N * 8;
-    auto a_row = [&](int r) -> uint32_t {
-        r = min(r, rows - 1);
-        return grp.row_token ? (uint32_t)source_row(grp, tile.m0 + r) : (uint32_t)r;
-    };
     auto b_row = [&](int r) { return (uint32_t)min(r, N - n0 - 1); };
     constexpr int kPass = Sh::kRows * kWaves;  // rows from one code load to the next
-#pragma unroll
-    for (int l = 0; l < Sh::kA; ++l) g.aoff[l] = a_row(lrow + kPass * l) * (uint32_t)(K / 2) + g.kc * 16;
-#pragma unroll
-    for (int l = 0; l < Sh::kB; ++l) g.boff[l] = b_row(lrow + kPass * l) * (uint32_t)(K / 2) + g.kc * 16;
     // scale words: CH = 8, lane l of a fragment: row l % 32, word l / 32; CH = 4, row l
     const int srow = CH == 8 ? lane & 31 : lane, sword = CH == 8 ? 4 * (lane >> 5) : 0;
+    int a_row[Sh::kA + Sh::kSA];
+#pragma unroll
+    for (int l = 0; l < Sh::kA; ++l) a_row[l] = lrow + kPass * l;
 #pragma unroll
     for (int q = 0; q < Sh::kSA; ++q)
-        g.saoff[q] = a_row((wave + kWaves * q) % (Sh::kBM / Sh::kScaleRows) * Sh::kScaleRows + srow) * 8 + sword;
+        a_row[Sh::kA + q] = (wave + kWaves * q) % (Sh::kBM / Sh::kScaleRows) * Sh::kScaleRows + srow;
+#pragma unroll
+    for (int &r : a_row) r = min(r, rows - 1) + (grp.row_token ? tile.m0 : 0);
+    source_rows(grp, a_row);
+#pragma unroll
+    for (int l = 0; l < Sh::kB; ++l) g.boff[l] = b_row(lrow + kPass * l) * (uint32_t)(K / 2) + g.kc * 16;
+#pragma unroll
+    for (int l = 0; l < Sh::kA; ++l) g.aoff[l] = (uint32_t)a_row[l] * (uint32_t)(K / 2) + g.kc * 16;
+#pragma unroll
+    for (int q = 0; q < Sh::kSA; ++q) g.saoff[q] = (uint32_t)a_row[Sh::kA + q] * 8 + sword;
 #pragma unroll
     for (int q = 0; q < Sh::kSB; ++q)
         g.sboff[q] = b_row((wave + kWaves * q) % (Sh::kBN / Sh::kScaleRows) * Sh::kScaleRows + srow) * 8 + sword;
@@ -270,8 +274,16 @@ __device__ __forceinline__ void aim(Loads<Sh> &g, const Operands &op, const Grou
 template <typename Sh, bool KTAIL>
 __device__ __forceinline__ void load_stage(const Loads<Sh> &g, int j, uint4 *st, int wave) {
     const Sources src = g.at(j);
+    // the weight's first: the activations' addresses may still be on their way
+    constexpr int kA = Sh::kA, kW = Sh::kA + Sh::kB, kSA = kW + Sh::kSA;
 #pragma unroll
-    for (int l = 0; l < Sh::kLoads; ++l) load_one<Sh, KTAIL>(g, src, l, j, st, wave);
+    for (int l = kA; l < kW; ++l) load_one<Sh, KTAIL>(g, src, l, j, st, wave);
+#pragma unroll
+    for (int l = kSA; l < Sh::kLoads; ++l) load_one<Sh, KTAIL>(g, src, l, j, st, wave);
+#pragma unroll
+    for (int l = 0; l < kA; ++l) load_one<Sh, KTAIL>(g, src, l, j, st, wave);
+#pragma unroll
+    for (int l = kW; l < kSA; ++l) load_one<Sh, KTAIL>(g, src, l, j, st, wave);
 }
 
 // Waits for this wavefront's vector-memory operations (vmcnt 0 only).
@@ -358,18 +370,22 @@ __global__ __launch_bounds__(GM *GN *kWave, OCC *GM *GN / 4) void tiled_kernel(
     const int a_scale = wm * (WM / 32) * kSc + sl, b_scale = (BM / 32 + wn * (WN / 32)) * kSc + sl;
     const int fswz = swz<CH>(frag_row);
 
-    if (grp.offsets) tiles_m = count_tiles<BM>(grp);
+    GroupScan scan{};
+    if (grp.offsets) {
+        scan = scan_groups<BM>(grp, 0);
+        tiles_m = count_tiles<BM>(grp, scan);
+    }
     const int tiles = tiles_m * tiles_n;
     // tiles XCD by XCD, in groups of 4 tile rows, so that concurrent tiles
     // share activation and weight rows in one L2
-    auto locate = [&](int pid, int &n0) {
+    auto locate = [&](const GroupScan &scan, int pid, int &n0) {
         constexpr int kGroupM = 4;
         const int t = w8a8::xcd_contiguous(pid, tiles);
         const int per_group = kGroupM * tiles_n;
         const int first_m = (t / per_group) * kGroupM;
         const int gsize = min(tiles_m - first_m, kGroupM);
         n0 = ((t % per_group) / gsize) * BN;
-        return find_tile<BM>(grp, first_m + (t % per_group) % gsize);
+        return find_tile<BM>(grp, scan, first_m + (t % per_group) % gsize);
     };
     int pid = blockIdx.x;
     if (pid >= tiles) return;
@@ -381,7 +397,7 @@ __global__ __launch_bounds__(GM *GN *kWave, OCC *GM *GN / 4) void tiled_kernel(
     if (!PERSIST && pid < slots && tiles > 2 * slots)
         for (int wait = pid / 8 % 32; wait > 0; --wait) __builtin_amdgcn_s_sleep(8);
     int n0;
-    Tile tile = locate(pid, n0);
+    Tile tile = locate(scan, pid, n0);
     Loads<Sh> g;
     int first = 0;  // buffer of the first stage
     auto start = [&] {
@@ -458,7 +474,8 @@ __global__ __launch_bounds__(GM *GN *kWave, OCC *GM *GN / 4) void tiled_kernel(
         // all fragment reads done, and (empty) loads landed: the buffers are free
         vm_barrier<0>();
         if (more) {
-            tile = locate(pid, n0);
+            // (scanned again: kept, it would cost three registers)
+            tile = locate(grp.offsets ? scan_groups<BM>(grp, 0) : GroupScan{}, pid, n0);
             start();
         }
         if (done.e >= 0) {
