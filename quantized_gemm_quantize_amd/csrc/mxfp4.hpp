@@ -141,11 +141,17 @@ __device__ __forceinline__ int count_tiles(const Groups &g, const GroupScan &fir
     return total;
 }
 
-// Tile t of the groups' rows cut into tiles of BM rows, group after group, 64
-// groups at a time.
+// The group that holds tile t of the groups' rows cut into tiles of BM rows,
+// group after group, 64 groups at a time.
+struct Group {
+    int e;      // E for the rows without a weight, -1 past the last tile
+    int lo, n;  // first row, rows
+    int first;  // its first tile
+};
+
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const Groups &g, const GroupScan &first, int t) {
-    if (!g.offsets) return Tile{t * BM < g.S ? 0 : -1, t * BM, g.S};
+__device__ __forceinline__ Group find_group(const Groups &g, const GroupScan &first, int t) {
+    if (!g.offsets) return Group{t * BM < g.S ? 0 : -1, 0, g.S, 0};
     GroupScan s = first;
     int before = 0;
     for (int base = 0; base <= g.E; base += kWave) {
@@ -154,12 +160,11 @@ __device__ __forceinline__ Tile find_tile(const Groups &g, const GroupScan &firs
         if (hit) {
             const int l = __builtin_ctzll(hit);
             const int lo = __builtin_amdgcn_readlane(s.lo, l), n = __builtin_amdgcn_readlane(s.n, l);
-            const int first_t = before + __builtin_amdgcn_readlane(s.upto, l) - (n + BM - 1) / BM;
-            return Tile{base + l, lo + (t - first_t) * BM, lo + n};
+            return Group{base + l, lo, n, before + __builtin_amdgcn_readlane(s.upto, l) - (n + BM - 1) / BM};
         }
         before += __builtin_amdgcn_readlane(s.upto, kWave - 1);
     }
-    return Tile{-1, 0, 0};
+    return Group{-1, 0, 0, 0};
 }
 
 // Most tiles of BM rows that S rows in E groups (and the rows without a

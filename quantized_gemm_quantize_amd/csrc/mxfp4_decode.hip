@@ -140,7 +140,9 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
         t = Tile{expert_of(slots, slot, grp.E), slot, slot + 1};
         xbase = slot / slots.top;
     } else {
-        t = find_tile<16 * MT>(grp, grp.offsets ? scan_groups<16 * MT>(grp, 0) : GroupScan{}, blockIdx.x / tiles_n);
+        const int tile = blockIdx.x / tiles_n;
+        const Group own = find_group<16 * MT>(grp, grp.offsets ? scan_groups<16 * MT>(grp, 0) : GroupScan{}, tile);
+        t = Tile{own.e, own.lo + (tile - own.first) * 16 * MT, own.lo + own.n};
     }
     if (t.e < 0) return;
     const int n0 = (blockIdx.x % tiles_n) * 16 * CT;

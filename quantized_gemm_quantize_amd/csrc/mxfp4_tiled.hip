@@ -376,16 +376,19 @@ __global__ __launch_bounds__(GM *GN *kWave, OCC *GM *GN / 4) void tiled_kernel(
         tiles_m = count_tiles<BM>(grp, scan);
     }
     const int tiles = tiles_m * tiles_n;
-    // tiles XCD by XCD, in groups of 4 tile rows, so that concurrent tiles
-    // share activation and weight rows in one L2
+    // Tiles XCD by XCD, a group's tiles after another's, in parts of up to kPart
+    // tile rows by all columns: the tiles that run at once share activation and
+    // weight rows in one L2.
     auto locate = [&](const GroupScan &scan, int pid, int &n0) {
-        constexpr int kGroupM = 4;
+        constexpr int kPart = 6;
         const int t = w8a8::xcd_contiguous(pid, tiles);
-        const int per_group = kGroupM * tiles_n;
-        const int first_m = (t / per_group) * kGroupM;
-        const int gsize = min(tiles_m - first_m, kGroupM);
-        n0 = ((t % per_group) / gsize) * BN;
-        return find_tile<BM>(grp, scan, first_m + (t % per_group) % gsize);
+        const Group own = find_group<BM>(grp, scan, t / tiles_n);
+        const int rows = (own.n + BM - 1) / BM, parts = (rows + kPart - 1) / kPart;
+        const int per_part = (rows + parts - 1) / parts, in_group = t - own.first * tiles_n;
+        const int m = in_group / (per_part * tiles_n) * per_part, in_part = in_group % (per_part * tiles_n);
+        const int part = min(rows - m, per_part);
+        n0 = in_part / part * BN;
+        return Tile{own.e, own.lo + (m + in_part % part) * BM, own.lo + own.n};
     };
     int pid = blockIdx.x;
     if (pid >= tiles) return;
