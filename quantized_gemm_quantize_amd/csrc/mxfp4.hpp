@@ -181,7 +181,6 @@ inline int64_t most_tiles(int64_t S, int64_t E, int BM, bool grouped) {
 // together.
 template <int N>
 __device__ __forceinline__ void source_rows(const Groups &g, int (&r)[N]) {
-    if (!g.row_token) return;
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = g.row_token[r[i]];
 #pragma unroll

@@ -164,7 +164,7 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
             row[3 * m + 1] = t.m0 + min(16 * m + 8 + lr, rows - 1);
             row[3 * m + 2] = t.m0 + min(16 * m + r16, rows - 1);
         }
-        if constexpr (XD == kCodes) source_rows(grp, row);
+        if (XD == kCodes && grp.row_token) source_rows(grp, row);
         const uint8_t *wrow[CT][2], *xrow[MT][2], *wsc[CT], *xsc[MT];
         int chunk[2];
 #pragma unroll

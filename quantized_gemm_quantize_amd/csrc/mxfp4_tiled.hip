@@ -16,8 +16,8 @@
 //    of row r sits at slot c ^ swz(r), which keeps the 16-byte fragment reads
 //    free of bank conflicts. Scales lie as 32-bit words: CH = 8, one per lane of a
 //    32-row fragment; CH = 4, one per row, read by both halves.
-//  - Rows past the group or N are read from the last valid row (their outputs
-//    are never stored). Blocks past K are read from inside the row; both sides'
+//  - Codes of rows past the group or N are not read (they are 0; the scales are
+//    the last valid row's), and the outputs are never stored. Blocks past K are read from inside the row; both sides'
 //    scale codes there are the storage's padding 0, so that each product is
 //    below 2^-240 and adds nothing in fp32.
 //  - Rows grouped by expert read their activation row through row_token, so no
@@ -232,6 +232,7 @@ template <typename Sh>
 __device__ __forceinline__ void aim(Loads<Sh> &g, const Operands &op, const Groups &grp,
                                     const Tile &tile, int n0, int N, int K, int KB, int lane, int wave) {
     constexpr int CH = Sh::kCH, kWaves = Sh::kWaves;
+    asm volatile("" : "+v"(lane));  // or a persistent kernel keeps the row numbers in registers
     const int lrow = Sh::kRows * wave + lane / CH;
     g.kc = (lane % CH) ^ swz<CH>(lrow);
     g.half_k = K / 2;
@@ -242,33 +243,43 @@ __device__ __forceinline__ void aim(Loads<Sh> &g, const Operands &op, const Grou
     const int64_t half_k = K / 2, first_n = (int64_t)tile.e * N + n0;
     const uint8_t *a = op.xq + row0 * half_k, *b = op.wq + first_n * half_k, *sa = op.xs + row0 * 8,
                   *sb = op.ws + ((int64_t)tile.e * KB * N + n0) * 8;
-    g.src = Sources{buffer(a, (grp.T - row0) * half_k), buffer(b, (N - n0) * half_k),
+    // codes of rows past the group's or the weight's end are past these ends: no memory is read
+    g.src = Sources{buffer(a, (grp.row_token ? grp.T : rows) * half_k), buffer(b, (N - n0) * half_k),
                     buffer(sa, ((int64_t)KB * grp.T - row0) * 8), buffer(sb, ((int64_t)KB * N - n0) * 8)};
     g.none = Sources{buffer(a, 0), buffer(b, 0), buffer(sa, 0), buffer(sb, 0)};
     g.sa_step = grp.T * 8;
     g.sb_step = N * 8;
-    auto b_row = [&](int r) { return (uint32_t)min(r, N - n0 - 1); };
     constexpr int kPass = Sh::kRows * kWaves;  // rows from one code load to the next
     // scale words: CH = 8, lane l of a fragment: row l % 32, word l / 32; CH = 4, row l
     const int srow = CH == 8 ? lane & 31 : lane, sword = CH == 8 ? 4 * (lane >> 5) : 0;
-    int a_row[Sh::kA + Sh::kSA];
+    auto scale_row = [&](int q, int side, int end) {
+        return min((wave + kWaves * q) % (side / Sh::kScaleRows) * Sh::kScaleRows + srow, end - 1);
+    };
+    int a_row[Sh::kA], s_row[Sh::kSA];
 #pragma unroll
     for (int l = 0; l < Sh::kA; ++l) a_row[l] = lrow + kPass * l;
 #pragma unroll
-    for (int q = 0; q < Sh::kSA; ++q)
-        a_row[Sh::kA + q] = (wave + kWaves * q) % (Sh::kBM / Sh::kScaleRows) * Sh::kScaleRows + srow;
+    for (int q = 0; q < Sh::kSA; ++q) s_row[q] = scale_row(q, Sh::kBM, rows);
+    if (grp.row_token) {
+        int token[Sh::kA + Sh::kSA];
 #pragma unroll
-    for (int &r : a_row) r = min(r, rows - 1) + (grp.row_token ? tile.m0 : 0);
-    source_rows(grp, a_row);
+        for (int l = 0; l < Sh::kA; ++l) token[l] = tile.m0 + min(a_row[l], rows - 1);
 #pragma unroll
-    for (int l = 0; l < Sh::kB; ++l) g.boff[l] = b_row(lrow + kPass * l) * (uint32_t)(K / 2) + g.kc * 16;
+        for (int q = 0; q < Sh::kSA; ++q) token[Sh::kA + q] = tile.m0 + s_row[q];
+        source_rows(grp, token);
+#pragma unroll
+        for (int l = 0; l < Sh::kA; ++l) a_row[l] = a_row[l] < rows ? token[l] : grp.T;
+#pragma unroll
+        for (int q = 0; q < Sh::kSA; ++q) s_row[q] = token[Sh::kA + q];
+    }
 #pragma unroll
     for (int l = 0; l < Sh::kA; ++l) g.aoff[l] = (uint32_t)a_row[l] * (uint32_t)(K / 2) + g.kc * 16;
 #pragma unroll
-    for (int q = 0; q < Sh::kSA; ++q) g.saoff[q] = (uint32_t)a_row[Sh::kA + q] * 8 + sword;
+    for (int l = 0; l < Sh::kB; ++l) g.boff[l] = (uint32_t)(lrow + kPass * l) * (uint32_t)(K / 2) + g.kc * 16;
 #pragma unroll
-    for (int q = 0; q < Sh::kSB; ++q)
-        g.sboff[q] = b_row((wave + kWaves * q) % (Sh::kBN / Sh::kScaleRows) * Sh::kScaleRows + srow) * 8 + sword;
+    for (int q = 0; q < Sh::kSA; ++q) g.saoff[q] = (uint32_t)s_row[q] * 8 + sword;
+#pragma unroll
+    for (int q = 0; q < Sh::kSB; ++q) g.sboff[q] = (uint32_t)scale_row(q, Sh::kBN, N - n0) * 8 + sword;
 }
 
 template <typename Sh, bool KTAIL>
