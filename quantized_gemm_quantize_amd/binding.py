@@ -444,7 +444,7 @@ def _check(t, name, dtype, ndim):
 def _result(t, name, shape, dtype, like):
     """`t` checked, or a new tensor on `like`'s device."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(*shape, dtype=dtype, device=like.device)  # the quickest form
     _check(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -455,7 +455,7 @@ def _scratch(workspace, need, like, stream):
     """(address, bytes) of a workspace of `need` bytes: the caller's, or a new one that the caching
     allocator keeps until `stream` has run what is queued on it."""
     if workspace is None:
-        workspace = like.new_empty((need,), dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
         if stream is not None:
             workspace.record_stream(stream)
         return workspace.data_ptr(), need
