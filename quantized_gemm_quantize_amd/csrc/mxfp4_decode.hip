@@ -5,11 +5,11 @@
 // once. A workgroup owns 16 CT channels of one group's weight and up to 16 MT
 // of its rows; its WAVES wavefronts split K in pairs of 128 bytes of codes (256
 // elements), wavefront w taking pairs w, w + WAVES, ..., so that neighbouring
-// wavefronts read neighbouring cache lines. Measured,
-// least and median of 15: 1 x 4096 x 4096 (8.9 MB) 5.6 and 6.6 us; 32 experts' gate and
-// up [4096, 4096] for 64 tokens (285 MB) 44 and 56 us, 6.5 and 5.1 TB/s; their down
-// products (142 MB) 24.5 and 29 us; one token's four experts 9.2 and 6.5 us (36 and 18
-// MB), where the start and the end of one workgroup per CU show.
+// wavefronts read neighbouring cache lines. Measured: 1 x 4096 x 4096 (8.9
+// MB) 4.0 us back to back, 5.5 alone; 32 experts' gate and up [4096, 4096] for 64 tokens
+// (285 MB) 44-48 us, 6.5-5.9 TB/s; their down products (142 MB) 24.5-26.5 us; one token's
+// four experts 9.2 and 4.5 us (36 and 18 MB), where the start and the end of one
+// workgroup per CU show.
 //
 //  - Codes of weights and activations travel global -> LDS with 16-byte
 //    direct-to-LDS loads of 8 whole lines each, two pairs in flight per
@@ -108,6 +108,13 @@ struct RawPair {
 // before (loads return in order). The compiler's own wait for those is not
 // enough where some of the loads in flight are behind a branch.
 __device__ __forceinline__ void landed(uint32_t &v) { asm volatile("" : "+v"(v)::"memory"); }
+
+// Waits for this wavefront's LDS reads: a buffer may then be filled again.
+__device__ __forceinline__ void fragments_read() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));  // lgkmcnt 0
+    asm volatile("" ::: "memory");
+}
 
 // One pair in flight: its scales (and activations that have no codes yet).
 template <int MT, int CT, int XD>
@@ -248,8 +255,10 @@ __global__ __launch_bounds__(WAVES *kWave) void decode_kernel(
         if (p + WAVES < KB) load(p + WAVES, q1, s1);
         for (; p < KB; p += 2 * WAVES) {
             multiply(q0, s0);
+            fragments_read();
             if (p + 2 * WAVES < KB) load(p + 2 * WAVES, q0, s0);
             if (p + WAVES < KB) multiply(q1, s1);
+            fragments_read();
             if (p + 3 * WAVES < KB) load(p + 3 * WAVES, q1, s1);
         }
     }
@@ -404,12 +413,16 @@ __global__ __launch_bounds__(kDownWaves *kWave) void down_combine_kernel(
     if (i + 3 * kDownWaves < items) load(i + 3 * kDownWaves, q3, s3);
     for (; i < items; i += 4 * kDownWaves) {
         multiply(q0, s0);
+        fragments_read();
         if (i + 4 * kDownWaves < items) load(i + 4 * kDownWaves, q0, s0);
         if (i + kDownWaves < items) multiply(q1, s1);
+        fragments_read();
         if (i + 5 * kDownWaves < items) load(i + 5 * kDownWaves, q1, s1);
         if (i + 2 * kDownWaves < items) multiply(q2, s2);
+        fragments_read();
         if (i + 6 * kDownWaves < items) load(i + 6 * kDownWaves, q2, s2);
         if (i + 3 * kDownWaves < items) multiply(q3, s3);
+        fragments_read();
         if (i + 7 * kDownWaves < items) load(i + 7 * kDownWaves, q3, s3);
     }
     __syncthreads();  // every wavefront has read its last fragments

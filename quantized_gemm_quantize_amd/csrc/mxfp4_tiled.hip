@@ -28,14 +28,15 @@
 //    16-byte pieces of contiguous rows; SwiGLU joins gate and up in registers
 //    and stores the hidden activations as MXFP4, 17/64 of their bf16 bytes.
 //
-// What bounds it (8192 x 8192, by K): a 256 x 256 tile's K stage takes 1.6 us,
-// 5.3 PFLOP/s over the chip, where the MFMA loop alone reaches 5.3-6.5 (its clock
-// falls under the load). Alone, a stage's 68 KB of operands take 1.27 us: 64
-// reads of 128 bytes in flight per CU at a latency of about 300 clocks, 27 bytes
-// per clock, whatever the address pattern; so a tile with more products per byte
-// is faster until too few tiles are left (see the choice at the end). Around its
-// stages a tile costs about 8 us more: its first loads, and the stores of a
-// plain output or the exponentials of SwiGLU.
+// What bounds it (8192 x 8192, by K): 20 us for the stores (134 MB, 6.7 TB/s) and
+// the starts, and 1.6 us for each K stage of the 256 x 256 tiles, 5.1 PFLOP/s over
+// the chip, where the MFMA loop alone reaches 5.3-6.5 (its clock falls under the
+// load). Alone, a stage's 68 KB of operands take 1.27 us: 64 reads of 128 bytes
+// in flight per CU at a latency of about 300 clocks, 27 bytes per clock, whatever
+// the address pattern; so a tile with more products per byte is faster until
+// too few tiles are left (see the choice at the end). 2048 x 4096 x 4096 20 us, 38400
+// x 4096 x 1024 119 us, 32 experts' gate and up of 8192 tokens x 4 302 us, their
+// down products 167 us.
 #include <algorithm>
 
 #include "launch.hpp"
@@ -567,9 +568,9 @@ hipError_t launch_gemm_tiled(const uint8_t *xq, const uint8_t *xs, const uint8_t
     // 16.4, 14.6, 12.4, 15.3, 26.5; M = 1536 28.1, 23.4, 24.1, 17.5, 27.6; M = 4096
     // 68.5, 54.4, 49.5, 47.5, 36.1.
     // Short K: two workgroups of 256 x 128 per CU with 128-element stages, whose
-    // starts and stores overlap each other's products (8192 x 8192, K = 512 47.6 ->
-    // 44.1 us, K = 1024 61.3 -> 56.2, K = 2048 86.6 -> 90.5; 32 experts' gate and up
-    // [2944, 960] with 285 rows each 42.1 -> 36.4).
+    // starts and stores overlap each other's products (8192 x 8192, against 256 x
+    // 256: K = 512 43.3 -> 39.2 us, K = 1024 56.0 -> 56.3, K = 2048 81.4 -> 89.6; 32
+    // experts' gate and up [2944, 960] with 285 rows each 41.3 -> 35.4).
     // Small groups: 64 rows, as a taller tile is mostly empty (32 experts with 64
     // rows each: gate and up [4096, 4096] 82.1 -> 77.5, down [4096, 2048] 45.1 -> 38.9;
     // with 256 rows 111 -> 152 and 63 -> 82).
