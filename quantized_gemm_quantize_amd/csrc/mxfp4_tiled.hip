@@ -17,9 +17,9 @@
 //    free of bank conflicts. Scales lie as 32-bit words: CH = 8, one per lane of a
 //    32-row fragment; CH = 4, one per row, read by both halves.
 //  - Codes of rows past the group or N are not read (they are 0; the scales are
-//    the last valid row's), and the outputs are never stored. Blocks past K are read from inside the row; both sides'
-//    scale codes there are the storage's padding 0, so that each product is
-//    below 2^-240 and adds nothing in fp32.
+//    the last valid row's), and the outputs are never stored. Blocks past K are
+//    read from inside the row; both sides' scale codes there are the storage's
+//    padding 0, so that each product is below 2^-240 and adds nothing in fp32.
 //  - Rows grouped by expert read their activation row through row_token, so no
 //    sorted copy of the activations exists. A wavefront whose rows lie past the
 //    group's end only loads.
