@@ -34,14 +34,16 @@ __device__ __forceinline__ Hidden quantize_swiglu(const v16f &lo, const v16f &hi
 #pragma unroll
     for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int u = 0; u < 8; u += 4) {
+            const v16f &a = jj ? hi : lo;
+            const v4f v = swiglu4(v4f{a[2 * u], a[2 * u + 2], a[2 * u + 4], a[2 * u + 6]},
+                                  v4f{a[2 * u + 1], a[2 * u + 3], a[2 * u + 5], a[2 * u + 7]});
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const v16f &a = jj ? hi : lo;
-                const float v = swiglu(a[4 * g + 2 * p], a[4 * g + 2 * p + 1]);
-                h[jj][2 * g + p] = v;
-                top = max(top, __float_as_uint(v) & 0x7FFFFFFFu);
+            for (int i = 0; i < 4; ++i) {
+                h[jj][u + i] = v[i];
+                top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
             }
+        }
     top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
     const uint32_t code = scale_code(__uint_as_float(top));
     const float scale = scale_value(code);
