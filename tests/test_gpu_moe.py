@@ -369,3 +369,28 @@ def test_refusals():
         b.mxfp4_expert_swiglu(yq, ys, offsets, wq[None, :48].contiguous(), ws[None, :, :48].contiguous())
     with pytest.raises(ValueError):
         b.mxfp4_moe(x, ids, w, wq[None], ws[None], wq[None], ws[None])   # w2 is not [H, F]
+
+
+@pytest.mark.parametrize("T,top,E,H,F", [(1, 1, 2, 64, 2080), (1, 3, 4, 96, 800), (2, 4, 6, 160, 544), (1, 5, 8, 320, 1056),
+                                         (1, 8, 8, 1056, 2080), (8, 1, 3, 32, 1312), (4, 2, 5, 2080, 288)])
+@pytest.mark.parametrize("drop", [0.0, 0.4])
+def test_few_slots_of_every_depth(T, top, E, H, F, drop):
+    """The layer of a few slots with one to nine items of K per wavefront and more, slots without an
+    expert between them: as in 64 bits (bound as above), and the same bits in every run."""
+    ids = torch.from_numpy(routing(T, top, E, seed=H + T, drop=drop)).to(DEV)
+    weights = torch.rand((T, top), generator=torch.Generator().manual_seed(1)).to(DEV)
+    x, x64 = rows(T, H, "f32", seed=2, spread=0.5)
+    w13 = [packed(2 * F, H, seed=10 + e, lo=119, hi=123) for e in range(E)]
+    w2 = [packed(H, F, seed=50 + e, lo=119, hi=123) for e in range(E)]
+    stacks = [torch.stack([w[i] for w in ws]) for ws in (w13, w2) for i in (0, 1)]
+    runs = [b.mxfp4_moe(x, ids, weights, *stacks) for _ in range(20)]
+    assert all(torch.equal(runs[0], r) for r in runs[1:])
+    xv = ref.values(*ref.quantize(x64))
+    want = np.zeros((T, H))
+    for t, slots in enumerate(ids.tolist()):
+        for j, e in enumerate(slots):
+            if e >= 0:
+                h = ref.values(*ref.quantize(ref.swiglu(xv[t:t + 1] @ w13[e][2].T)))
+                want[t] += weights[t, j].item() * (h @ w2[e][2].T)[0]
+    err = np.linalg.norm(runs[0].double().cpu().numpy() - want)
+    assert err <= (2.0 ** -8 + 3 * HALF_ULP["f32"]) * np.linalg.norm(want)
