@@ -16,7 +16,7 @@
 // by HBM and go token by token, so that each token is read once. Measured, 16448
 // tokens x 4 slots x 4096 bf16: gather 121 us (674 MB, 5.6 TB/s), combine 111 (6.1),
 // its backward 230 (1.21 GB, 5.3), the gather's 110; the sort of the 65792 slots,
-// bound by the latency of its two launches, 16.
+// bound by the latency of its two launches, 11, of 16.8 million 128 (three launches).
 #include <type_traits>
 
 #include "launch.hpp"
@@ -37,6 +37,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kSortIters = 4;                               // slots per thread
 constexpr int kChunk = kSortThreads * kSortIters;           // slots per workgroup
+constexpr int kSums = 12;                                   // chunks that a thread sums, see sort_ids
 constexpr int kMaxBins = 513;                               // experts, and the dropped slots
 
 template <typename I>
@@ -93,25 +94,72 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(const I *__restrict
         counts[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
 }
 
+// Many chunks: workgroup e turns bin e's counts into the bin's slots in earlier
+// chunks, and leaves its slots in all chunks behind them (`counts` has chunks + 1
+// rows then).
+__global__ __launch_bounds__(kSortThreads) void scan_kernel(int32_t *__restrict__ counts, int chunks, int bins) {
+    __shared__ int wave_sum[kSortWaves];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    w8a8::lds_poison(wave_sum);
+    w8a8::lds_poison_done();
+    int before = 0;
+    for (int base = 0; base < chunks; base += kSortThreads) {
+        const int c = base + threadIdx.x;
+        int32_t *at = counts + (int64_t)c * bins + blockIdx.x;
+        const int own = c < chunks ? *at : 0;
+        int upto = own;
+#pragma unroll
+        for (int off = 1; off < kWave; off <<= 1) {
+            const int o = __shfl_up(upto, off, kWave);
+            if (lane >= off) upto += o;
+        }
+        if (lane == kWave - 1) wave_sum[wave] = upto;
+        __syncthreads();
+        int all = 0, earlier = before;
+        for (int w = 0; w < kSortWaves; ++w) {
+            if (w < wave) earlier += wave_sum[w];
+            all += wave_sum[w];
+        }
+        if (c < chunks) *at = earlier + upto - own;
+        before += all;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) counts[(int64_t)chunks * bins + blockIdx.x] = before;
+}
+
 // Places the slots of one chunk. Wavefront w owns slots [w * 64 * kSortIters,
 // +64 * kSortIters) of the chunk; a slot's row is the bin's first row, plus
 // the bin's slots in earlier chunks (counts), in earlier wavefronts, and
 // before it in its own wavefront (lane order within a match mask): the stable
-// order. With one chunk the counts are this workgroup's own.
-template <typename I, int QD>
+// order. With one chunk the counts are this workgroup's own, with several each
+// workgroup sums them, and with many the scan has (SCANNED).
+template <typename I, int QD, bool SCANNED>
 __global__ __launch_bounds__(kSortThreads) void place_kernel(
     const I *__restrict__ ids, int64_t S, int top, int E, int bits,
     const int32_t *__restrict__ counts, int chunks, int32_t *__restrict__ offsets,
     int32_t *__restrict__ slot_pos, int32_t *__restrict__ row_token, Rows q) {
     if (QD >= 0 && (int)blockIdx.x >= chunks) return quantize_beside<QD>(blockIdx.x - chunks, q);
-    extern __shared__ int hist[];  // [kSortWaves][E + 1] counts, then first rows
+    extern __shared__ int hist[];  // [kSortWaves][E + 1] counts, then first rows; [2][E + 1] sums over chunks
     __shared__ int wave_sum[kSortWaves];
     const int bins = E + 1;
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     w8a8::lds_poison(wave_sum);
     w8a8::lds_poison_done();
-    for (int i = threadIdx.x; i < kSortWaves * bins; i += kSortThreads) hist[i] = 0;
+    int *sums = hist + kSortWaves * bins;
+    for (int i = threadIdx.x; i < (kSortWaves + 2) * bins; i += kSortThreads) hist[i] = 0;
     __syncthreads();
+    if (!SCANNED && chunks > 1) {
+        // as many threads per bin as there are, each with every parts-th chunk
+        const int parts = kSortThreads / bins, b = threadIdx.x % bins;
+        int before = 0, all = 0;
+        for (int c = threadIdx.x / bins; c < chunks && threadIdx.x < parts * bins; c += parts) {
+            const int v = counts[(int64_t)c * bins + b];
+            if (c < (int)blockIdx.x) before += v;
+            all += v;
+        }
+        if (before) atomicAdd(&sums[b], before);  // integers: the order does not matter
+        if (all) atomicAdd(&sums[bins + b], all);
+    }
     int bin[kSortIters], before[kSortIters];
     const int64_t first = (int64_t)blockIdx.x * kChunk + wave * (kWave * kSortIters) + lane;
 #pragma unroll
@@ -138,13 +186,12 @@ __global__ __launch_bounds__(kSortThreads) void place_kernel(
             hist[w * bins + e] = total;
             total += c;
         }
-        if (chunks > 1) {
-            total = 0;
-            for (int c = 0; c < chunks; ++c) {
-                const int v = counts[(int64_t)c * bins + e];
-                if (c < (int)blockIdx.x) earlier += v;
-                total += v;
-            }
+        if constexpr (SCANNED) {
+            earlier = counts[(int64_t)blockIdx.x * bins + e];
+            total = counts[(int64_t)chunks * bins + e];
+        } else if (chunks > 1) {
+            earlier = sums[e];
+            total = sums[bins + e];
         }
     }
     // first row of each bin: an exclusive scan of the totals over the threads
@@ -423,16 +470,27 @@ hipError_t sort_ids(const I *ids, int64_t S, int top, int E, int32_t *offsets, i
     while ((1 << bits) <= E) ++bits;
     const int steps_per_block = kSortThreads / 32;
     const int beside = QD >= 0 ? (int)((q.M * q.KB + steps_per_block - 1) / steps_per_block) : 0;
-    const size_t lds = kSortWaves * (E + 1) * sizeof(int);
-    if (chunks > 1) {
-        count_kernel<I, QD><<<chunks + beside, kSortThreads, 0, stream>>>(ids, S, E, counts, chunks, q);
-        if (hipError_t e = hipGetLastError()) return e;
-        place_kernel<I, -1><<<chunks, kSortThreads, lds, stream>>>(ids, S, top, E, bits, counts, chunks, offsets,
-                                                                   slot_pos, row_token, q);
-    } else {
-        place_kernel<I, QD><<<chunks + beside, kSortThreads, lds, stream>>>(ids, S, top, E, bits, counts, chunks,
-                                                                            offsets, slot_pos, row_token, q);
+    const size_t lds = (kSortWaves + 2) * (E + 1) * sizeof(int);
+    if (chunks == 1) {
+        place_kernel<I, QD, false><<<chunks + beside, kSortThreads, lds, stream>>>(ids, S, top, E, bits, counts, chunks,
+                                                                                   offsets, slot_pos, row_token, q);
+        return hipGetLastError();
     }
+    count_kernel<I, QD><<<chunks + beside, kSortThreads, 0, stream>>>(ids, S, E, counts, chunks, q);
+    if (hipError_t e = hipGetLastError()) return e;
+    // Every workgroup sums the chunks, kSortThreads / bins threads per bin, or a
+    // scan of its own launch does (us: 17 chunks of 64 experts 14.5 with a thread
+    // per bin, 10.9 with 15; 512 experts, 59 chunks 26.4 so, 16 scanned; 512 chunks of
+    // 64 experts 133, 23.4 scanned).
+    if ((int64_t)chunks * (E + 1) <= kSums * kSortThreads) {
+        place_kernel<I, -1, false><<<chunks, kSortThreads, lds, stream>>>(ids, S, top, E, bits, counts, chunks, offsets,
+                                                                          slot_pos, row_token, q);
+        return hipGetLastError();
+    }
+    scan_kernel<<<E + 1, kSortThreads, 0, stream>>>(counts, chunks, E + 1);
+    if (hipError_t e = hipGetLastError()) return e;
+    place_kernel<I, -1, true><<<chunks, kSortThreads, lds, stream>>>(ids, S, top, E, bits, counts, chunks, offsets,
+                                                                     slot_pos, row_token, q);
     return hipGetLastError();
 }
 
@@ -450,7 +508,7 @@ hipError_t sort_any(const void *ids, bool ids64, int64_t S, int top, int E, int3
 
 int64_t sort_workspace(int64_t S, int64_t E) {
     const int64_t chunks = (S + kChunk - 1) / kChunk;
-    return chunks > 1 ? chunks * (E + 1) * (int64_t)sizeof(int32_t) : 0;
+    return chunks > 1 ? (chunks + 1) * (E + 1) * (int64_t)sizeof(int32_t) : 0;
 }
 
 hipError_t launch_sort(const void *ids, bool ids64, int64_t S, int top, int E, int32_t *offsets,

@@ -35,6 +35,16 @@ def test_sort(T, top, E, drop, wide):
     assert np.array_equal(row_token.cpu().numpy(), want[2])
 
 
+@pytest.mark.parametrize("T,top,E", [(30000, 8, 512), (12300, 4, 511), (50000, 8, 130), (1100000, 4, 100), (70000, 8, 3)])
+def test_sort_many_slots(T, top, E):
+    """Slots of many workgroups, whose counts each sums or a scan does (one and two passes of it)."""
+    ids = np.random.default_rng(E).integers(-1, E + 1, (T, top))
+    ids[T // 3:T // 2] = E - 1  # workgroups with a single expert
+    got = b.moe_sort(torch.from_numpy(ids).to(DEV), E)
+    for g, w in zip(got, ref.sort(ids, E)):
+        assert np.array_equal(g.cpu().numpy(), w)
+
+
 def test_sort_ids_outside_the_experts():
     """Any id outside [0, E) is a dropped slot, 64-bit ones that wrap in 32 bits too."""
     ids = np.array([[0, 7, 8], [-1, 2 ** 32 + 3, -2 ** 63], [3, 2 ** 31, 3], [2 ** 63 - 1, 1, 0]])
