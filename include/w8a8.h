@@ -405,7 +405,7 @@ w8a8_status moe_sort(const void *expert_ids, int ids_bits, int64_t T, int64_t to
                      int64_t workspace_bytes, void *stream);
 
 /*
- * Rows in sorted order and back, H >= 1 elements of dtype each, any H. Arrays
+ * Rows in sorted order and back, 1 <= H <= 2^23 elements of dtype each. Arrays
  * of rows need the alignment of their element type only (16-byte aligned rows
  * take 16-byte accesses); x and d_out have a row stride (ldx, ldd >= H), the
  * others are dense. Sums are made in fp32, in the order of the slots, and
