@@ -112,7 +112,6 @@ struct Sources {
 // 32-bit offset per lane that stays, and a uniform offset that moves with the
 // stage. (Addresses in vector registers cost a 64-bit addition per load, which
 // holds up the MFMAs' issue.)
-
 template <typename Sh>
 struct Loads {
     Sources src, none;                // none: the same buffers with no bytes (loads give 0)
@@ -390,7 +389,8 @@ __global__ __launch_bounds__(GM *GN *kWave, OCC *GM *GN / 4) void tiled_kernel(
     const int tiles = tiles_m * tiles_n;
     // Tiles XCD by XCD, a group's tiles after another's, in parts of up to kPart
     // tile rows by all columns: the tiles that run at once share activation and
-    // weight rows in one L2.
+    // weight rows in one L2 (a layer of 8192 tokens and 32 experts 609 us with parts
+    // of 4 rows that cross groups, 589 so; gate and up read 925 and 632 MB).
     auto locate = [&](const GroupScan &scan, int pid, int &n0) {
         constexpr int kPart = 6;
         const int t = w8a8::xcd_contiguous(pid, tiles);
