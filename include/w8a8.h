@@ -460,10 +460,12 @@ w8a8_status mxfp4_expert_swiglu(const uint8_t *xq, const uint8_t *xs, int64_t T,
 
 /*
  * A whole expert layer: moe_sort, mxfp4_quantize_rows of x, mxfp4_expert_swiglu
- * with w13 [E][2F,H], mxfp4_expert_gemm with w2 [E][H,F] (to dtype), and
- * moe_combine with weights into out [T,H] of dtype. Few slots (T * top <= 8, or
- * <= 64 of small experts) take two launches without the sort; there the experts'
- * outputs are summed in fp32 and not rounded to dtype before.
+ * with w13 [E][2F,H], mxfp4_expert_gemm with w2 [E][H,F] and the weighted sum
+ * with weights into out [T,H] of dtype. The experts' outputs and their sum are held
+ * in fp32 and the sum is rounded to dtype once; only a binary16 layer of more than a
+ * few slots rounds each expert's output to binary16's precision first (not to its
+ * range), as mxfp4_expert_gemm and moe_combine in that type do. Few slots (T * top
+ * <= 8, or <= 64 of small experts) take two launches without the sort.
  *   x [T,H] of dtype with row stride ldx; H a positive multiple of 32 (and 16),
  *   F a positive multiple of 32; expert_ids, ids_bits, top, E as for moe_sort.
  * workspace: device, 16-byte aligned, at least mxfp4_moe_workspace(...) bytes.

@@ -704,7 +704,8 @@ def mxfp4_moe(x, expert_ids, weights, w13q, w13s, w2q, w2s, out=None, workspace=
     """An expert layer: x [T,H] quantized to MXFP4, routed by expert_ids [T,top] (int32 or int64)
     through the experts' gate/up weights w13 [E,2F,H] with SwiGLU and down weights w2 [E,H,F]
     (both MXFP4), and summed with the router's weights [T,top] (float32) -> out [T,H] of x's
-    dtype. workspace: uint8 of at least mxfp4_moe_workspace(...) bytes (a new one if None)."""
+    dtype. The experts' outputs and the sum are held in float32 and rounded once; a float16 layer
+    of more than a few slots rounds the experts' outputs to float16's precision too. workspace: uint8 of at least mxfp4_moe_workspace(...) bytes (a new one if None)."""
     dt, ld, T, H = _float_rows(x, "x")
     T2, top, bits = _expert_ids(expert_ids)
     _routing_weights(weights, T, top)

@@ -125,6 +125,9 @@ hipError_t launch_gather(const void *x, int64_t ldx, const int32_t *slot_pos, in
 // weights null: the plain sum (the gather's gradient)
 hipError_t launch_combine(const void *rows, const int32_t *slot_pos, const float *weights,
                           int64_t T, int top, int H, int dtype, void *out, hipStream_t stream);
+// the layer's sum: fp32 rows (16-byte aligned, H a multiple of 32) to out of dtype
+hipError_t launch_combine_layer(const float *rows, const int32_t *slot_pos, const float *weights,
+                                int64_t T, int top, int H, int dtype, void *out, hipStream_t stream);
 hipError_t launch_combine_backward(const void *d_out, int64_t ldd, const void *rows,
                                    const int32_t *slot_pos, const float *weights, int64_t T,
                                    int top, int H, int dtype, void *d_rows, float *d_weights,

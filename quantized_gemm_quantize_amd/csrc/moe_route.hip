@@ -229,16 +229,19 @@ constexpr int kSlots = 4;  // slots of a token whose rows are in flight together
 template <Dtype D>
 constexpr int size_of() { return D == kF32 ? 4 : 2; }
 
-// V elements of a row, as loaded: 16 bytes (V * size = 16), 4 bytes, or one
+typedef uint32_t v2u32 __attribute__((ext_vector_type(2)));
+
+// V elements of a row, as loaded: 16 bytes (V * size = 16), 8, 4 bytes, or one
 // element. Everything here is read once and written once: streaming accesses.
 template <Dtype D, int V>
 struct Vec {
     static constexpr int kBytes = V * size_of<D>();
-    static_assert(kBytes == 16 || kBytes == 4 || V == 1, "one access");
+    static_assert(kBytes == 16 || kBytes == 8 || kBytes == 4 || V == 1, "one access");
     static constexpr int kWords = kBytes >= 4 ? kBytes / 4 : 1;
     uint32_t w[kWords];
 
     __device__ __forceinline__ void load(const char *p) {
+        static_assert(kBytes != 8, "8 bytes are only written");
         if constexpr (kBytes == 16) {
             const uint4 u = w8a8::load16_stream(p);
             w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
@@ -250,6 +253,8 @@ struct Vec {
     }
     __device__ __forceinline__ void store(char *p) const {
         if constexpr (kBytes == 16) w8a8::store16_nt(p, make_uint4(w[0], w[1], w[2], w[3]));
+        else if constexpr (kBytes == 8)
+            __builtin_nontemporal_store(__builtin_bit_cast(v2u32, make_uint2(w[0], w[1])), reinterpret_cast<v2u32 *>(p));
         else if constexpr (kBytes == 4) __builtin_nontemporal_store(w[0], reinterpret_cast<uint32_t *>(p));
         else __builtin_nontemporal_store((uint16_t)w[0], reinterpret_cast<uint16_t *>(p));
     }
@@ -309,9 +314,19 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(const char *__restrict
     }
 }
 
-// The token's rows, kSlots of them in flight together, summed in the order of
-// its slots.
-template <Dtype D, int V, int U, bool WEIGHTS>
+// A row's value in the sum of a layer of type D whose rows are held in fp32. Binary16
+// layers give what their products and sums give one by one, to the bit: the value has
+// binary16's precision, but where that type has no finite value for it it stays as it is
+// (an expert's output may lie past 65504 while the weighted sum does not).
+template <Dtype D, Dtype R>
+__device__ __forceinline__ float row_value(float v) {
+    if constexpr (D == kF16 && R == kF32) return fabsf(v) < 65520.0f ? (float)(_Float16)v : v;
+    else return v;
+}
+
+// The token's rows (type R), kSlots of them in flight together, summed in the order
+// of its slots.
+template <Dtype D, Dtype R, int V, int U, bool WEIGHTS>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const char *__restrict__ rows,
                                                            const int32_t *__restrict__ slot_pos,
                                                            const float *__restrict__ weights,
@@ -321,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const char *__restric
     const int h0 = (blockIdx.y * U * kThreads + threadIdx.x) * V;
     float sum[U][V] = {};
     for (int j0 = 0; j0 < top; j0 += kSlots) {
-        Vec<D, V> v[kSlots][U];
+        Vec<R, V> v[kSlots][U];
         float w[kSlots];
         bool kept[kSlots];
 #pragma unroll
@@ -334,7 +349,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const char *__restric
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (h0 + u * kThreads * V < H)
-                        v[j][u].load(rows + ((int64_t)p * H + h0 + u * kThreads * V) * size_of<D>());
+                        v[j][u].load(rows + ((int64_t)p * H + h0 + u * kThreads * V) * size_of<R>());
             }
         }
 #pragma unroll
@@ -343,7 +358,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const char *__restric
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[u][i] += WEIGHTS ? w[j] * v[j][u].get(i) : v[j][u].get(i);
+                for (int i = 0; i < V; ++i) {
+                    const float y = row_value<D, R>(v[j][u].get(i));
+                    sum[u][i] += WEIGHTS ? w[j] * y : y;
+                }
         }
     }
 #pragma unroll
@@ -546,10 +564,26 @@ hipError_t launch_combine(const void *rows, const int32_t *slot_pos, const float
         const char *r = static_cast<const char *>(rows);
         char *o = static_cast<char *>(out);
         if (weights)
-            combine_kernel<decltype(d)::value, V, U, true><<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
+            combine_kernel<decltype(d)::value, decltype(d)::value, V, U, true><<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
         else
-            combine_kernel<decltype(d)::value, V, U, false><<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
+            combine_kernel<decltype(d)::value, decltype(d)::value, V, U, false><<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
     });
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_layer(const float *rows, const int32_t *slot_pos, const float *weights,
+                                int64_t T, int top, int H, int dtype, void *out, hipStream_t stream) {
+    // H is a multiple of 32 and the arrays are aligned: 16 bytes of rows per access
+    constexpr int V = 4, U = 2;
+    const dim3 grid((unsigned)T, segments(H, V * U));
+    const char *r = reinterpret_cast<const char *>(rows);
+    char *o = static_cast<char *>(out);
+    if (dtype == kBf16)
+        combine_kernel<kBf16, kF32, V, U, true><<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
+    else if (dtype == kF16)
+        combine_kernel<kF16, kF32, V, U, true><<<grid, kThreads, 0, stream>>>(r, slot_pos, weights, top, T * top, H, o);
+    else
+        return launch_combine(rows, slot_pos, weights, T, top, H, dtype, out, stream);
     return hipGetLastError();
 }
 

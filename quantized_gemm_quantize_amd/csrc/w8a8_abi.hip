@@ -537,8 +537,8 @@ struct MoeParts {
     int64_t offsets, slot_pos, row_token, sort, sort_bytes, xq, xs, hq, hs, y, total;
 };
 
-static w8a8_status moe_parts(int64_t T, int64_t top, int64_t E, int64_t H, int64_t F, int dt,
-                      MoeParts &p) {
+static w8a8_status moe_parts(int64_t T, int64_t top, int64_t E, int64_t H, int64_t F,
+                             MoeParts &p) {
     if (w8a8_status s = moe_shape(T, top)) return s;
     if (E <= 0 || E > MOE_MAX_EXPERTS) return W8A8_ERR_SHAPE;
     const int64_t S = T * top;
@@ -560,7 +560,7 @@ static w8a8_status moe_parts(int64_t T, int64_t top, int64_t E, int64_t H, int64
     p.xs = take(mx_scales(T, H));
     p.hq = take(mx_codes(S, F));
     p.hs = take(mx_scales(S, F));
-    p.y = take(S * H * dtype_size(dt));
+    p.y = take(S * H * 4);  // the experts' outputs stay in fp32 up to their weighted sum
     p.total = at;
     return W8A8_OK;
 }
@@ -569,7 +569,7 @@ int64_t mxfp4_moe_workspace(int64_t T, int64_t top, int64_t E, int64_t H, int64_
                             mxfp4_dtype dtype) {
     MoeParts p;
     const int dt = selector(&dtype);
-    if (T <= 0 || !mx_dtype_ok(dt) || moe_parts(T, top, E, H, F, dt, p) != W8A8_OK) return 0;
+    if (T <= 0 || !mx_dtype_ok(dt) || moe_parts(T, top, E, H, F, p) != W8A8_OK) return 0;
     return p.total;
 }
 
@@ -582,7 +582,7 @@ w8a8_status mxfp4_moe(const void *x, int64_t ldx, mxfp4_dtype dtype, int64_t T, 
     if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
     if (ids_bits != 32 && ids_bits != 64) return W8A8_ERR_DTYPE;
     MoeParts p;
-    if (w8a8_status s = moe_parts(T, top, E, H, F, dt, p)) return s;
+    if (w8a8_status s = moe_parts(T, top, E, H, F, p)) return s;
     if (ldx < H || ldx > INT_MAX) return W8A8_ERR_SHAPE;
     if (T > 0 && workspace_bytes < p.total) return W8A8_ERR_SHAPE;
     if (T == 0) return W8A8_OK;
@@ -615,9 +615,10 @@ w8a8_status mxfp4_moe(const void *x, int64_t ldx, mxfp4_dtype dtype, int64_t T, 
                                             w13s, F, H, ws + p.hq, ws + p.hs, stream))
         return s;
     if (w8a8_status s = mxfp4_expert_gemm(ws + p.hq, ws + p.hs, S, nullptr, S, offsets, E, w2q, w2s,
-                                          H, F, dtype, ws + p.y, stream))
+                                          H, F, MXFP4_F32, ws + p.y, stream))
         return s;
-    return moe_combine(ws + p.y, slot_pos, weights, T, top, H, dtype, out, stream);
+    return hip_status(moe::launch_combine_layer(reinterpret_cast<const float *>(ws + p.y), slot_pos, weights, T,
+                                                (int)top, (int)H, dt, out, static_cast<hipStream_t>(stream)));
 }
 
 const char *w8a8_status_string(int status) {
