@@ -451,16 +451,21 @@ def _result(t, name, shape, dtype, like):
     return t
 
 
-def _scratch(workspace, need, like, stream):
-    """(address, bytes) of a workspace of `need` bytes: the caller's, or a new one that the caching
-    allocator keeps until `stream` has run what is queued on it."""
+def _scratch(workspace, need, like):
+    """A workspace of `need` bytes: the caller's, or a new one. The caller of this function holds it
+    until the library has been called: freed before the launch, its memory could go to another
+    tensor that the kernels then write over."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-        if stream is not None:
-            workspace.record_stream(stream)
-        return workspace.data_ptr(), need
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
     _check(workspace, "workspace", torch.uint8, 1)
-    return workspace.data_ptr(), workspace.shape[0]
+    return workspace
+
+
+def _queued(workspace, own, stream):
+    """After the launch: the allocator keeps a workspace of the binding's until `stream`, if not the
+    current one, has run what is queued on it."""
+    if own is None and workspace is not None and stream is not None:
+        workspace.record_stream(stream)
 
 
 def _stream_of(t, stream) -> int:
@@ -536,12 +541,14 @@ def mxfp4_linear(x, wq, ws, out=None, out_dtype=None, workspace=None, stream=Non
         od = _float_dtype(out_dtype, "out_dtype")
     lib = load()
     out = _result(out, "out", (M, N), out_dtype, x)
-    address = size = 0
+    work, address, size = None, 0, 0
     need = lib.mxfp4_linear_workspace(M, N, K)
     if need or workspace is not None:
-        address, size = _scratch(workspace, need, x, stream)
+        work = _scratch(workspace, need, x)
+        address, size = work.data_ptr(), work.shape[0]
     _done(lib.mxfp4_linear(x.data_ptr(), ld, xd, M, wq.data_ptr(), ws.data_ptr(), N, K, od,
                            out.data_ptr(), address, size, _stream_of(x, stream)), "mxfp4_linear")
+    _queued(work, workspace, stream)
     return out
 
 
@@ -571,12 +578,14 @@ def moe_sort(expert_ids, num_experts, offsets=None, slot_pos=None, row_token=Non
     row_token = _result(row_token, "row_token", (T * top,), torch.int32, expert_ids)
     lib = load()
     need = lib.moe_sort_workspace(T * top, num_experts)
-    address, size = 0, 0
+    work, address, size = None, 0, 0
     if need or workspace is not None:
-        address, size = _scratch(workspace, need, expert_ids, stream)
+        work = _scratch(workspace, need, expert_ids)
+        address, size = work.data_ptr(), work.shape[0]
     _done(lib.moe_sort(expert_ids.data_ptr(), bits, T, top, num_experts, offsets.data_ptr(),
                        slot_pos.data_ptr(), row_token.data_ptr(), address, size,
                        _stream_of(expert_ids, stream)), "moe_sort")
+    _queued(work, workspace, stream)
     return offsets, slot_pos, row_token
 
 
@@ -718,10 +727,11 @@ def mxfp4_moe(x, expert_ids, weights, w13q, w13s, w2q, w2s, out=None, workspace=
         raise ValueError("operand shapes")
     lib = load()
     out = _result(out, "out", (T, H), x.dtype, x)
-    address, size = _scratch(workspace, lib.mxfp4_moe_workspace(T, top, E, H, F, dt), x, stream)
+    work = _scratch(workspace, lib.mxfp4_moe_workspace(T, top, E, H, F, dt), x)
     _done(lib.mxfp4_moe(x.data_ptr(), ld, dt, T, H, expert_ids.data_ptr(), bits, weights.data_ptr(),
                         top, E, w13q.data_ptr(), w13s.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), F,
-                        out.data_ptr(), address, size, _stream_of(x, stream)), "mxfp4_moe")
+                        out.data_ptr(), work.data_ptr(), work.shape[0], _stream_of(x, stream)), "mxfp4_moe")
+    _queued(work, workspace, stream)
     return out
 
 
