@@ -2,8 +2,13 @@
 
 Each function checks tensor dtypes, shapes and devices, allocates missing
 outputs with torch.empty on the input's device, and passes raw device
-pointers plus the current HIP stream to the library function of the same
-name. All arithmetic runs in the library's kernels; there is no fallback. If
+pointers plus the current HIP stream, or `stream`, to the library function of
+the same name. With `stream`, what the binding allocates (outputs and
+workspaces) belongs to that stream, as if the call were made under
+torch.cuda.stream(stream); the caller orders the rest: `stream` has to wait for
+inputs and buffers of the caller's that other streams still write or read, other
+streams for the outputs, and a tensor that is dropped while another stream than
+its own uses it needs torch's record_stream. All arithmetic runs in the library's kernels; there is no fallback. If
 libw8a8.so is absent, every entry point raises.
 """
 from __future__ import annotations
@@ -99,6 +104,15 @@ def load():
     return lib
 
 
+def _new(shape, dtype, like, stream):
+    """A new tensor on `like`'s device in the pool of the stream that will write it: the allocator
+    hands out memory that was freed with work still queued on its stream."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=like.device)  # the quickest form
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=like.device)
+
+
 def _stream_handle(stream) -> int:
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
@@ -135,9 +149,9 @@ def _quantize(fn, x, xq, x_scale, stream, dtype):
     _check_tensor(x, "x", dtype, 2)
     M, K = x.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        xq = _new((M, K), torch.int8, x, stream)
     if x_scale is None:
-        x_scale = torch.empty((M,), dtype=torch.float32, device=x.device)
+        x_scale = _new((M,), torch.float32, x, stream)
     _check_tensor(xq, "xq", torch.int8, 2)
     _check_tensor(x_scale, "x_scale", torch.float32, 1)
     if tuple(xq.shape) != (M, K) or tuple(x_scale.shape) != (M,):
@@ -156,10 +170,10 @@ def w8a8_quantize_rows_f32(x, xq=None, x_scale=None, stream=None):
     return _quantize("w8a8_quantize_rows_f32", x, xq, x_scale, stream, torch.float32)
 
 
-def _out(out, M, N, out_dtype, device):
+def _out(out, M, N, out_dtype, like, stream):
     tdtype = torch.bfloat16 if out_dtype == W8A8_OUT_BF16 else torch.int32
     if out is None:
-        out = torch.empty((M, N), dtype=tdtype, device=device)
+        out = _new((M, N), tdtype, like, stream)
     _check_tensor(out, "out", tdtype, 2)
     if tuple(out.shape) != (M, N):
         raise ValueError("out shape")
@@ -185,7 +199,7 @@ def w8a8_gemm(xq, x_scale, wq, w_scale, out=None, out_dtype="bf16", stream=None)
     N, K2 = wq.shape
     if K2 != K or tuple(x_scale.shape) != (M,) or tuple(w_scale.shape) != (N,):
         raise ValueError("operand shapes")
-    out = _out(out, M, N, od, xq.device)
+    out = _out(out, M, N, od, xq, stream)
     _call("w8a8_gemm", xq.data_ptr(), x_scale.data_ptr(), M, wq.data_ptr(), w_scale.data_ptr(),
           N, K, out.data_ptr(), od, _stream_handle(stream))
     return out
@@ -208,7 +222,7 @@ def w8a8_gemm_addmm(xq, x_scale, wq, w_scale, bias=None, alpha=1.0, beta=None, o
         _check_tensor(bias, "bias", torch.float32, 1)
         if tuple(bias.shape) != (N,):
             raise ValueError("bias shape")
-    out = _out(out, M, N, _out_dtype("bf16"), xq.device)
+    out = _out(out, M, N, _out_dtype("bf16"), xq, stream)
     _call("w8a8_gemm_addmm", xq.data_ptr(), x_scale.data_ptr(), M, wq.data_ptr(),
           w_scale.data_ptr(), N, K, None if bias is None else bias.data_ptr(), float(alpha),
           float(beta), out.data_ptr(), _stream_handle(stream))
@@ -221,9 +235,9 @@ def w8a8_compress24(wq, values=None, meta=None, stream=None):
     _check_tensor(wq, "wq", torch.int8, 2)
     N, K = wq.shape
     if values is None:
-        values = torch.empty((K // 128, N, 64), dtype=torch.int8, device=wq.device)
+        values = _new((K // 128, N, 64), torch.int8, wq, stream)
     if meta is None:
-        meta = torch.empty((K // 128, N, 4), dtype=torch.int32, device=wq.device)
+        meta = _new((K // 128, N, 4), torch.int32, wq, stream)
     _check_tensor(values, "values", torch.int8, 3)
     _check_tensor(meta, "meta", torch.int32, 3)
     if tuple(values.shape) != (K // 128, N, 64) or tuple(meta.shape) != (K // 128, N, 4):
@@ -247,7 +261,7 @@ def w8a8_sparse24_gemm(xq, x_scale, values, meta, w_scale, out=None, out_dtype="
     if (tuple(values.shape) != (K // 128, N, 64) or tuple(meta.shape) != (K // 128, N, 4)
             or tuple(x_scale.shape) != (M,)):
         raise ValueError("operand shapes")
-    out = _out(out, M, N, od, xq.device)
+    out = _out(out, M, N, od, xq, stream)
     _call("w8a8_sparse24_gemm", xq.data_ptr(), x_scale.data_ptr(), M, values.data_ptr(),
           meta.data_ptr(), w_scale.data_ptr(), N, K, out.data_ptr(), od, _stream_handle(stream))
     return out
@@ -285,7 +299,7 @@ def w4a16_dequant(wq4, scales, zeros, signed=False, out=None, stream=None):
     complement (s4)."""
     N, K, G, dt = _w4a16_operands(wq4, scales, zeros)
     if out is None:
-        out = torch.empty((N, K), dtype=dt, device=wq4.device)
+        out = _new((N, K), dt, wq4, stream)
     _check_tensor(out, "out", dt, 2)
     if tuple(out.shape) != (N, K):
         raise ValueError("out shape")
@@ -304,7 +318,7 @@ def w4a16_gemm(x, wq4, scales, zeros, signed=False, out=None, stream=None):
     if x.shape[1] != K:
         raise ValueError("operand shapes")
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=x.device)
+        out = _new((M, N), dt, x, stream)
     _check_tensor(out, "out", dt, 2)
     if tuple(out.shape) != (M, N):
         raise ValueError("out shape")
@@ -329,7 +343,7 @@ def w8a8_bsr_gemm(xq, x_scale, crow, col, values, w_scale, out=None, out_dtype="
     N = w_scale.shape[0]
     if bs != bs2 or col.shape[0] != nnzb or crow.shape[0] != N // max(bs, 1) + 1:
         raise ValueError("BSR array shapes")
-    out = _out(out, M, N, od, xq.device)
+    out = _out(out, M, N, od, xq, stream)
     _call("w8a8_bsr_gemm", xq.data_ptr(), x_scale.data_ptr(), M, K, crow.data_ptr(),
           col.data_ptr() if nnzb else 0, values.data_ptr() if nnzb else 0, nnzb, bs,
           w_scale.data_ptr(), N, out.data_ptr(), od, _stream_handle(stream))
@@ -357,7 +371,7 @@ def w8a8_bsr_gemm_addmm(xq, x_scale, crow, col, values, w_scale, bias=None, alph
         _check_tensor(bias, "bias", torch.float32, 1)
         if tuple(bias.shape) != (N,):
             raise ValueError("bias shape")
-    out = _out(out, M, N, _out_dtype("bf16"), xq.device)
+    out = _out(out, M, N, _out_dtype("bf16"), xq, stream)
     _call("w8a8_bsr_gemm_addmm", xq.data_ptr(), x_scale.data_ptr(), M, K, crow.data_ptr(),
           col.data_ptr() if nnzb else 0, values.data_ptr() if nnzb else 0, nnzb, bs,
           w_scale.data_ptr(), N, None if bias is None else bias.data_ptr(), float(alpha),
@@ -382,7 +396,7 @@ def w8a8_fused_linear(x, wq, w_scale, bias=None, alpha=1.0, beta=None, out=None,
         _check_tensor(bias, "bias", torch.float32, 1)
         if tuple(bias.shape) != (N,):
             raise ValueError("bias shape")
-    out = _out(out, M, N, _out_dtype("bf16"), x.device)
+    out = _out(out, M, N, _out_dtype("bf16"), x, stream)
     _call("w8a8_fused_linear", x.data_ptr(), M, K, wq.data_ptr(), w_scale.data_ptr(), N,
           None if bias is None else bias.data_ptr(), float(alpha), float(beta), out.data_ptr(),
           _stream_handle(stream))
@@ -441,31 +455,24 @@ def _check(t, name, dtype, ndim):
         _check_tensor(t, name, dtype, ndim)
 
 
-def _result(t, name, shape, dtype, like):
+def _result(t, name, shape, dtype, like, stream):
     """`t` checked, or a new tensor on `like`'s device."""
     if t is None:
-        return torch.empty(*shape, dtype=dtype, device=like.device)  # the quickest form
+        return _new(shape, dtype, like, stream)
     _check(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
 
-def _scratch(workspace, need, like):
+def _scratch(workspace, need, like, stream):
     """A workspace of `need` bytes: the caller's, or a new one. The caller of this function holds it
     until the library has been called: freed before the launch, its memory could go to another
     tensor that the kernels then write over."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
+        return _new((need,), torch.uint8, like, stream)
     _check(workspace, "workspace", torch.uint8, 1)
     return workspace
-
-
-def _queued(workspace, own, stream):
-    """After the launch: the allocator keeps a workspace of the binding's until `stream`, if not the
-    current one, has run what is queued on it."""
-    if own is None and workspace is not None and stream is not None:
-        workspace.record_stream(stream)
 
 
 def _stream_of(t, stream) -> int:
@@ -497,8 +504,8 @@ def mxfp4_quantize_rows(x, codes=None, scales=None, stream=None):
     """x [M,K] (bfloat16, float16 or float32; rows may lie apart) -> MXFP4: codes uint8 [M,K/2]
     and scales uint8 [ceil(K/256),M,8], the storage of include/w8a8.h."""
     dt, ld, M, K = _float_rows(x, "x")
-    codes = _result(codes, "codes", (M, K // 2), torch.uint8, x)
-    scales = _result(scales, "scales", ((K + 255) // 256, M, 8), torch.uint8, x)
+    codes = _result(codes, "codes", (M, K // 2), torch.uint8, x, stream)
+    scales = _result(scales, "scales", ((K + 255) // 256, M, 8), torch.uint8, x, stream)
     _done(load().mxfp4_quantize_rows(x.data_ptr(), ld, M, K, dt, codes.data_ptr(), scales.data_ptr(),
                                      _stream_of(x, stream)), "mxfp4_quantize_rows")
     return codes, scales
@@ -508,7 +515,7 @@ def mxfp4_dequantize_rows(codes, scales, dtype=torch.bfloat16, out=None, stream=
     """The values [M,K] that MXFP4 rows stand for, in `dtype`."""
     M, K = _check_mx(codes, scales)
     dt = _float_dtype(dtype)
-    out = _result(out, "out", (M, K), dtype, codes)
+    out = _result(out, "out", (M, K), dtype, codes, stream)
     _done(load().mxfp4_dequantize_rows(codes.data_ptr(), scales.data_ptr(), M, K, dt, out.data_ptr(),
                                        _stream_of(codes, stream)), "mxfp4_dequantize_rows")
     return out
@@ -521,7 +528,7 @@ def mxfp4_gemm(xq, xs, wq, ws, out=None, out_dtype=torch.bfloat16, stream=None):
     if K2 != K:
         raise ValueError("operand shapes")
     dt = _float_dtype(out_dtype, "out_dtype")
-    out = _result(out, "out", (M, N), out_dtype, xq)
+    out = _result(out, "out", (M, N), out_dtype, xq, stream)
     _done(load().mxfp4_gemm(xq.data_ptr(), xs.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K, dt,
                             out.data_ptr(), _stream_of(xq, stream)), "mxfp4_gemm")
     return out
@@ -540,15 +547,14 @@ def mxfp4_linear(x, wq, ws, out=None, out_dtype=None, workspace=None, stream=Non
     else:
         od = _float_dtype(out_dtype, "out_dtype")
     lib = load()
-    out = _result(out, "out", (M, N), out_dtype, x)
+    out = _result(out, "out", (M, N), out_dtype, x, stream)
     work, address, size = None, 0, 0
     need = lib.mxfp4_linear_workspace(M, N, K)
     if need or workspace is not None:
-        work = _scratch(workspace, need, x)
+        work = _scratch(workspace, need, x, stream)
         address, size = work.data_ptr(), work.shape[0]
     _done(lib.mxfp4_linear(x.data_ptr(), ld, xd, M, wq.data_ptr(), ws.data_ptr(), N, K, od,
                            out.data_ptr(), address, size, _stream_of(x, stream)), "mxfp4_linear")
-    _queued(work, workspace, stream)
     return out
 
 
@@ -573,19 +579,18 @@ def moe_sort(expert_ids, num_experts, offsets=None, slot_pos=None, row_token=Non
     without an expert): (offsets int32 [num_experts+1], slot_pos int32 [T,top], row_token int32
     [T*top]) -- include/w8a8.h defines them. The order is stable."""
     T, top, bits = _expert_ids(expert_ids)
-    offsets = _result(offsets, "offsets", (max(num_experts, 0) + 1,), torch.int32, expert_ids)
-    slot_pos = _result(slot_pos, "slot_pos", (T, top), torch.int32, expert_ids)
-    row_token = _result(row_token, "row_token", (T * top,), torch.int32, expert_ids)
+    offsets = _result(offsets, "offsets", (max(num_experts, 0) + 1,), torch.int32, expert_ids, stream)
+    slot_pos = _result(slot_pos, "slot_pos", (T, top), torch.int32, expert_ids, stream)
+    row_token = _result(row_token, "row_token", (T * top,), torch.int32, expert_ids, stream)
     lib = load()
     need = lib.moe_sort_workspace(T * top, num_experts)
     work, address, size = None, 0, 0
     if need or workspace is not None:
-        work = _scratch(workspace, need, expert_ids)
+        work = _scratch(workspace, need, expert_ids, stream)
         address, size = work.data_ptr(), work.shape[0]
     _done(lib.moe_sort(expert_ids.data_ptr(), bits, T, top, num_experts, offsets.data_ptr(),
                        slot_pos.data_ptr(), row_token.data_ptr(), address, size,
                        _stream_of(expert_ids, stream)), "moe_sort")
-    _queued(work, workspace, stream)
     return offsets, slot_pos, row_token
 
 
@@ -601,7 +606,7 @@ def moe_gather(x, slot_pos, out=None, stream=None):
     top = slot_pos.shape[1]
     if slot_pos.shape[0] != T:
         raise ValueError("slot_pos must have a row per token")
-    out = _result(out, "out", (T * top, H), x.dtype, x)
+    out = _result(out, "out", (T * top, H), x.dtype, x, stream)
     _done(load().moe_gather(x.data_ptr(), ld, slot_pos.data_ptr(), T, top, H, dt, out.data_ptr(),
                             _stream_of(x, stream)), "moe_gather")
     return out
@@ -622,7 +627,7 @@ def _sorted_rows(rows, name, slot_pos):
 def moe_gather_backward(d_rows, slot_pos, out=None, stream=None):
     """Gradient of moe_gather: d_rows [T*top,H] -> d_x [T,H], the sum of each token's rows."""
     dt, T, top, H = _sorted_rows(d_rows, "d_rows", slot_pos)
-    out = _result(out, "out", (T, H), d_rows.dtype, d_rows)
+    out = _result(out, "out", (T, H), d_rows.dtype, d_rows, stream)
     _done(load().moe_gather_backward(d_rows.data_ptr(), slot_pos.data_ptr(), T, top, H, dt,
                                      out.data_ptr(), _stream_of(d_rows, stream)),
           "moe_gather_backward")
@@ -640,7 +645,7 @@ def moe_combine(rows, slot_pos, weights, out=None, stream=None):
     weights [T,top] (float32) and summed."""
     dt, T, top, H = _sorted_rows(rows, "rows", slot_pos)
     _routing_weights(weights, T, top)
-    out = _result(out, "out", (T, H), rows.dtype, rows)
+    out = _result(out, "out", (T, H), rows.dtype, rows, stream)
     _done(load().moe_combine(rows.data_ptr(), slot_pos.data_ptr(), weights.data_ptr(), T, top, H, dt,
                              out.data_ptr(), _stream_of(rows, stream)), "moe_combine")
     return out
@@ -653,8 +658,8 @@ def moe_combine_backward(d_out, rows, slot_pos, weights, d_rows=None, d_weights=
     dd, ld, n, width = _float_rows(d_out, "d_out")
     if dd != dt or n != T or width != H:
         raise ValueError("d_out must have the dtype of rows and a row per token")
-    d_rows = _result(d_rows, "d_rows", (T * top, H), rows.dtype, rows)
-    d_weights = _result(d_weights, "d_weights", (T, top), torch.float32, rows)
+    d_rows = _result(d_rows, "d_rows", (T * top, H), rows.dtype, rows, stream)
+    d_weights = _result(d_weights, "d_weights", (T, top), torch.float32, rows, stream)
     _done(load().moe_combine_backward(d_out.data_ptr(), ld, rows.data_ptr(), slot_pos.data_ptr(),
                                       weights.data_ptr(), T, top, H, dt, d_rows.data_ptr(),
                                       d_weights.data_ptr(), _stream_of(rows, stream)),
@@ -684,7 +689,7 @@ def mxfp4_expert_gemm(xq, xs, offsets, wq, ws, row_token=None, out=None, out_dty
     all MXFP4; rows past offsets[E] are 0. With row_token [S], row r is row row_token[r] of xq."""
     T, S, E, N, K = _expert_operands(xq, xs, offsets, wq, ws, row_token)
     dt = _float_dtype(out_dtype, "out_dtype")
-    out = _result(out, "out", (S, N), out_dtype, xq)
+    out = _result(out, "out", (S, N), out_dtype, xq, stream)
     _done(load().mxfp4_expert_gemm(xq.data_ptr(), xs.data_ptr(), T,
                                    None if row_token is None else row_token.data_ptr(), S,
                                    offsets.data_ptr(), E, wq.data_ptr(), ws.data_ptr(), N, K, dt,
@@ -699,8 +704,8 @@ def mxfp4_expert_swiglu(xq, xs, offsets, wq, ws, row_token=None, hq=None, hs=Non
     F = N // 2
     if N % 64:
         raise ValueError("wq must have 2F rows per expert, F a multiple of 32")
-    hq = _result(hq, "hq", (S, F // 2), torch.uint8, xq)
-    hs = _result(hs, "hs", ((F + 255) // 256, S, 8), torch.uint8, xq)
+    hq = _result(hq, "hq", (S, F // 2), torch.uint8, xq, stream)
+    hs = _result(hs, "hs", ((F + 255) // 256, S, 8), torch.uint8, xq, stream)
     _done(load().mxfp4_expert_swiglu(xq.data_ptr(), xs.data_ptr(), T,
                                      None if row_token is None else row_token.data_ptr(), S,
                                      offsets.data_ptr(), E, wq.data_ptr(), ws.data_ptr(), F, K,
@@ -726,12 +731,11 @@ def mxfp4_moe(x, expert_ids, weights, w13q, w13s, w2q, w2s, out=None, workspace=
     if T2 != T or K != H or N2 != H or N != 2 * F:
         raise ValueError("operand shapes")
     lib = load()
-    out = _result(out, "out", (T, H), x.dtype, x)
-    work = _scratch(workspace, lib.mxfp4_moe_workspace(T, top, E, H, F, dt), x)
+    out = _result(out, "out", (T, H), x.dtype, x, stream)
+    work = _scratch(workspace, lib.mxfp4_moe_workspace(T, top, E, H, F, dt), x, stream)
     _done(lib.mxfp4_moe(x.data_ptr(), ld, dt, T, H, expert_ids.data_ptr(), bits, weights.data_ptr(),
                         top, E, w13q.data_ptr(), w13s.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), F,
                         out.data_ptr(), work.data_ptr(), work.shape[0], _stream_of(x, stream)), "mxfp4_moe")
-    _queued(work, workspace, stream)
     return out
 
 
