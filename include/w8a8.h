@@ -336,7 +336,7 @@ typedef enum {
  * (no other rounding than the definition's) for every finite input.
  * x and ldx * element size must be 16-byte aligned.
  * Errors: NULL, SHAPE (M < 0, K not a positive multiple of 32 or above
- *         MXFP4_MAX_K, ldx < K, M * ceil(K/256) >= 2^27), ALIGN,
+ *         MXFP4_MAX_K, ldx < K, M * ceil(K/256) > 2^27 - 8), ALIGN,
  *         DTYPE, HIP.
  */
 w8a8_status mxfp4_quantize_rows(const void *x, int64_t ldx, int64_t M, int64_t K,
@@ -442,7 +442,8 @@ w8a8_status moe_combine_backward(const void *d_out, int64_t ldd, const void *row
  *   wq         [E][N, K/2], ws [E][ceil(K/256), N, 8]
  *   out        [S,N] of dtype
  * S >= 0 rows, N and K as for mxfp4_gemm; with row_token, x's codes hold less
- * than 2^32 bytes.
+ * than 2^32 bytes. A launch holds fewer than 2^32 threads, which (few rows for each
+ * of many experts with millions of channels) bounds N below that: SHAPE then.
  * mxfp4_expert_swiglu: N = 2F, rows 2f and 2f+1 of a weight are the gate and
  * the up projection of hidden unit f (F a positive multiple of 32); writes the
  * hidden activations gate / (1 + exp(-gate)) * up, computed in fp32 from the
@@ -468,7 +469,8 @@ w8a8_status mxfp4_expert_swiglu(const uint8_t *xq, const uint8_t *xs, int64_t T,
  * <= 8, or <= 64 of small experts) take two launches without the sort.
  *   x [T,H] of dtype with row stride ldx; H a positive multiple of 32 (and 16),
  *   F a positive multiple of 32; expert_ids, ids_bits, top, E as for moe_sort.
- * workspace: device, 16-byte aligned, at least mxfp4_moe_workspace(...) bytes.
+ * workspace: device, 16-byte aligned, at least mxfp4_moe_workspace(...) bytes (0
+ * for sizes that are refused, the bounds of the calls it is made of).
  * Errors: as the calls it is made of; SHAPE when workspace_bytes is too small.
  */
 int64_t mxfp4_moe_workspace(int64_t T, int64_t top, int64_t E, int64_t H, int64_t F,

@@ -34,6 +34,9 @@ hipError_t launch_sparse24_gemm(const int8_t *xq, const float *xs, int M, const 
                                 const uint32_t *meta, const float *ws, int N, int K, void *out,
                                 bool out_i32, hipStream_t stream);
 
+// A launch holds fewer than 2^32 threads.
+inline bool grid_fits(int64_t workgroups, int threads) { return workgroups * threads < ((int64_t)1 << 32); }
+
 // Compute units of the current device (queried once per device).
 int device_cu_count();
 

@@ -25,6 +25,7 @@
 //    needs whole blocks of 32 hidden units: CT = 4, 64 channels.
 #include "launch.hpp"
 #include "mxfp4_epilogue.hpp"
+#include "mxfp4_form.hpp"
 
 namespace mxfp4 {
 namespace {
@@ -460,24 +461,16 @@ hipError_t launch_plain(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
     }
 }
 
-// Channels and wavefronts per workgroup. Grouped rows: 64 channels by 2
-// wavefronts (40 KB of LDS: four workgroups of a CU hide each other's start and
-// end; 32 experts' down products of 8 rows, 25.5 us against 28.5 with 4
-// wavefronts), unless there are too few workgroups for that: 4 wavefronts
-// (1 token, 4 experts: gate and up 9.6 against 10.2 us, down 5.6 against 6.1).
-// Dense: 16 channels by 8 wavefronts, as a single weight has few channels.
 template <int MT>
 hipError_t launch_rows(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
-                       const Groups &g, int N, int K, int epilogue, const Output &o, hipStream_t stream) {
+                       const Groups &g, int N, int K, int epilogue, const Output &o, const Form &f,
+                       hipStream_t stream) {
     if constexpr (MT < 4) {
-        const int64_t quads = most_tiles(g.S, g.E, 16 * MT, true) * ((N + 63) / 64);
-        const bool few = quads <= 2 * w8a8::device_cu_count();
         if (epilogue == kSwiglu)
-            return few ? launch_ep<MT, 4, 4, kSwiglu>(xq, xs, wq, ws, g, N, K, o, stream)
-                       : launch_ep<MT, 4, 2, kSwiglu>(xq, xs, wq, ws, g, N, K, o, stream);
-        if (g.offsets)
-            return few ? launch_plain<MT, 2, 4>(xq, xs, wq, ws, g, N, K, epilogue, o, stream)
-                       : launch_plain<MT, 4, 2>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
+            return f.waves == 4 ? launch_ep<MT, 4, 4, kSwiglu>(xq, xs, wq, ws, g, N, K, o, stream)
+                                : launch_ep<MT, 4, 2, kSwiglu>(xq, xs, wq, ws, g, N, K, o, stream);
+        if (f.channels == 64) return launch_plain<MT, 4, 2>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
+        if (f.channels == 32) return launch_plain<MT, 2, 4>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
         return launch_plain<MT, 1, 8>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
     } else {
         return launch_plain<MT, 1, 4>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
@@ -561,10 +554,10 @@ hipError_t launch_moe_down(const uint8_t *hq, const uint8_t *hs, const Ids &slot
 
 hipError_t launch_gemm_decode(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
                               const uint8_t *ws, const Groups &g, int N, int K, int epilogue,
-                              const Output &o, int row_tiles, hipStream_t stream) {
-    if (row_tiles <= 1) return launch_rows<1>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
-    if (row_tiles <= 2) return launch_rows<2>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
-    return launch_rows<4>(xq, xs, wq, ws, g, N, K, epilogue, o, stream);
+                              const Output &o, const Form &f, hipStream_t stream) {
+    if (f.rows == 16) return launch_rows<1>(xq, xs, wq, ws, g, N, K, epilogue, o, f, stream);
+    if (f.rows == 32) return launch_rows<2>(xq, xs, wq, ws, g, N, K, epilogue, o, f, stream);
+    return launch_rows<4>(xq, xs, wq, ws, g, N, K, epilogue, o, f, stream);
 }
 
 }  // namespace mxfp4

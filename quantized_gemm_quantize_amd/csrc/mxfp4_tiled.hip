@@ -34,13 +34,14 @@
 // load). Alone, a stage's 68 KB of operands take 1.27 us: 64 reads of 128 bytes
 // in flight per CU at a latency of about 300 clocks, 27 bytes per clock, whatever
 // the address pattern; so a tile with more products per byte is faster until
-// too few tiles are left (see the choice at the end). 2048 x 4096 x 4096 20 us, 38400
+// too few tiles are left (tiled_form in mxfp4_gemm.hip). 2048 x 4096 x 4096 20 us, 38400
 // x 4096 x 1024 119 us, 32 experts' gate and up of 8192 tokens x 4 302 us, their
 // down products 167 us.
 #include <algorithm>
 
 #include "launch.hpp"
 #include "mxfp4_epilogue.hpp"
+#include "mxfp4_form.hpp"
 
 namespace mxfp4 {
 namespace {
@@ -559,34 +560,14 @@ hipError_t launch_shape(const Operands &op, const Groups &g, int N, int K, int e
 
 hipError_t launch_gemm_tiled(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
                              const uint8_t *ws, const Groups &g, int N, int K, int epilogue,
-                             const Output &o, hipStream_t stream) {
+                             const Output &o, const Form &f, hipStream_t stream) {
     const Operands op{xq, xs, wq, ws};
-    // The smallest tile whose tiles all run at once (one workgroup per CU),
-    // else 256 x 256, whose operands' bytes per product are the fewest. Measured
-    // at N = K = 4096 (us; 64x64, 64x128, 128x128, 256x128, 256x256): M = 256
-    // 8.6, 10.0, 11.3, 14.3, 25.3; M = 384 10.9, 10.4, 11.5, 14.4, 25.2; M = 768
-    // 16.4, 14.6, 12.4, 15.3, 26.5; M = 1536 28.1, 23.4, 24.1, 17.5, 27.6; M = 4096
-    // 68.5, 54.4, 49.5, 47.5, 36.1.
-    // Short K: two workgroups of 256 x 128 per CU with 128-element stages, whose
-    // starts and stores overlap each other's products (8192 x 8192, against 256 x
-    // 256: K = 512 43.3 -> 39.2 us, K = 1024 56.0 -> 56.3, K = 2048 81.4 -> 89.6; 32
-    // experts' gate and up [2944, 960] with 285 rows each 41.3 -> 35.4).
-    // Small groups: 64 rows, as a taller tile is mostly empty (32 experts with 64
-    // rows each: gate and up [4096, 4096] 82.1 -> 77.5, down [4096, 2048] 45.1 -> 38.9;
-    // with 256 rows 111 -> 152 and 63 -> 82).
-    const int64_t cus = w8a8::device_cu_count();
-    auto tiles = [&](int bm, int bn) {
-        return most_tiles(g.S, g.E, bm, g.offsets != nullptr) * ((N + bn - 1) / bn);
-    };
-    if (tiles(64, 64) <= cus && epilogue != kSwiglu)
-        return launch_plain<64, 64, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
-    if (tiles(64, 128) <= cus) return launch_shape<64, 128, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
-    if (g.offsets && g.S < 96ll * g.E)
-        return launch_shape<64, 128, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
-    if (tiles(128, 128) <= cus) return launch_shape<128, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
-    if (tiles(256, 128) <= cus) return launch_shape<256, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
-    if (K <= 1024) return launch_shape<256, 128, 2, 2, 4, 3, 2>(op, g, N, K, epilogue, o, stream);
-    return launch_shape<256, 256, 2, 4, 8, 2, 1>(op, g, N, K, epilogue, o, stream);
+    if (f.channels == 64) return launch_plain<64, 64, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
+    if (f.rows == 64) return launch_shape<64, 128, 2, 2, 8, 3, 2>(op, g, N, K, epilogue, o, stream);
+    if (f.rows == 128) return launch_shape<128, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
+    if (f.channels == 256) return launch_shape<256, 256, 2, 4, 8, 2, 1>(op, g, N, K, epilogue, o, stream);
+    if (f.waves == 8) return launch_shape<256, 128, 4, 2, 8, 3, 1>(op, g, N, K, epilogue, o, stream);
+    return launch_shape<256, 128, 2, 2, 4, 3, 2>(op, g, N, K, epilogue, o, stream);
 }
 
 }  // namespace mxfp4

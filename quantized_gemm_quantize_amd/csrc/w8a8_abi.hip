@@ -16,6 +16,7 @@
 #include "common.hpp"
 #include "launch.hpp"
 #include "mxfp4_epilogue.hpp"
+#include "mxfp4_form.hpp"
 
 namespace {
 
@@ -291,7 +292,8 @@ static int64_t dtype_size(int d) { return d == MXFP4_F32 ? 4 : 2; }
 static w8a8_status mx_shape(int64_t rows, int64_t K) {
     if (rows < 0 || rows > INT_MAX / 2 || K <= 0 || K % 32 != 0 || K > MXFP4_MAX_K)
         return W8A8_ERR_SHAPE;
-    if (rows * ((K + 255) / 256) >= (1 << 27)) return W8A8_ERR_SHAPE;  // 32 threads each, one grid
+    // 32 threads per 256 elements, 8 of them to a workgroup
+    if (rows * ((K + 255) / 256) > (1 << 27) - 8) return W8A8_ERR_SHAPE;
     return W8A8_OK;
 }
 
@@ -300,7 +302,8 @@ static w8a8_status mx_weight(int64_t N, int64_t K) {
     return mx_shape(N, K);
 }
 
-// Outputs of a product: at most 2^36 (the kernels count tiles in 32 bits).
+// Outputs of a product: at most 2^36 (the kernels count tiles in 32 bits, and a dense
+// product's workgroups are then within a grid's threads).
 static w8a8_status mx_out(int64_t rows, int64_t N) {
     return rows > 0 && N > ((int64_t)1 << 36) / rows ? W8A8_ERR_SHAPE : W8A8_OK;
 }
@@ -503,6 +506,7 @@ static w8a8_status expert_entry(const uint8_t *xq, const uint8_t *xs, int64_t T,
     if (row_token)
         if (w8a8_status s = mx_tokens(T, K)) return s;
     if (S == 0) return W8A8_OK;
+    if (!mxfp4::product_fits(mxfp4::Rows{S, E, true}, (int)N, (int)K, epilogue)) return W8A8_ERR_SHAPE;
     if (!xq || !xs || !offsets || !wq || !ws) return W8A8_ERR_NULL;
     if (epilogue == mxfp4::kSwiglu ? !o.codes || !o.scales : !o.out) return W8A8_ERR_NULL;
     if (misaligned(xq) || misaligned(xs) || misaligned(wq) || misaligned(ws) || misaligned(o.out) ||
@@ -548,7 +552,7 @@ static w8a8_status moe_parts(int64_t T, int64_t top, int64_t E, int64_t H, int64
     if (w8a8_status s = mx_weight(2 * F, H)) return s;
     if (w8a8_status s = mx_out(S, 2 * F)) return s;
     if (w8a8_status s = mx_out(S, H)) return s;
-    if (w8a8_status s = mx_tokens(T, H)) return s;
+    if (w8a8_status s = mx_tokens(T, H)) return s;  // so the sort's grid holds the tokens' quantization too
     int64_t at = 0;
     auto take = [&](int64_t bytes) { const int64_t b = at; at += align256(bytes); return b; };
     p.offsets = take((E + 1) * 4);
