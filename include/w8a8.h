@@ -447,7 +447,9 @@ w8a8_status moe_combine_backward(const void *d_out, int64_t ldd, const void *row
  * mxfp4_expert_swiglu: N = 2F, rows 2f and 2f+1 of a weight are the gate and
  * the up projection of hidden unit f (F a positive multiple of 32); writes the
  * hidden activations gate / (1 + exp(-gate)) * up, computed in fp32 from the
- * accumulators, as MXFP4 rows: hq [S,F/2], hs [ceil(F/256), S, 8].
+ * accumulators, as MXFP4 rows: hq [S,F/2], hs [ceil(F/256), S, 8]. 1 / (1 +
+ * exp(-gate)) is held in fp32: for gates under -87 it has a step of 2^-149, and it
+ * is 0 for gates under -104.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, HIP.
  */
 w8a8_status mxfp4_expert_gemm(const uint8_t *xq, const uint8_t *xs, int64_t T,

@@ -188,22 +188,35 @@ __device__ __forceinline__ void source_rows(const Groups &g, int (&r)[N]) {
 }
 
 // Gate and up projections of one hidden unit -> its activation, gate / (1 +
-// exp(-gate)) * up. The reciprocal is v_rcp_f32 (within 1 ulp; it flushes
-// results below 2^-126, which only gates under -87 reach): the correctly
+// exp(-gate)) * up. With t = 2^-13 exp(-gate / 2) the sum is 2^26 (t^2 + 2^-26): it
+// overflows for no gate above -105, where the sigmoid rounds to 0, and v_rcp_f32
+// (within 1 ulp; it flushes results below 2^-126) sees 2^-26 to 2^126, so that gates
+// under -87 keep their activations (the sigmoid is then below 2^-126, in steps of
+// 2^-149). The 13 in the exponent's argument costs 2^-21 of t at most. The correctly
 // rounded division made the epilogue of a 256 x 256 tile several times as long.
+constexpr float kHalfLog2e = 0.72134752f;
+constexpr float kTwoM26 = 1.0f / 67108864.0f;
+
 __device__ __forceinline__ float swiglu(float gate, float up) {
-    return gate * __builtin_amdgcn_rcpf(1.0f + __expf(-gate)) * up;
+    const float t = __builtin_amdgcn_exp2f(__builtin_fmaf(-kHalfLog2e, gate, -13.0f));
+    const float r = __builtin_amdgcn_rcpf(__builtin_fmaf(t, t, kTwoM26));
+    return gate * (r * kTwoM26) * up;
 }
 
 // Four at once, step by step: one after the other, each waits for its own
 // exponential and reciprocal (32 experts' gate and up of 8192 tokens 318 -> 314 us).
 __device__ __forceinline__ v4f swiglu4(const v4f &gate, const v4f &up) {
-    float e0 = __expf(-gate[0]), e1 = __expf(-gate[1]), e2 = __expf(-gate[2]), e3 = __expf(-gate[3]);
-    asm volatile("" : "+v"(e0), "+v"(e1), "+v"(e2), "+v"(e3));
-    e0 = __builtin_amdgcn_rcpf(1.0f + e0), e1 = __builtin_amdgcn_rcpf(1.0f + e1);
-    e2 = __builtin_amdgcn_rcpf(1.0f + e2), e3 = __builtin_amdgcn_rcpf(1.0f + e3);
-    asm volatile("" : "+v"(e0), "+v"(e1), "+v"(e2), "+v"(e3));
-    return v4f{gate[0] * e0 * up[0], gate[1] * e1 * up[1], gate[2] * e2 * up[2], gate[3] * e3 * up[3]};
+    float t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(-kHalfLog2e, gate[i], -13.0f));
+    asm volatile("" : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = __builtin_amdgcn_rcpf(__builtin_fmaf(t[i], t[i], kTwoM26));
+    asm volatile("" : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3]));
+    v4f v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = gate[i] * (t[i] * kTwoM26) * up[i];
+    return v;
 }
 
 }  // namespace mxfp4
