@@ -5,7 +5,7 @@
 `ExpertLayer.forward` is the serving path: one call quantizes the tokens, runs the experts' gate and
 up products with SwiGLU, their down products and the weighted sum. `ExpertLayer.train_router` keeps
 the experts frozen and trains the router through the gradient of the weighted sum. `MixtureFunction`
-shows the routing around experts of the user's own, with gradients for tokens and weights.
+shows the routing around experts of the user's own, with gradients for tokens, weights and the experts' parameters.
 """
 import os
 import sys
@@ -66,27 +66,49 @@ class ExpertLayer:
         return error.square().sum(dim=1).mean().item()
 
 
-class MixtureFunction(torch.autograd.Function):
-    """tokens [T,H], expert ids and weights -> the weighted sum of experts' outputs, where
-    `run_experts` maps rows in expert order and their offsets to rows of the same shape and is
-    differentiable in the rows."""
+class Gather(torch.autograd.Function):
+    """Tokens [T,H] -> rows [T*top,H] in expert order, zeros for slots without an expert."""
 
     @staticmethod
-    def forward(ctx, x, ids, weights, experts, run_experts):
-        offsets, slot_pos, _ = b.moe_sort(ids, experts)
-        with torch.enable_grad():
-            rows = b.moe_gather(x, slot_pos).requires_grad_()
-            outputs = run_experts(rows, offsets)
-        ctx.rows, ctx.outputs = rows, outputs
-        ctx.save_for_backward(slot_pos, weights)
-        return b.moe_combine(outputs.detach(), slot_pos, weights)
+    def forward(ctx, x, slot_pos):
+        ctx.save_for_backward(slot_pos)
+        return b.moe_gather(x, slot_pos)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_rows):
+        slot_pos, = ctx.saved_tensors
+        return b.moe_gather_backward(d_rows.contiguous(), slot_pos), None
+
+
+class Combine(torch.autograd.Function):
+    """Rows in expert order and the router's weights -> their weighted sums [T,H]."""
+
+    @staticmethod
+    def forward(ctx, rows, slot_pos, weights):
+        rows, weights = rows.contiguous(), weights.contiguous()
+        ctx.save_for_backward(rows, slot_pos, weights)
+        return b.moe_combine(rows, slot_pos, weights)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, d_out):
-        slot_pos, weights = ctx.saved_tensors
-        d_outputs, d_weights = b.moe_combine_backward(d_out.contiguous(), ctx.outputs.detach(), slot_pos, weights)
-        d_rows, = torch.autograd.grad(ctx.outputs, ctx.rows, d_outputs)
-        return b.moe_gather_backward(d_rows.contiguous(), slot_pos), None, d_weights, None, None
+        rows, slot_pos, weights = ctx.saved_tensors
+        d_rows, d_weights = b.moe_combine_backward(d_out.contiguous(), rows, slot_pos, weights)
+        return d_rows, None, d_weights
+
+
+class MixtureFunction:
+    """tokens [T,H], expert ids and weights -> the weighted sum of experts' outputs, where
+    `run_experts` maps rows in expert order and their offsets to rows of the same shape (those past
+    the last offset have no expert and count for nothing). Gradients reach the tokens, the weights and,
+    through `run_experts`, whatever parameters it uses."""
+
+    @staticmethod
+    def apply(x, ids, weights, experts, run_experts):
+        offsets, slot_pos, _ = b.moe_sort(ids, experts)
+        outputs = run_experts(Gather.apply(x, slot_pos), offsets)
+        return Combine.apply(outputs, slot_pos, weights)
 
 
 def main(tokens=256, experts=8, top=2, hidden=1024, ffn=512, steps=30, rate=0.001):
