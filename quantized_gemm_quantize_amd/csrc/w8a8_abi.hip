@@ -517,6 +517,15 @@ static w8a8_status expert_entry(const uint8_t *xq, const uint8_t *xs, int64_t T,
                                          static_cast<hipStream_t>(stream)));
 }
 
+// Not part of the interface (the tests ask it which sizes reach which kernel): the form of a
+// product's workgroups on a device of `cus` compute units, as stream * 10^9 + rows * 10^6 +
+// channels * 10^3 + wavefronts.
+extern "C" int mxfp4_debug_form(int64_t S, int64_t E, int grouped, int64_t N, int64_t K, int epilogue,
+                                int64_t cus) {
+    const mxfp4::Form f = mxfp4::product_form(mxfp4::Rows{S, E, grouped != 0}, (int)N, (int)K, epilogue, cus);
+    return (f.stream ? 1000000000 : 0) + f.rows * 1000000 + f.channels * 1000 + f.waves;
+}
+
 w8a8_status mxfp4_expert_gemm(const uint8_t *xq, const uint8_t *xs, int64_t T,
                               const int32_t *row_token, int64_t S, const int32_t *offsets,
                               int64_t E, const uint8_t *wq, const uint8_t *ws, int64_t N,
