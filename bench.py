@@ -27,7 +27,8 @@ The line also carries:
   peaks        reference rates measured on the same GPU in the same run
                (libpeaks.so): the int8 MFMA issue rate of back-to-back
                v_mfma_i32_32x32x32_i8 (and the bf16 rate of
-               v_mfma_f32_32x32x16_bf16) with the shader clock it ran at
+               v_mfma_f32_32x32x16_bf16, the MXFP4 rate of
+               v_mfma_scale_f32_32x32x64_f8f6f4) with the shader clock it ran at
                (s_memtime against the 100 MHz reference), HBM streaming read
                and write rates over 1 GiB, and the time to stream-read 16.8 MB
                (the M=16 weight matrix) with the buffers rotated past the
@@ -37,7 +38,9 @@ The line also carries:
                (its tiles, tile order, direct-to-LDS ring and barriers, no
                arithmetic) over operand sets rotated past the Infinity Cache
                (roofline.operand_stream_us and frac_of_operand_stream on the
-               prefill line), and over one set that stays in the cache.
+               prefill line), and over one set that stays in the cache, and the
+               time of a 256-element stage of the MXFP4 GEMM's 256 x 256 tiles'
+               operand stream (8192 x 8192 x 8192).
                roofline.frac_measured is the kernel's rate
                against these (for HBM-bound kernels: the time its read and
                write bytes take at the measured rates, over its time);
@@ -264,8 +267,11 @@ def measure_peaks(torch, eager=False):
     lib.peaks_write.argtypes = [p, i64, i32, p]
     lib.peaks_read_rows.argtypes = [p, i32, p, p]
     lib.peaks_operand_stream.argtypes = [p, p, i32, i32, i32, p, p]
-    for f in (lib.peaks_mfma_i8, lib.peaks_mfma_bf16, lib.peaks_read, lib.peaks_write,
-              lib.peaks_read_rows, lib.peaks_operand_stream):
+    lib.peaks_mfma_mxfp4.argtypes = [i32, i32, p, p, p]
+    lib.peaks_operand_stream256.argtypes = [p, p, i32, i32, i32, p, p]
+    for f in (lib.peaks_mfma_i8, lib.peaks_mfma_bf16, lib.peaks_mfma_mxfp4, lib.peaks_read,
+              lib.peaks_write, lib.peaks_read_rows, lib.peaks_operand_stream,
+              lib.peaks_operand_stream256):
         f.restype = i32
     dev = torch.device("cuda:0")
     cus = torch.cuda.get_device_properties(0).multi_processor_count
@@ -290,6 +296,13 @@ def measure_peaks(torch, eager=False):
     cb = clk.cpu().tolist()
     bf16_tflops = wgs * 4 * iters * 8 * 32768 / (ms_bf16 * 1e-3) / 1e12
     bf16_mhz = cb[0] / (cb[1] / 100e6) / 1e6 if cb[1] else None
+
+    mx = lambda i: call(lib.peaks_mfma_mxfp4(wgs, iters, sink.data_ptr(), clk.data_ptr(), stream()))
+    mx(0)
+    ms_mx = time_median(mx, 20, torch, 1, eager)
+    cm = clk.cpu().tolist()
+    mx_tflops = wgs * 4 * iters * 8 * 131072 / (ms_mx * 1e-3) / 1e12
+    mx_mhz = cm[0] / (cm[1] / 100e6) / 1e6 if cm[1] else None
 
     nbytes = 1 << 30
     big = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -331,9 +344,22 @@ def measure_peaks(torch, eager=False):
                                                  Mp, Np, Kp, osink.data_ptr(), stream()))
     operand_cached_us = time_median(oc, 10 * Ro, torch, 1, eager) * 1e3
     del ops
+    # the MXFP4 GEMM's 256 x 256 tiles, 8192 x 8192 x 8192 (4096 bytes of codes per row)
+    Mx = 8192
+    qa, qb = (torch.empty(Mx * Mx // 2, dtype=torch.uint8, device=dev) for _ in range(2))
+    for t in (qa, qb):
+        call(lib.peaks_write(t.data_ptr(), Mx * Mx // 2, 8 * cus, stream()))
+    qsink = torch.zeros((Mx // 256) ** 2 * 512, dtype=torch.int32, device=dev)
+    oq = lambda i: call(lib.peaks_operand_stream256(qa.data_ptr(), qb.data_ptr(), Mx, Mx, Mx // 2,
+                                                    qsink.data_ptr(), stream()))
+    tiles = -(-(Mx // 256) ** 2 // cus)
+    mx_stage_us = time_median(oq, 20, torch, 1, eager) * 1e3 / (tiles * Mx // 256)
+    del qa, qb
     torch.cuda.synchronize()
     return {"mfma_int8_TOPs": round(mfma_tops, 1), "mfma_loop_shader_MHz": round(shader_mhz, 1),
             "mfma_bf16_TFLOPs": round(bf16_tflops, 1), "mfma_bf16_loop_shader_MHz": round(bf16_mhz, 1),
+            "mfma_mxfp4_TFLOPs": round(mx_tflops, 1), "mfma_mxfp4_loop_shader_MHz": round(mx_mhz, 1),
+            "mxfp4_operand_stream_stage_us": round(mx_stage_us, 3),
             "hbm_read_GBps": round(read_gbs, 1), "hbm_write_GBps": round(write_gbs, 1),
             "read_16_8MB_us": round(read_small_us, 3),
             "read_16_8MB_GBps": round(small / (read_small_us * 1e-6) / 1e9, 1),
@@ -343,7 +369,8 @@ def measure_peaks(torch, eager=False):
             "prefill_operand_stream_GBps_per_CU": round((256 + 128) * Kp / (operand_us * 1e-6) / 1e9, 1),
             "prefill_operand_stream_cached_us": round(operand_cached_us, 3),
             "method": "libpeaks.so: 8 independent v_mfma_i32_32x32x32_i8 (and, separately, "
-                      "v_mfma_f32_32x32x16_bf16) chains per wavefront, "
+                      "v_mfma_f32_32x32x16_bf16, v_mfma_scale_f32_32x32x64_f8f6f4 on 4-bit codes) "
+                      "chains per wavefront, "
                       f"{wgs} workgroups of 4 wavefronts; 16-byte loads / streaming stores over "
                       "1 GiB; 16.8 MB reads over rotated buffers, grid-stride and in the M-small "
                       "GEMM's row-slice pattern (256 workgroups, 16 loads per lane in flight); "

@@ -10,6 +10,8 @@
 //   so the multipliers toggle as under real data.
 // peaks_mfma_bf16: the same with v_mfma_f32_32x32x16_bf16 (32768 flops each;
 //   operands are finite bf16 values in [1, 2) whose mantissas vary per lane).
+// peaks_mfma_mxfp4: the same with v_mfma_scale_f32_32x32x64_f8f6f4 on 4-bit codes
+//   (131072 flops each; all bits of the codes vary per lane, scales of 1).
 // peaks_read: every thread reads 16-byte chunks, grid-stride, with the
 //   nontemporal hint (as the kernels that read their weights once do), and
 //   folds them into one word per thread (written once, so the loads cannot be
@@ -20,6 +22,9 @@
 //   tiles in its tile order, 128-byte K stages through a 3-stage direct-to-LDS
 //   ring with its counted waits and one barrier per stage; no fragment reads,
 //   MFMAs or epilogue): the time that kernel's loads take by themselves.
+// peaks_operand_stream256: the same for the MXFP4 GEMM's 256 x 256 tiles (8
+//   wavefronts, stages of 512 rows x 128 bytes in two buffers; the codes without
+//   their scales, a 16th of them).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -91,6 +96,41 @@ __global__ __launch_bounds__(256) void mfma_loop_bf16(int iters, int *sink, uint
     }
 }
 
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+__global__ __launch_bounds__(256) void mfma_loop_mxfp4(int iters, int *sink, uint64_t *clk) {
+    const uint32_t lane = threadIdx.x;
+    const uint64_t c0 = __builtin_amdgcn_s_memtime(), r0 = __builtin_amdgcn_s_memrealtime();
+    // 32 codes per operand in the first four registers
+    v8i a = {}, b = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[i] = (int)(lane * 2654435761u + i * 977u);
+        b[i] = (int)(lane * 2246822519u + i * 40503u);
+    }
+    v16f acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = v16f{};
+    for (int it = 0; it < iters; ++it) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i], 4, 4, 0, 127, 0, 127);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] ^= it;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += acc[i][e];
+    if (s == 0.123f) sink[blockIdx.x] = 1;  // never (sums of multiples of 1/4): keeps the loop alive
+    const uint64_t c1 = __builtin_amdgcn_s_memtime(), r1 = __builtin_amdgcn_s_memrealtime();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        clk[0] = c1 - c0;
+        clk[1] = r1 - r0;
+    }
+}
+
 __global__ __launch_bounds__(256) void read_loop(const uint4 *__restrict__ p, int64_t n16,
                                                  uint32_t *__restrict__ sink) {
     uint32_t s = 0;
@@ -135,18 +175,19 @@ __device__ __forceinline__ void vm_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// A [M, K] and B [N, K] int8 (M % 256 == 0, N % 128 == 0, K % 128 == 0),
-// one workgroup of 4 wavefronts per 256 x 128 tile. Tile order: each XCD
+// A [M, K] and B [N, K] bytes (M % BM == 0, N % BN == 0, K % 128 == 0), one
+// workgroup of WAVES wavefronts per BM x BN tile. Tile order: each XCD
 // (workgroup i runs on XCD i % 8) owns a contiguous range of tiles, taken in
-// groups of 4 tile rows. A stage is 384 rows x 128 bytes: load l of wavefront
-// w fills 16-byte slots 64 (w + 4 l) .. of the stage, 8 rows x 128 bytes
+// groups of 4 tile rows. A stage is BM + BN rows x 128 bytes: load l of wavefront
+// w fills 16-byte slots 64 (w + WAVES l) .. of the stage, 8 rows x 128 bytes
 // (chunk c of row r lands at slot 8 r + (c ^ (r % 8) ^ ((r / 8) % 2))). Stage
 // s + 2 is issued before stage s + 1 is awaited.
-__global__ __launch_bounds__(256, 1) void operand_stream(const int8_t *__restrict__ A,
-                                                         const int8_t *__restrict__ B, int K,
-                                                         int tiles_m, int tiles_n, uint32_t *sink) {
-    constexpr int BM = 256, BN = 128, STAGE = (BM + BN) * 8, A_LD = BM / 32, NLD = (BM + BN) / 32;
-    __shared__ uint4 lds[3 * STAGE];
+template <int BM, int BN, int RING, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 1) void operand_stream(const int8_t *__restrict__ A,
+                                                                const int8_t *__restrict__ B, int K,
+                                                                int tiles_m, int tiles_n, uint32_t *sink) {
+    constexpr int STAGE = (BM + BN) * 8, PASS = 8 * WAVES, A_LD = BM / PASS, NLD = (BM + BN) / PASS;
+    __shared__ uint4 lds[RING * STAGE];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int tiles = tiles_m * tiles_n;
     const int q = tiles / 8, r = tiles % 8, xcd = blockIdx.x % 8, idx = blockIdx.x / 8;
@@ -154,20 +195,20 @@ __global__ __launch_bounds__(256, 1) void operand_stream(const int8_t *__restric
     const int per_group = 4 * tiles_n, first_m = (t / per_group) * 4;
     const int gsize = min(tiles_m - first_m, 4);
     const int m0 = (first_m + (t % per_group) % gsize) * BM, n0 = ((t % per_group) / gsize) * BN;
-    const int row = 8 * wave + (lane >> 3);  // + 32 l
+    const int row = 8 * wave + (lane >> 3);  // + PASS l
     const int kc = (lane & 7) ^ (row & 7) ^ ((row >> 3) & 1);
     const int8_t *src[NLD];
 #pragma unroll
     for (int l = 0; l < NLD; ++l)
-        src[l] = l < A_LD ? A + (int64_t)(m0 + row + 32 * l) * K + 16 * kc
-                          : B + (int64_t)(n0 + row + 32 * (l - A_LD)) * K + 16 * kc;
+        src[l] = l < A_LD ? A + (int64_t)(m0 + row + PASS * l) * K + 16 * kc
+                          : B + (int64_t)(n0 + row + PASS * (l - A_LD)) * K + 16 * kc;
     const int nk = K / 128;
     auto issue = [&](int s) {
-        uint4 *dst = lds + (s % 3) * STAGE;
+        uint4 *dst = lds + (s % RING) * STAGE;
         const int k0 = 128 * min(s, nk - 1);  // stages past the last reload the last
 #pragma unroll
         for (int l = 0; l < NLD; ++l)
-            __builtin_amdgcn_global_load_lds((global_void *)(src[l] + k0), (lds_void *)(dst + 64 * (wave + 4 * l)),
+            __builtin_amdgcn_global_load_lds((global_void *)(src[l] + k0), (lds_void *)(dst + 64 * (wave + WAVES * l)),
                                              16, 0, 0);
     };
     issue(0);
@@ -211,6 +252,13 @@ int peaks_mfma_bf16(int workgroups, int iters, int *sink, uint64_t *clk, void *s
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
+// As peaks_mfma_i8, with 4-bit operands: the flops are workgroups * 4 * iters * 8 * 131072.
+int peaks_mfma_mxfp4(int workgroups, int iters, int *sink, uint64_t *clk, void *stream) {
+    if (workgroups <= 0 || iters <= 0 || !sink || !clk) return -1;
+    mfma_loop_mxfp4<<<workgroups, 256, 0, static_cast<hipStream_t>(stream)>>>(iters, sink, clk);
+    return hipGetLastError() == hipSuccess ? 0 : -7;
+}
+
 // bytes: a multiple of 16; sink: at least workgroups * 256 words.
 int peaks_read(const void *buf, int64_t bytes, int workgroups, uint32_t *sink, void *stream) {
     if (bytes <= 0 || bytes % 16 || workgroups <= 0 || !buf || !sink) return -1;
@@ -233,7 +281,17 @@ int peaks_read_rows(const void *buf, int rows, uint32_t *sink, void *stream) {
 int peaks_operand_stream(const void *a, const void *b, int M, int N, int K, uint32_t *sink, void *stream) {
     if (!a || !b || !sink || M <= 0 || N <= 0 || K <= 0 || M % 256 || N % 128 || K % 128) return -1;
     const int tm = M / 256, tn = N / 128;
-    operand_stream<<<tm * tn, 256, 0, static_cast<hipStream_t>(stream)>>>(
+    operand_stream<256, 128, 3, 4><<<tm * tn, 256, 0, static_cast<hipStream_t>(stream)>>>(
+        static_cast<const int8_t *>(a), static_cast<const int8_t *>(b), K, tm, tn, sink);
+    return hipGetLastError() == hipSuccess ? 0 : -7;
+}
+
+// a: [M, K], b: [N, K] bytes; M and N positive multiples of 256, K of 128; sink: at
+// least (M / 256) * (N / 256) * 512 words.
+int peaks_operand_stream256(const void *a, const void *b, int M, int N, int K, uint32_t *sink, void *stream) {
+    if (!a || !b || !sink || M <= 0 || N <= 0 || K <= 0 || M % 256 || N % 256 || K % 128) return -1;
+    const int tm = M / 256, tn = N / 256;
+    operand_stream<256, 256, 2, 8><<<tm * tn, 512, 0, static_cast<hipStream_t>(stream)>>>(
         static_cast<const int8_t *>(a), static_cast<const int8_t *>(b), K, tm, tn, sink);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
