@@ -101,22 +101,23 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 __global__ __launch_bounds__(256) void mfma_loop_mxfp4(int iters, int *sink, uint64_t *clk) {
     const uint32_t lane = threadIdx.x;
     const uint64_t c0 = __builtin_amdgcn_s_memtime(), r0 = __builtin_amdgcn_s_memrealtime();
-    // 32 codes per operand in the first four registers
-    v8i a = {}, b = {};
+    // 32 codes per operand in the first four registers; as in a tile, no two products in
+    // a row have the same pair (repeated pairs switch less, and run at a higher clock)
+    v8i a[4] = {}, b[2] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        a[i] = (int)(lane * 2654435761u + i * 977u);
-        b[i] = (int)(lane * 2246822519u + i * 40503u);
-    }
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[j][i] = (int)(lane * 2654435761u + j * 40503u + i * 97777777u);
+            if (j < 2) b[j][i] = (int)(lane * 2246822519u + j * 7919u + i * 13131313u);
+        }
     v16f acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = v16f{};
     for (int it = 0; it < iters; ++it) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i], 4, 4, 0, 127, 0, 127);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] ^= it;
+            acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[i / 2], b[i % 2], acc[i], 4, 4, 0, 127, 0, 127);
     }
     float s = 0.0f;
 #pragma unroll
