@@ -1,8 +1,9 @@
-// Weight-streaming MXFP4 products (few rows): a dense layer of up to 64 rows, or
-// groups of a few rows each.
+// Weight-streaming MXFP4 products: a dense layer of up to 32 rows, or of more in parts
+// of 64 while that fills the CUs better than tiles, or groups of a few rows each
+// (product_form in mxfp4_gemm.hip).
 //
-// With few rows the kernel is bound by reading each weight in use from HBM
-// once. A workgroup owns 16 CT channels of one group's weight and up to 16 MT
+// With few rows the kernel is bound by reading each weight in use from HBM, once for
+// every 16 MT rows. A workgroup owns 16 CT channels of one group's weight and up to 16 MT
 // of its rows; its WAVES wavefronts split K in pairs of 128 bytes of codes (256
 // elements), wavefront w taking pairs w, w + WAVES, ..., so that neighbouring
 // wavefronts read neighbouring cache lines. Measured: 1 x 4096 x 4096 (8.9

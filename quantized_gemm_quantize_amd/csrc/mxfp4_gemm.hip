@@ -61,6 +61,12 @@ Form tiled_form(const Rows &r, int N, int K, int epilogue, int64_t cus) {
 // 5.4, 4.8, 5.9 / 7.5; M = 64 8.0, 7.9, 6.6 / 8.1; M = 96 11.8, 11.4, 9.0 / 8.0;
 // 257 x 1040 x 1312 5.5, 6.2, 4.4 / 5.1. 32 experts' down products [4096, 2048],
 // 8 rows each on average 24.9, 26.8, 36.1 / 32.1, 32 rows 47.9, 39.4, 45.3 / 36.2.
+// More than 32 dense rows stream, 64 at a time by 16 channels, while tiles would
+// leave half the CUs idle and the streaming workgroups, each of which reads its rows and
+// its channels itself, run at once, or K is short and the starts count (streaming
+// against tiles, us: 64 x 1040 x 4096 5.8 / 7.2, 1000 x 256 x 8192 9.6 / 12.3, 8000 x
+// 16 x 4096 7.6 / 7.9; past the CUs 257 x 1040 3.7 / 4.6 for K = 1024, 9.6 / 8.0 for
+// 4096, 1500 x 304 x 2048 7.7 / 5.6, 8000 x 64 x 8192 27.4 / 12.9).
 Form product_form(const Rows &r, int N, int K, int epilogue, int64_t cus) {
     int row_tiles = 0;  // 16-row tiles that stream the weights together
     if (r.grouped) {
@@ -71,7 +77,8 @@ Form product_form(const Rows &r, int N, int K, int epilogue, int64_t cus) {
         const int64_t tiles = (r.S + 63) / 64 * ((N + 63) / 64);
         if (r.S <= 16) row_tiles = 1;
         else if (r.S <= 32) row_tiles = 2;
-        else if (2 * tiles < cus) row_tiles = 4;  // half the CUs idle with tiles
+        else if (2 * tiles < cus && ((r.S + 63) / 64 * ((N + 15) / 16) <= cus || (K <= 1536 && r.S <= 1024)))
+            row_tiles = 4;
     }
     return row_tiles > 0 ? streaming_form(row_tiles, r, N, epilogue, cus) : tiled_form(r, N, K, epilogue, cus);
 }

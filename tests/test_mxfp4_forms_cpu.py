@@ -44,5 +44,12 @@ def test_every_variant_is_reached(lib):
     assert swiglu == with_swiglu | {(True, r, 64, w, None) for r in (16, 32) for w in (2, 4)}
     dense = {kernel(lib, M, 1, 0, N, K, 2) for M, N in DENSE for K in DEPTHS}
     assert dense == tails | {(True, 16, 16, 8, None), (True, 32, 16, 8, None), (True, 64, 16, 4, None)}
-    # tall and narrow: streamed whatever the number of rows
-    assert kernel(lib, 8000, 1, 0, 16, 1024, 2)[0] and not kernel(lib, 8200, 1, 0, 16, 1024, 2)[0]
+
+
+@pytest.mark.parametrize("M,N,K,streams", [(8000, 16, 8192, True), (8000, 64, 1024, False), (8000, 48, 8192, False),
+                                           (3000, 96, 2048, False), (1000, 256, 8192, True), (257, 1040, 1312, True),
+                                           (257, 1040, 4096, False), (1000, 304, 1024, True), (1500, 304, 1024, False)])
+def test_tall_narrow_layers(lib, M, N, K, streams):
+    """The streaming kernel takes dense rows past 64 only while its workgroups run at once, or K is
+    short (measured at these sizes, the other kernel takes up to 2.1 times as long)."""
+    assert kernel(lib, M, 1, 0, N, K, 2)[0] == streams
