@@ -15,8 +15,10 @@
 // results do not depend on how the work is spread. The rows' kernels are bound
 // by HBM and go token by token, so that each token is read once. Measured, 16448
 // tokens x 4 slots x 4096 bf16: gather 121 us (674 MB, 5.6 TB/s), combine 111 (6.1),
-// its backward 230 (1.21 GB, 5.3), the gather's 110; the sort of the 65792 slots,
-// bound by the latency of its two launches, 11, of 16.8 million 128 (three launches).
+// its backward 232 (1.21 GB, 5.2), the gather's 111; rows that are no multiple of 16
+// bytes: 4098 elements gather 239, combine 165, backward 389, 4095 195, 132, 407. The sum
+// of a layer's fp32 rows, 8192 tokens x 4, 100 (604 MB, 6.0). The sort of the 65792
+// slots, bound by the latency of its two launches, 12, of 16.8 million 128 (three).
 #include <type_traits>
 
 #include "launch.hpp"

@@ -28,15 +28,18 @@
 //    16-byte pieces of contiguous rows; SwiGLU joins gate and up in registers
 //    and stores the hidden activations as MXFP4, 17/64 of their bf16 bytes.
 //
-// What bounds it (8192 x 8192, by K): 20 us for the stores (134 MB, 6.7 TB/s) and
-// the starts, and 1.6 us for each K stage of the 256 x 256 tiles, 5.1 PFLOP/s over
-// the chip, where the MFMA loop alone reaches 5.3-6.5 (its clock falls under the
-// load). Alone, a stage's 68 KB of operands take 1.27 us: 64 reads of 128 bytes
-// in flight per CU at a latency of about 300 clocks, 27 bytes per clock, whatever
-// the address pattern; so a tile with more products per byte is faster until
-// too few tiles are left (tiled_form in mxfp4_gemm.hip). 2048 x 4096 x 4096 20 us, 38400
-// x 4096 x 1024 119 us, 32 experts' gate and up of 8192 tokens x 4 302 us, their
-// down products 167 us.
+// What bounds it (8192 x 8192, weights and rows in the Infinity Cache): 34 us for the
+// stores (134 MB, 20 us at 6.7 TB/s), the starts and the tiles' ends, and 1.66 us
+// (K = 2048 to 4096; 1.78 to 8192, where the clock falls) for each K stage of the 256 x
+// 256 tiles: 5.2 PFLOP/s, where the MFMA loop alone reaches 5.7 with one wavefront
+// per SIMD and 6.6 with two. A stage's operands alone, two stages under way, take
+// 0.71 us (92 GB/s per CU); so the MFMAs, two thirds of a stage's clocks, are what it waits
+// for most, and the rest are the barrier and the loads that start behind it. A tile with
+// more products per byte is faster until too few tiles are left (tiled_form in
+// mxfp4_gemm.hip). 2048 x 4096 x 4096 20-21 us, 38400 x 4096 x 1024 111 us (124
+// in a loop of products alone), 32 experts' gate and up of 8192 tokens x 4 310 us, their
+// down products to fp32 242 us (199 with the weights in the Infinity Cache; to bf16
+// 200 and 179).
 #include <algorithm>
 
 #include "launch.hpp"
