@@ -1,12 +1,16 @@
 """MXFP4 products through every compiled variant of their kernels, ragged groups, empty experts and
 dropped slots among them, against 64 bits."""
+import os
+
 import numpy as np
 import pytest
 import torch
 
 import mx_reference as ref
+from gpu_layer import library
 from mxfp4_sizes import DENSE, DEPTHS, GROUPED
 from quantized_gemm_quantize_amd import binding as b
+from quantized_gemm_quantize_amd import build
 from test_gpu_moe import check_hidden, routing
 from test_gpu_mxfp4 import DEV, HALF_ULP, TINY, TYPES, packed, rows
 
@@ -121,3 +125,32 @@ def test_few_slots_of_wide_tokens(T, top, E, H, F, dtype):
             want[t] += weights[t, j].item() * (h @ values(w2q[e], w2s[e]).cpu().numpy().T)[0]
     err = np.linalg.norm(out.double().cpu().numpy() - want)
     assert err <= (2.0 ** -8 + 2 * HALF_ULP[dtype]) * np.linalg.norm(want)
+
+
+def test_lds_poisoned_build_gives_the_same():
+    """Every variant again in the build whose kernels fill their LDS with a pattern first: a read of LDS
+    that the launch has not written would change the bits."""
+    if not os.path.exists(build.POISON_LIB):
+        pytest.skip("the LDS-poisoned build is missing")
+    ks = (64, 288, 512, 768, 1312)
+    cases = []
+    for T, top, E, N in GROUPED:
+        _, _, offsets, token = plan(T, top, E, seed=T)
+        for K in ks:
+            cases.append((storage((), T, K, 122, 126, seed=1), offsets, storage((E,), N, K, 120, 124, seed=2), token))
+    dense = [(storage((), M, K, 118, 126, seed=1), storage((), N, K, 118, 126, seed=2)) for M, N in DENSE for K in ks]
+
+    def run():
+        out = []
+        for x, offsets, w, token in cases:
+            out.append(b.mxfp4_expert_gemm(*x, offsets, *w, row_token=token))
+            out += b.mxfp4_expert_swiglu(*x, offsets, *w, row_token=token)
+        return out + [b.mxfp4_gemm(*x, *w) for x, w in dense]
+
+    want = run()
+    torch.cuda.synchronize()
+    with library(build.POISON_LIB):
+        got = run()
+        torch.cuda.synchronize()
+    for g, v in zip(got, want):
+        assert torch.equal(g.view(torch.uint8), v.view(torch.uint8))
