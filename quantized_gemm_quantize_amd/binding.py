@@ -8,8 +8,8 @@ workspaces) belongs to that stream, as if the call were made under
 torch.cuda.stream(stream); the caller orders the rest: `stream` has to wait for
 inputs and buffers of the caller's that other streams still write or read, other
 streams for the outputs, and a tensor that is dropped while another stream than
-its own uses it needs torch's record_stream. All arithmetic runs in the library's kernels; there is no fallback. If
-libw8a8.so is absent, every entry point raises.
+its own uses it needs torch's record_stream. All arithmetic runs in the library's
+kernels; there is no fallback. If libw8a8.so is absent, every entry point raises.
 """
 from __future__ import annotations
 
@@ -719,7 +719,8 @@ def mxfp4_moe(x, expert_ids, weights, w13q, w13s, w2q, w2s, out=None, workspace=
     through the experts' gate/up weights w13 [E,2F,H] with SwiGLU and down weights w2 [E,H,F]
     (both MXFP4), and summed with the router's weights [T,top] (float32) -> out [T,H] of x's
     dtype. The experts' outputs and the sum are held in float32 and rounded once; a float16 layer
-    of more than a few slots rounds the experts' outputs to float16's precision too. workspace: uint8 of at least mxfp4_moe_workspace(...) bytes (a new one if None)."""
+    of more than a few slots rounds the experts' outputs to float16's precision too. workspace:
+    uint8 of at least mxfp4_moe_workspace(...) bytes (a new one if None)."""
     dt, ld, T, H = _float_rows(x, "x")
     T2, top, bits = _expert_ids(expert_ids)
     _routing_weights(weights, T, top)
