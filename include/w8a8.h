@@ -66,7 +66,7 @@ typedef enum {
     W8A8_ERR_BLOCKSIZE = -5,  /* BSR block size other than 64 */
     W8A8_ERR_DTYPE = -6,      /* unknown output dtype selector */
     W8A8_ERR_HIP = -7,        /* the HIP runtime reported an error at launch */
-    W8A8_ERR_VALUE = -8       /* a scalar argument (alpha, beta) is not finite */
+    W8A8_ERR_VALUE = -8       /* a scalar argument (alpha, beta, scale, eps) is not finite, or eps not positive */
 } w8a8_status;
 
 typedef enum {
@@ -482,6 +482,135 @@ w8a8_status mxfp4_moe(const void *x, int64_t ldx, mxfp4_dtype dtype, int64_t T, 
                       int64_t E, const uint8_t *w13q, const uint8_t *w13s, const uint8_t *w2q,
                       const uint8_t *w2s, int64_t F, void *out, void *workspace,
                       int64_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Around a layer: the norms with the residual stream, products with an epilogue.
+ */
+
+/* Activations of the epilogues, computed in fp32: v; max(v, 0); v P(v) with P the
+ * normal distribution function; the tanh form of it, v (1 + tanh(sqrt(2 / pi) (v +
+ * 0.044715 v^3))) / 2; v / (1 + exp(-v)). */
+typedef enum {
+    W8A8_ACT_NONE = 0,
+    W8A8_ACT_RELU = 1,
+    W8A8_ACT_GELU = 2,
+    W8A8_ACT_GELU_TANH = 3,
+    W8A8_ACT_SILU = 4
+} w8a8_activation;
+
+/*
+ * Dense W8A8 GEMM with bias, activation and residual in its epilogue (bf16 output):
+ *   out[m,n] = bf16_rne(act(acc * x_scale[m] * w_scale[n] + bias[n]) + residual[m,n])
+ * in fp32, rounded once. bias [N] fp32 and residual (bf16 rows, row stride ldr >= N
+ * elements) may be NULL; residual may be out itself (with ldr = N). Other arguments as
+ * w8a8_gemm.
+ * Errors: NULL, SHAPE (also ldr < N or > 2^31 - 1), K_OVERFLOW, ALIGN (bias and
+ *         residual included, 2 * ldr % 16), DTYPE (activation), HIP.
+ */
+w8a8_status w8a8_gemm_act(const int8_t *xq, const float *x_scale, int64_t M, const int8_t *wq,
+                          const float *w_scale, int64_t N, int64_t K, const float *bias,
+                          w8a8_activation activation, const void *residual, int64_t ldr, void *out,
+                          void *stream);
+
+/*
+ * 16-bit products: layers that stay in bf16 or binary16 beside the quantized ones, served
+ * and trained. x [M,K] (row stride ldx >= K), w [N,K], both of dtype:
+ *   pre[m,n] = sum_k x[m,k] w[n,k] + bias[n]
+ *   out[m,n] = act(pre[m,n]) + residual[m,n]
+ * accumulated in fp32, out and pre (NULL: not wanted) each rounded once to dtype, [M,N].
+ * bias [N] fp32 and residual (row stride ldr >= N) may be NULL; residual may be out
+ * itself (with ldr = N). N and K positive multiples of 8 up to W16A16_MAX_WIDTH, M < 2^27,
+ * M * N, M * K and N * K at most 2^35.
+ * Few rows or few tiles of a long K are split over K and joined in a workspace: device,
+ * 16-byte aligned, at least w16a16_linear_workspace(M, N, K) bytes (may be 0: then NULL).
+ * Errors: NULL, SHAPE (also a workspace that is too small), ALIGN (rows included: 2 * ld
+ *         % 16), DTYPE (dtype, activation), HIP.
+ */
+#define W16A16_MAX_WIDTH 1048576
+int64_t w16a16_linear_workspace(int64_t M, int64_t N, int64_t K);
+w8a8_status w16a16_linear(const void *x, int64_t ldx, int64_t M, const void *w, int64_t N,
+                          int64_t K, w4a16_dtype dtype, const float *bias,
+                          w8a8_activation activation, const void *residual, int64_t ldr, void *pre,
+                          void *out, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of w16a16_linear, from d_out (row stride ldd >= N) and the pre that it wrote:
+ *   d_pre = d_out act'(pre)             [M,N], rounded to dtype: the operand of the products
+ *   d_bias = sum_m d_out act'(pre)      [N] fp32, of the unrounded values
+ *   d_x = d_pre w                       [M,K] of dtype
+ *   d_w = d_pre^T x                     [N,K] of dtype
+ * (the residual's gradient is d_out itself). Without an activation d_pre is d_out: pre
+ * and d_pre are not accessed and may be NULL. d_x, d_w and d_bias may each be NULL: not
+ * wanted. relu's slope at 0 is 0. With M = 0, d_w and d_bias are written as 0. Sums are
+ * made in a fixed order: repeated calls agree bit for bit.
+ * workspace: as above, w16a16_linear_backward_workspace(M, N, K) bytes.
+ * Errors: as w16a16_linear.
+ */
+int64_t w16a16_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
+w8a8_status w16a16_linear_backward(const void *d_out, int64_t ldd, const void *x, int64_t ldx,
+                                   const void *w, const void *pre, int64_t M, int64_t N, int64_t K,
+                                   w4a16_dtype dtype, w8a8_activation activation, void *d_pre,
+                                   void *d_x, void *d_w, float *d_bias, void *workspace,
+                                   int64_t workspace_bytes, void *stream);
+
+/*
+ * The step between two blocks: the output y of a block joins the residual stream, which
+ * is normalized for the next one. rms(v) = sqrt(sum_h v[h]^2 / H + eps) per row:
+ *   u  = y, or with post_norm  y / rms(y) * post_weight
+ *   r' = residual + scale * gate * u        -> new_residual [T,H], rounded to dtype
+ *   o  = r' / rms(r') * weight (of the unrounded r')
+ * block_norm writes o as rows of dtype, out [T,H]; block_norm_w8a8 as w8a8_quantize_rows
+ * would quantize the unrounded o (xq [T,H], x_scale [T]; H a multiple of 16);
+ * block_norm_mxfp4 as mxfp4_quantize_rows would (codes [T,H/2], scales [ceil(H/256),T,8];
+ * H a multiple of 32).
+ * residual, y and gate are rows of dtype with strides ldr, ldy, ldg >= H. gate NULL: 1;
+ * ldg = 0: gate is one fp32 vector [H] for all rows. weight and post_weight are fp32 [H],
+ * NULL: ones. y NULL: the plain norm of residual (new_residual is not written and may be
+ * NULL; gate, post_norm and scale have no effect). new_residual may be residual or y (of
+ * stride H). Everything is computed in fp32: squares of a row have to sum up within its range.
+ * 0 <= T < 2^24, 1 <= H <= BLOCK_NORM_MAX_H, T * H <= 2^34; rows need the alignment of
+ * their elements only, vectors, codes and scales 16 bytes.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, VALUE (scale not finite, eps not finite or not
+ *         positive), HIP.
+ */
+#define BLOCK_NORM_MAX_H 16384
+w8a8_status block_norm(const void *residual, int64_t ldr, const void *y, int64_t ldy,
+                       int post_norm, const float *post_weight, const void *gate, int64_t ldg,
+                       float scale, const float *weight, float eps, int64_t T, int64_t H,
+                       mxfp4_dtype dtype, void *new_residual, void *out, void *stream);
+w8a8_status block_norm_w8a8(const void *residual, int64_t ldr, const void *y, int64_t ldy,
+                            int post_norm, const float *post_weight, const void *gate,
+                            int64_t ldg, float scale, const float *weight, float eps, int64_t T,
+                            int64_t H, mxfp4_dtype dtype, void *new_residual, int8_t *xq,
+                            float *x_scale, void *stream);
+w8a8_status block_norm_mxfp4(const void *residual, int64_t ldr, const void *y, int64_t ldy,
+                             int post_norm, const float *post_weight, const void *gate,
+                             int64_t ldg, float scale, const float *weight, float eps, int64_t T,
+                             int64_t H, mxfp4_dtype dtype, void *new_residual, uint8_t *codes,
+                             uint8_t *scales, void *stream);
+
+/*
+ * Gradients of block_norm from those of out (d_out) and of new_residual (d_new, NULL: 0),
+ * given new_residual as it was written (without y: the residual that was normalized).
+ * Rows have strides ldo, ldn, ldr, ldy, ldg. Outputs:
+ *   d_residual [T,H] of dtype; d_y [T,H] of dtype (with y)
+ *   d_gate of dtype [T,H], or fp32 [H] for a vector (ldg = 0); may be NULL
+ *   d_weight, d_post_weight fp32 [H], may be NULL (d_post_weight is written with
+ *   post_norm only)
+ * Vectors are sums over the rows in a fixed order, 0 with T = 0. d_residual may be d_new
+ * or d_out, d_y may be y and d_gate the gate's rows (each of stride H).
+ * workspace: device, 16-byte aligned, block_norm_backward_workspace(T, H) bytes (0 for no
+ * rows).
+ * Errors: as block_norm; SHAPE when workspace_bytes is too small.
+ */
+int64_t block_norm_backward_workspace(int64_t T, int64_t H);
+w8a8_status block_norm_backward(const void *d_out, int64_t ldo, const void *d_new, int64_t ldn,
+                                const void *new_residual, int64_t ldr, const void *y, int64_t ldy,
+                                int post_norm, const float *post_weight, const void *gate,
+                                int64_t ldg, float scale, const float *weight, float eps,
+                                int64_t T, int64_t H, mxfp4_dtype dtype, void *d_residual,
+                                void *d_y, void *d_gate, float *d_weight, float *d_post_weight,
+                                void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Static, human-readable text for a status code (never NULL). */
 const char *w8a8_status_string(int status);

@@ -96,6 +96,24 @@ def load():
     lib.mxfp4_moe_workspace.argtypes = [i64, i64, i64, i64, i64, i32]
     for fn in ("mxfp4_linear_workspace", "moe_sort_workspace", "mxfp4_moe_workspace"):
         getattr(lib, fn).restype = i64
+    lib.w8a8_gemm_act.argtypes = [p, p, i64, p, p, i64, i64, p, i32, p, i64, p, p]
+    lib.w16a16_linear.argtypes = [p, i64, i64, p, i64, i64, i32, p, i32, p, i64, p, p, p, i64, p]
+    lib.w16a16_linear_backward.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, i32, i32, p, p, p, p,
+                                           p, i64, p]
+    norm = [p, i64, p, i64, i32, p, p, i64, f32, p, f32, i64, i64, i32, p]
+    lib.block_norm.argtypes = norm + [p, p]
+    lib.block_norm_w8a8.argtypes = lib.block_norm_mxfp4.argtypes = norm + [p, p, p]
+    lib.block_norm_backward.argtypes = [p, i64, p, i64, p, i64, p, i64, i32, p, p, i64, f32, p, f32,
+                                        i64, i64, i32, p, p, p, p, p, p, i64, p]
+    for fn in ("w8a8_gemm_act", "w16a16_linear", "w16a16_linear_backward", "block_norm",
+               "block_norm_w8a8", "block_norm_mxfp4", "block_norm_backward"):
+        getattr(lib, fn).restype = i32
+    lib.w16a16_linear_workspace.argtypes = [i64, i64, i64]
+    lib.w16a16_linear_backward_workspace.argtypes = [i64, i64, i64]
+    lib.block_norm_backward_workspace.argtypes = [i64, i64]
+    for fn in ("w16a16_linear_workspace", "w16a16_linear_backward_workspace",
+               "block_norm_backward_workspace"):
+        getattr(lib, fn).restype = i64
     lib.w8a8_status_string.argtypes = [i32]
     lib.w8a8_status_string.restype = ctypes.c_char_p
     lib.w8a8_last_hip_error.argtypes = []
@@ -743,3 +761,279 @@ def mxfp4_moe(x, expert_ids, weights, w13q, w13s, w2q, w2s, out=None, workspace=
 def mxfp4_moe_workspace(T, top, num_experts, H, F, dtype=torch.bfloat16) -> int:
     """Bytes of workspace that mxfp4_moe needs."""
     return load().mxfp4_moe_workspace(T, top, num_experts, H, F, _float_dtype(dtype))
+
+
+# ---------------------------------------------------------------- around a layer
+
+W16A16_MAX_WIDTH = 1048576
+BLOCK_NORM_MAX_H = 16384
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _activation(activation) -> int:
+    try:
+        return ACTIVATIONS[activation]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}") from None
+
+
+def _vector(t, name, n):
+    """The address of an fp32 vector [n], None for none."""
+    if t is None:
+        return None
+    _check(t, name, torch.float32, 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have shape {(n,)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _like_rows(t, name, dtype, rows, width):
+    """(address, row stride) of rows [rows, width] of dtype that may lie apart, (None, 0) for none."""
+    if t is None:
+        return None, 0
+    _, ld, m, n = _float_rows(t, name)
+    if t.dtype is not dtype or m != rows or n != width:
+        raise ValueError(f"{name} must be {dtype} {(rows, width)}, got {t.dtype} {(m, n)}")
+    if ld < width:
+        raise ValueError(f"{name} must have rows of their own, not expanded ones")
+    return t.data_ptr(), ld
+
+
+def _on_device(t, *others):
+    """Refuses tensors of several devices, and a device that is not the current one: the launch would go to
+    the current one."""
+    d = t.get_device()
+    if d != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{d}, the current device is cuda:{torch.cuda.current_device()}")
+    for o in others:
+        if isinstance(o, torch.Tensor) and o.get_device() != d:
+            raise ValueError("all tensors must be on one device")
+
+
+def w8a8_gemm_act(xq, x_scale, wq, w_scale, bias=None, activation="none", residual=None, out=None,
+                  stream=None):
+    """out [M,N] = bf16(act(sum_k xq[m,k] wq[n,k] * x_scale[m] * w_scale[n] + bias[n]) + residual[m,n]);
+    activation "none", "relu", "gelu", "gelu_tanh" or "silu"; bias float32 [N]; residual bfloat16 [M,N]
+    (rows may lie apart), which may be `out` itself."""
+    a = _activation(activation)
+    _check(xq, "xq", torch.int8, 2)
+    _check(x_scale, "x_scale", torch.float32, 1)
+    _check(wq, "wq", torch.int8, 2)
+    _check(w_scale, "w_scale", torch.float32, 1)
+    M, K = xq.shape
+    N, K2 = wq.shape
+    if K2 != K or x_scale.shape[0] != M or w_scale.shape[0] != N:
+        raise ValueError("operand shapes")
+    _on_device(xq, x_scale, wq, w_scale, bias, residual, out)
+    bias = _vector(bias, "bias", N)
+    r, ldr = _like_rows(residual, "residual", torch.bfloat16, M, N)
+    out = _result(out, "out", (M, N), torch.bfloat16, xq, stream)
+    _done(load().w8a8_gemm_act(xq.data_ptr(), x_scale.data_ptr(), M, wq.data_ptr(), w_scale.data_ptr(), N, K,
+                               bias, a, r, ldr, out.data_ptr(), _stream_of(xq, stream)), "w8a8_gemm_act")
+    return out
+
+
+def _linear16_operands(x, w):
+    """(dtype code, x's row stride, M, N, K) of 16-bit rows and their weight."""
+    code, ld, M, K = _float_rows(x, "x")
+    if code == MXFP4_F32:
+        raise TypeError("x must be bfloat16 or float16")
+    _check(w, "w", x.dtype, 2)
+    N, K2 = w.shape
+    if K2 != K:
+        raise ValueError("operand shapes")
+    return code, ld, M, N, K
+
+
+def w16a16_linear(x, w, bias=None, activation="none", residual=None, pre=None, out=None, workspace=None,
+                  stream=None):
+    """out [M,N] = act(x w^T + bias) + residual for x [M,K] (rows may lie apart) and w [N,K], both bfloat16
+    or both float16; bias float32 [N]; residual of x's dtype [M,N] (rows may lie apart), which may be `out`
+    itself. pre: True or a tensor for x w^T + bias too, which the gradient of an activation needs; the result
+    is (out, pre) then. workspace: uint8 of at least w16a16_linear_workspace(M, N, K) bytes (a new one if
+    None)."""
+    a = _activation(activation)
+    code, ld, M, N, K = _linear16_operands(x, w)
+    _on_device(x, w, bias, residual, pre, out, workspace)
+    bias = _vector(bias, "bias", N)
+    r, ldr = _like_rows(residual, "residual", x.dtype, M, N)
+    lib = load()
+    out = _result(out, "out", (M, N), x.dtype, x, stream)
+    if pre is False:
+        pre = None
+    elif pre is not None:
+        pre = _result(None if pre is True else pre, "pre", (M, N), x.dtype, x, stream)
+    work, address, size = None, 0, 0
+    need = lib.w16a16_linear_workspace(M, N, K)
+    if need or workspace is not None:
+        work = _scratch(workspace, need, x, stream)
+        address, size = work.data_ptr(), work.shape[0]
+    _done(lib.w16a16_linear(x.data_ptr(), ld, M, w.data_ptr(), N, K, code, bias, a, r, ldr,
+                            None if pre is None else pre.data_ptr(), out.data_ptr(), address, size,
+                            _stream_of(x, stream)), "w16a16_linear")
+    return out if pre is None else (out, pre)
+
+
+def w16a16_linear_workspace(M, N, K) -> int:
+    """Bytes of workspace that w16a16_linear needs (0 for most sizes)."""
+    return load().w16a16_linear_workspace(M, N, K)
+
+
+def _wanted(t, name, shape, dtype, like, stream):
+    """A gradient: a new tensor for True, the caller's, or None for False or None (not wanted)."""
+    if t is None or t is False:
+        return None
+    return _result(None if t is True else t, name, shape, dtype, like, stream)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def w16a16_linear_backward(d_out, x, w, pre=None, activation="none", d_x=True, d_w=True, d_bias=True,
+                           d_pre=None, workspace=None, stream=None):
+    """Gradients of w16a16_linear from d_out [M,N] (rows may lie apart) and, with an activation, the pre that it
+    wrote: (d_x [M,K], d_w [N,K], d_bias float32 [N], d_pre [M,N]). d_x, d_w, d_bias: True for a new tensor,
+    a tensor to write, False or None to leave it out (None in the result). d_pre = d_out act'(pre), rounded, is
+    the operand of the products (d_out itself without an activation). The residual's gradient is d_out."""
+    a = _activation(activation)
+    code, ld, M, N, K = _linear16_operands(x, w)
+    _on_device(x, w, d_out, pre, d_x, d_w, d_bias, d_pre, workspace)
+    d, ldd = _like_rows(d_out, "d_out", x.dtype, M, N)
+    if d is None:
+        raise TypeError("d_out must be a torch.Tensor")
+    if a:
+        if pre is None:
+            raise ValueError("the gradient of an activation needs pre")
+        _check(pre, "pre", x.dtype, 2)
+        if pre.shape != (M, N):
+            raise ValueError(f"pre must have shape {(M, N)}, got {tuple(pre.shape)}")
+        d_pre = _result(d_pre, "d_pre", (M, N), x.dtype, x, stream)
+    else:
+        pre, d_pre = None, d_out
+    lib = load()
+    d_x = _wanted(d_x, "d_x", (M, K), x.dtype, x, stream)
+    d_w = _wanted(d_w, "d_w", (N, K), x.dtype, x, stream)
+    d_bias = _wanted(d_bias, "d_bias", (N,), torch.float32, x, stream)
+    work = _scratch(workspace, lib.w16a16_linear_backward_workspace(M, N, K), x, stream)
+    _done(lib.w16a16_linear_backward(d, ldd, x.data_ptr(), ld, w.data_ptr(), _address(pre), M, N, K, code, a,
+                                     d_pre.data_ptr() if a else None, _address(d_x), _address(d_w),
+                                     _address(d_bias), work.data_ptr(), work.shape[0],
+                                     _stream_of(x, stream)), "w16a16_linear_backward")
+    return d_x, d_w, d_bias, d_pre
+
+
+def w16a16_linear_backward_workspace(M, N, K) -> int:
+    """Bytes of workspace that w16a16_linear_backward needs."""
+    return load().w16a16_linear_backward_workspace(M, N, K)
+
+
+def _gate(gate, dtype, T, H):
+    """(address, row stride) of a gate: none, one float32 value per channel (stride 0), or rows."""
+    if gate is None:
+        return None, 0
+    if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+        return _vector(gate, "gate", H), 0
+    return _like_rows(gate, "gate", dtype, T, H)
+
+
+def _norm_operands(residual, weight, y, post_norm, post_weight, gate, new_residual, outputs, stream):
+    """The library's leading arguments, (dtype code, T, H) and the new residual of a block norm."""
+    code, ld, T, H = _float_rows(residual, "residual")
+    _on_device(residual, weight, y, post_weight, gate, new_residual, *outputs)
+    y_at, ldy = _like_rows(y, "y", residual.dtype, T, H)
+    if y is None and (gate is not None or post_norm or post_weight is not None):
+        raise ValueError("gate and post norm need y")
+    gate_at, ldg = _gate(gate, residual.dtype, T, H)
+    if y is not None:
+        new_residual = _result(new_residual, "new_residual", (T, H), residual.dtype, residual, stream)
+    else:
+        new_residual = residual
+    return (residual.data_ptr(), ld, y_at, ldy, 1 if post_norm or post_weight is not None else 0,
+            _vector(post_weight, "post_weight", H), gate_at, ldg), _vector(weight, "weight", H), code, T, H, new_residual
+
+
+def block_norm(residual, weight=None, y=None, post_norm=False, post_weight=None, gate=None, scale=1.0, eps=1e-6,
+               new_residual=None, out=None, stream=None):
+    """The step between two blocks: (new_residual, out) with, per row,
+    new_residual = residual + scale * gate * u, u = y or (post_norm, or a post_weight) y / rms(y) * post_weight,
+    out = new_residual / rms(new_residual) * weight, rms(v) = sqrt(mean(v^2) + eps).
+    residual, y: rows [T,H] of bfloat16, float16 or float32 (they may lie apart); gate: None, float32 [H], or
+    rows; weight, post_weight: float32 [H] or None (ones). Without y it is the plain norm, and new_residual is
+    residual. new_residual may be the (contiguous) residual or y."""
+    args, weight, code, T, H, new_residual = _norm_operands(residual, weight, y, post_norm, post_weight, gate,
+                                                            new_residual, (out,), stream)
+    out = _result(out, "out", (T, H), residual.dtype, residual, stream)
+    _done(load().block_norm(*args, scale, weight, eps, T, H, code, new_residual.data_ptr(), out.data_ptr(),
+                            _stream_of(residual, stream)), "block_norm")
+    return new_residual, out
+
+
+def block_norm_w8a8(residual, weight=None, y=None, post_norm=False, post_weight=None, gate=None, scale=1.0,
+                    eps=1e-6, new_residual=None, xq=None, x_scale=None, stream=None):
+    """block_norm with its output quantized to int8 rows, as w8a8_quantize_rows would the unrounded output:
+    (new_residual, xq int8 [T,H], x_scale float32 [T])."""
+    args, weight, code, T, H, new_residual = _norm_operands(residual, weight, y, post_norm, post_weight, gate,
+                                                            new_residual, (xq, x_scale), stream)
+    xq = _result(xq, "xq", (T, H), torch.int8, residual, stream)
+    x_scale = _result(x_scale, "x_scale", (T,), torch.float32, residual, stream)
+    _done(load().block_norm_w8a8(*args, scale, weight, eps, T, H, code, new_residual.data_ptr(), xq.data_ptr(),
+                                 x_scale.data_ptr(), _stream_of(residual, stream)), "block_norm_w8a8")
+    return new_residual, xq, x_scale
+
+
+def block_norm_mxfp4(residual, weight=None, y=None, post_norm=False, post_weight=None, gate=None, scale=1.0,
+                     eps=1e-6, new_residual=None, codes=None, scales=None, stream=None):
+    """block_norm with its output quantized to MXFP4 rows, as mxfp4_quantize_rows would the unrounded output:
+    (new_residual, codes uint8 [T,H/2], scales uint8 [ceil(H/256),T,8])."""
+    args, weight, code, T, H, new_residual = _norm_operands(residual, weight, y, post_norm, post_weight, gate,
+                                                            new_residual, (codes, scales), stream)
+    codes = _result(codes, "codes", (T, H // 2), torch.uint8, residual, stream)
+    scales = _result(scales, "scales", ((H + 255) // 256, T, 8), torch.uint8, residual, stream)
+    _done(load().block_norm_mxfp4(*args, scale, weight, eps, T, H, code, new_residual.data_ptr(),
+                                  codes.data_ptr(), scales.data_ptr(), _stream_of(residual, stream)),
+          "block_norm_mxfp4")
+    return new_residual, codes, scales
+
+
+def block_norm_backward(d_out, new_residual, weight=None, d_residual=None, y=None, post_norm=False,
+                        post_weight=None, gate=None, scale=1.0, eps=1e-6, workspace=None, stream=None):
+    """Gradients of block_norm: d_out is out's, d_residual (rows, or None for 0) new_residual's, which is given as
+    block_norm wrote it (without y: the residual). Returns (d_residual of the residual [T,H], d_weight float32 [H],
+    d_y [T,H], d_post_weight float32 [H], d_gate [T,H] or float32 [H]), None for those without an input (the
+    weights' gradients are given for absent weights, too, as those of ones; d_post_weight with a post norm)."""
+    code, ldr, T, H = _float_rows(new_residual, "new_residual")
+    dtype = new_residual.dtype
+    _on_device(new_residual, d_out, weight, d_residual, y, post_weight, gate, workspace)
+    o, ldo = _like_rows(d_out, "d_out", dtype, T, H)
+    if o is None:
+        raise TypeError("d_out must be a torch.Tensor")
+    n, ldn = _like_rows(d_residual, "d_residual", dtype, T, H)
+    y_at, ldy = _like_rows(y, "y", dtype, T, H)
+    post = post_norm or post_weight is not None
+    if y is None and (gate is not None or post):
+        raise ValueError("gate and post norm need y")
+    gate_at, ldg = _gate(gate, dtype, T, H)
+    weight, post_weight = _vector(weight, "weight", H), _vector(post_weight, "post_weight", H)
+    lib = load()
+    d_r = _new((T, H), dtype, new_residual, stream)
+    d_weight = _new((H,), torch.float32, new_residual, stream)
+    d_y = d_post_weight = d_gate = None
+    if y is not None:
+        d_y = _new((T, H), dtype, new_residual, stream)
+    if post:
+        d_post_weight = _new((H,), torch.float32, new_residual, stream)
+    if gate is not None:
+        d_gate = _new((T, H) if ldg else (H,), dtype if ldg else torch.float32, new_residual, stream)
+    work = _scratch(workspace, lib.block_norm_backward_workspace(T, H), new_residual, stream)
+    _done(lib.block_norm_backward(o, ldo, n, ldn, new_residual.data_ptr(), ldr, y_at, ldy, 1 if post else 0,
+                                  post_weight, gate_at, ldg, scale, weight, eps, T, H, code, d_r.data_ptr(),
+                                  _address(d_y), _address(d_gate), d_weight.data_ptr(), _address(d_post_weight),
+                                  work.data_ptr(), work.shape[0], _stream_of(new_residual, stream)),
+          "block_norm_backward")
+    return d_r, d_weight, d_y, d_post_weight, d_gate
+
+
+def block_norm_backward_workspace(T, H) -> int:
+    """Bytes of workspace that block_norm_backward needs."""
+    return load().block_norm_backward_workspace(T, H)

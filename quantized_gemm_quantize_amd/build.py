@@ -24,7 +24,8 @@ POISON_FLAGS = ["-DW8A8_LDS_POISON"]
 PEAKS_SOURCE = "peaks.hip"
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["quantize_rows.hip", "gemm_tiled.hip", "gemm_decode.hip", "bsr_gemm.hip", "sparse24.hip",
-           "w4a16.hip", "mxfp4_quantize.hip", "mxfp4_gemm.hip", "mxfp4_tiled.hip", "mxfp4_decode.hip", "moe_route.hip", "w8a8_abi.hip"]
+           "w4a16.hip", "mxfp4_quantize.hip", "mxfp4_gemm.hip", "mxfp4_tiled.hip", "mxfp4_decode.hip", "moe_route.hip",
+           "norm.hip", "norm_backward.hip", "linear16.hip", "w8a8_abi.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -31,19 +31,46 @@
 // each CU runs about eight vector instructions for each of the M * K
 // activations, which at M = 16, K = N = 4096 takes longer than the separate
 // quantize launch it replaces.
+#include <type_traits>
+
+#include "activation.hpp"
 #include "launch.hpp"
 #include "quant_math.hpp"
 
 namespace w8a8 {
 namespace {
 
+// The epilogues: acc * sa * sb; addmm; bias, activation and residual.
+enum Epi { kPlain, kAddmm, kAct };
+template <Epi EPI>
+using EpiArg = typename std::conditional<EPI == kAct, ActEpilogue, Addmm>::type;
+
+// One output of the bf16 epilogues from its dequantized product, bias and residual.
+template <Epi EPI>
+__device__ __forceinline__ float finish(float v, const EpiArg<EPI> &ep, float bias, float residual) {
+    if constexpr (EPI == kAct) {
+        float one[1] = {v + bias};
+        act::activate(ep.act, one);
+        return one[0] + residual;
+    } else {
+        return addmm<EPI == kAddmm>(v, ep, bias);
+    }
+}
+
+template <Epi EPI>
+__device__ __forceinline__ float residual_at(const EpiArg<EPI> &ep, int m, int n) {
+    if constexpr (EPI == kAct)
+        if (ep.residual) return bf16_lo(static_cast<const uint16_t *>(ep.residual)[m * ep.ldr + n]);
+    return 0.0f;
+}
+
 
 // kSteps: K steps (64 bytes each) whose loads a wavefront issues together.
-template <int MT, int KSPLIT, bool OUT_I32, bool ADDMM, int kSteps>
+template <int MT, int KSPLIT, bool OUT_I32, Epi EPI, int kSteps>
 __global__ __launch_bounds__(KSPLIT *kWave) void gemm_decode_kernel(
     const int8_t *__restrict__ A, const float *__restrict__ sa, const int8_t *__restrict__ B,
     const float *__restrict__ sb, void *__restrict__ out, int M, int N, int K,
-    int steps_per_wave, Addmm am) {
+    int steps_per_wave, EpiArg<EPI> am) {
     __shared__ int red[KSPLIT][MT][4][kWave];
     lds_poison(red);
     lds_poison_done();
@@ -65,14 +92,15 @@ __global__ __launch_bounds__(KSPLIT *kWave) void gemm_decode_kernel(
     // memory round trip after the reduction
     constexpr int kThreadsWg = KSPLIT * kWave;
     constexpr int EPT = (MT * 256 + kThreadsWg - 1) / kThreadsWg;  // outputs per thread
-    float esx[EPT], esw[EPT], ebias[EPT];
+    float esx[EPT], esw[EPT], ebias[EPT], eres[EPT];
 #pragma unroll
     for (int q = 0; q < EPT; ++q) {
         const int e = min((int)threadIdx.x + q * kThreadsWg, MT * 256 - 1);
         const int m = min((e >> 8) * 16 + ((e >> 4) & 15), M - 1), n = n0 + (e & 15);
         esx[q] = OUT_I32 ? 0.0f : sa[m];
         esw[q] = OUT_I32 ? 0.0f : sb[n];
-        ebias[q] = ADDMM && am.bias ? am.bias[n] : 0.0f;
+        ebias[q] = EPI != kPlain && am.bias ? am.bias[n] : 0.0f;
+        eres[q] = residual_at<EPI>(am, m, n);
     }
 
     const int total_steps = (K + 63) / 64;
@@ -118,8 +146,8 @@ __global__ __launch_bounds__(KSPLIT *kWave) void gemm_decode_kernel(
         if constexpr (OUT_I32) {
             static_cast<int32_t *>(out)[(int64_t)m * N + n] = sum;
         } else {
-            const float v =
-                addmm<ADDMM>(dequant(sum, split_scale(esx[q]), split_scale(esw[q])), am, ebias[q]);
+            const float v = finish<EPI>(dequant(sum, split_scale(esx[q]), split_scale(esw[q])), am,
+                                        ebias[q], eres[q]);
             static_cast<__bf16 *>(out)[(int64_t)m * N + n] = (__bf16)v;
         }
     }
@@ -157,10 +185,10 @@ __device__ __forceinline__ void wait_vm() {
 // Chunks past K are read from a clamped address (every load stays in bounds
 // and is always issued, so the counted waits hold) and their activation
 // fragments are zeroed before the MFMA.
-template <int WAVES, bool OUT_I32, bool ADDMM>
+template <int WAVES, bool OUT_I32, Epi EPI>
 __global__ __launch_bounds__(WAVES *kWave) void gemm_decode_lds_kernel(
     const int8_t *__restrict__ A, const float *__restrict__ sa, const int8_t *__restrict__ B,
-    const float *__restrict__ sb, void *__restrict__ out, int M, int N, int K, Addmm am) {
+    const float *__restrict__ sb, void *__restrict__ out, int M, int N, int K, EpiArg<EPI> am) {
     constexpr int kBlock = 4096;                 // K bytes per block, all wavefronts
     constexpr int kSlice = kBlock / WAVES;       // K bytes per wavefront per block
     constexpr int kPairs = kSlice / 128;         // 128-byte K pairs per slice
@@ -199,7 +227,8 @@ __global__ __launch_bounds__(WAVES *kWave) void gemm_decode_lds_kernel(
     const int em = e >> 4, en = n0 + (e & 15);
     const float esx = OUT_I32 ? 0.0f : sa[min(em, M - 1)];
     const float esw = OUT_I32 ? 0.0f : sb[en];
-    const float ebias = ADDMM && am.bias ? am.bias[en] : 0.0f;
+    const float ebias = EPI != kPlain && am.bias ? am.bias[en] : 0.0f;
+    const float eres = residual_at<EPI>(am, min(em, M - 1), en);
 
     // this lane's rows and chunks for the two halves of every load
     const int lr = lane >> 3, lc = lane & 7;
@@ -274,7 +303,7 @@ __global__ __launch_bounds__(WAVES *kWave) void gemm_decode_lds_kernel(
     if constexpr (OUT_I32) {
         static_cast<int32_t *>(out)[(int64_t)i * N + en] = sum;
     } else {
-        const float v = addmm<ADDMM>(dequant(sum, split_scale(esx), split_scale(esw)), am, ebias);
+        const float v = finish<EPI>(dequant(sum, split_scale(esx), split_scale(esw)), am, ebias, eres);
         static_cast<__bf16 *>(out)[(int64_t)i * N + en] = (__bf16)v;
     }
 }
@@ -452,19 +481,22 @@ template <> struct DecodeShape<2> { static constexpr int split = 4, steps = 16; 
 template <int MT, int KSPLIT, int STEPS>
 hipError_t launch_shape(const int8_t *xq, const float *xs, int M, const int8_t *wq,
                         const float *ws, int N, int K, void *out, bool out_i32,
-                        hipStream_t stream, const Addmm *am) {
+                        hipStream_t stream, const Addmm *am, const ActEpilogue *ep) {
     const int total_steps = (K + 63) / 64;
     const int steps_per_wave = (total_steps + KSPLIT - 1) / KSPLIT;
     const dim3 grid((unsigned)(N / 16)), block(KSPLIT * kWave);
     const Addmm a = am ? *am : Addmm{nullptr, 1.0f, 0.0f};
-    if (out_i32)
-        gemm_decode_kernel<MT, KSPLIT, true, false, STEPS>
+    if (ep)
+        gemm_decode_kernel<MT, KSPLIT, false, kAct, STEPS>
+            <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, steps_per_wave, *ep);
+    else if (out_i32)
+        gemm_decode_kernel<MT, KSPLIT, true, kPlain, STEPS>
             <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, steps_per_wave, a);
     else if (am)
-        gemm_decode_kernel<MT, KSPLIT, false, true, STEPS>
+        gemm_decode_kernel<MT, KSPLIT, false, kAddmm, STEPS>
             <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, steps_per_wave, a);
     else
-        gemm_decode_kernel<MT, KSPLIT, false, false, STEPS>
+        gemm_decode_kernel<MT, KSPLIT, false, kPlain, STEPS>
             <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, steps_per_wave, a);
     return hipGetLastError();
 }
@@ -474,13 +506,14 @@ hipError_t launch_shape(const int8_t *xq, const float *xs, int M, const int8_t *
 // 2.1 us for 8 x 8).
 template <int MT>
 hipError_t launch_mt(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
-                     int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am) {
+                     int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
+                     const ActEpilogue *ep) {
     constexpr int KSPLIT = DecodeShape<MT>::split, STEPS = DecodeShape<MT>::steps;
     if constexpr (KSPLIT != 8) {
         if ((K + 63) / 64 < KSPLIT * STEPS)
-            return launch_shape<MT, 8, 8>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
+            return launch_shape<MT, 8, 8>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     }
-    return launch_shape<MT, KSPLIT, STEPS>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
+    return launch_shape<MT, KSPLIT, STEPS>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
 }
 
 }  // namespace
@@ -497,15 +530,18 @@ hipError_t launch_linear_decode(const uint16_t *x, int M, const int8_t *wq, cons
 
 template <int WAVES>
 hipError_t launch_lds(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
-                      int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am) {
+                      int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
+                      const ActEpilogue *ep) {
     const dim3 grid((unsigned)(N / 16)), block(WAVES * kWave);
     const Addmm a = am ? *am : Addmm{nullptr, 1.0f, 0.0f};
-    if (out_i32)
-        gemm_decode_lds_kernel<WAVES, true, false><<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, a);
+    if (ep)
+        gemm_decode_lds_kernel<WAVES, false, kAct><<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, *ep);
+    else if (out_i32)
+        gemm_decode_lds_kernel<WAVES, true, kPlain><<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, a);
     else if (am)
-        gemm_decode_lds_kernel<WAVES, false, true><<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, a);
+        gemm_decode_lds_kernel<WAVES, false, kAddmm><<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, a);
     else
-        gemm_decode_lds_kernel<WAVES, false, false><<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, a);
+        gemm_decode_lds_kernel<WAVES, false, kPlain><<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, a);
     return hipGetLastError();
 }
 
@@ -519,16 +555,16 @@ hipError_t launch_lds(const int8_t *xq, const float *xs, int M, const int8_t *wq
 // against 3.5 us), so short K keeps the register path.
 hipError_t launch_gemm_decode(const int8_t *xq, const float *xs, int M, const int8_t *wq,
                               const float *ws, int N, int K, void *out, bool out_i32,
-                              hipStream_t stream, const Addmm *am) {
+                              hipStream_t stream, const Addmm *am, const ActEpilogue *ep) {
     if (M <= 16 && K >= 3072) {
-        if (K <= 4096) return launch_lds<4>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
-        return launch_lds<16>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
+        if (K <= 4096) return launch_lds<4>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+        return launch_lds<16>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     }
     switch ((M + 15) / 16) {
-        case 1: return launch_mt<1>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
-        case 2: return launch_mt<2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
-        case 3: return launch_mt<3>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
-        default: return launch_mt<4>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
+        case 1: return launch_mt<1>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+        case 2: return launch_mt<2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+        case 3: return launch_mt<3>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+        default: return launch_mt<4>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     }
 }
 

@@ -34,6 +34,9 @@
 //  - tiles are assigned XCD-contiguously, then in groups of 4 (256x128 tiles)
 //    or 8 (256x256) tile rows, so concurrently running tiles share A and B
 //    rows in the same L2.
+#include <type_traits>
+
+#include "activation.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -209,13 +212,19 @@ __device__ __forceinline__ void mainloop_stage(const int8_t *__restrict__ at,
     }
 }
 
+// The epilogues: acc * sa * sb; addmm; bias, activation and residual.
+enum Epi { kPlain, kAddmm, kAct };
+template <Epi EPI>
+using EpiArg = typename std::conditional<EPI == kAct, ActEpilogue, Addmm>::type;
+
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int CPR, int OCC, bool KTAIL,
-          bool OUT_I32, bool ADDMM>
+          bool OUT_I32, Epi EPI>
 __global__ __launch_bounds__(kThreads, OCC) void gemm_tiled_kernel(
     const int8_t *__restrict__ A, const float *__restrict__ sa, const int8_t *__restrict__ B,
     const float *__restrict__ sb, void *__restrict__ out, int M, int N, int K, int tiles_m,
-    int tiles_n, Addmm am) {
-    static_assert(!(ADDMM && OUT_I32), "the addmm epilogue writes bf16");
+    int tiles_n, EpiArg<EPI> am) {
+    static_assert(EPI == kPlain || !OUT_I32, "these epilogues write bf16");
+    constexpr bool ADDMM = EPI == kAddmm;
     static_assert(WAVES_M * WAVES_N == kWaves, "4 wavefronts");
     static_assert(STAGES == 2 || STAGES == 3, "double or triple buffering");
     constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
@@ -334,6 +343,88 @@ __global__ __launch_bounds__(kThreads, OCC) void gemm_tiled_kernel(
                             reinterpret_cast<v4i *>(static_cast<int32_t *>(out) + (int64_t)m * N + n));
                 }
         }
+    } else if constexpr (EPI == kAct) {
+        // The sub-tile is staged in fp32, as many rows at a time as the wave's share of LDS
+        // holds, so that bias, activation and residual act on 8 consecutive channels of a
+        // row per lane: the residual is read and the output written in whole 16-byte pieces,
+        // by the same lane (in-place residuals), and rounded once.
+        constexpr int kShare = STAGES * STAGE * 16 / kWaves;       // bytes
+        constexpr int kFit = kShare / (WN * 4) / 32 * 32;
+        constexpr int kPass = kFit < WM ? kFit : WM;               // rows per pass
+        static_assert(kPass >= 32 && WM % kPass == 0, "passes of whole 32-row tiles");
+        constexpr int CH = WN / 4, PM = CH - 1;                    // 16-byte chunks per staged row
+        static_assert((CH & PM) == 0, "the row-chunk permutation needs a power of two");
+        float4 *st = reinterpret_cast<float4 *>(lds) + wave * (kShare / 16);
+        const int lane_n = lane % (WN / 8) * 8, n = nw0 + lane_n;  // this lane's channels
+        float bv[8] = {};
+        if (am.bias && n < N) {
+            *reinterpret_cast<float4 *>(bv) = *reinterpret_cast<const float4 *>(am.bias + n);
+            *reinterpret_cast<float4 *>(bv + 4) = *reinterpret_cast<const float4 *>(am.bias + n + 4);
+        }
+#pragma unroll
+        for (int p = 0; p < WM / kPass; ++p) {
+            if (p) __syncthreads();
+            float sxv[kPass / 32];
+            bool rows_tame = true;
+#pragma unroll
+            for (int i = 0; i < kPass / 32; ++i) {
+                sxv[i] = sa[min(mw0 + p * kPass + i * 32 + frag_row, M - 1)];
+                rows_tame = rows_tame && tame_scale(sxv[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int nj = min(nw0 + j * 32 + 8 * g + 4 * half, N - 4);
+                    const float4 w = *reinterpret_cast<const float4 *>(sb + nj);
+                    const bool cheap = wave_all(rows_tame && tame_scale(w.x) && tame_scale(w.y) &&
+                                                tame_scale(w.z) && tame_scale(w.w));
+#pragma unroll
+                    for (int i = 0; i < kPass / 32; ++i) {
+                        const int ml = i * 32 + frag_row;
+                        const v16i &a = acc[p * (kPass / 32) + i][j];
+                        float4 v;
+                        if (cheap) {
+                            v.x = (float)a[4 * g] * sxv[i] * w.x;
+                            v.y = (float)a[4 * g + 1] * sxv[i] * w.y;
+                            v.z = (float)a[4 * g + 2] * sxv[i] * w.z;
+                            v.w = (float)a[4 * g + 3] * sxv[i] * w.w;
+                        } else {
+                            const SplitScale x = split_scale(sxv[i]);
+                            v.x = dequant(a[4 * g], x, split_scale(w.x));
+                            v.y = dequant(a[4 * g + 1], x, split_scale(w.y));
+                            v.z = dequant(a[4 * g + 2], x, split_scale(w.z));
+                            v.w = dequant(a[4 * g + 3], x, split_scale(w.w));
+                        }
+                        st[ml * CH + ((j * 8 + 2 * g + half) ^ (ml & PM))] = v;
+                    }
+                }
+            __syncthreads();
+#pragma unroll
+            for (int it = 0; it < kPass * (WN / 8) / kWave; ++it) {
+                const int ml = it * (kWave / (WN / 8)) + lane / (WN / 8);
+                const int m = mw0 + p * kPass + ml;
+                if (m >= M || n >= N) continue;
+                float v[8];
+                *reinterpret_cast<float4 *>(v) = st[ml * CH + ((lane_n / 4) ^ (ml & PM))];
+                *reinterpret_cast<float4 *>(v + 4) = st[ml * CH + ((lane_n / 4 + 1) ^ (ml & PM))];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += bv[e];
+                act::activate(am.act, v);
+                if (am.residual) {
+                    const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(am.residual) + m * am.ldr + n);
+                    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[2 * e] += bf16_lo(w[e]);
+                        v[2 * e + 1] += bf16_hi(w[e]);
+                    }
+                }
+                store16_nt(static_cast<__bf16 *>(out) + (int64_t)m * N + n,
+                           make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+            }
+        }
     } else {
         // stage the wave's WM x WN bf16 sub-tile in LDS (row-major, 16-byte
         // chunks of a row permuted by the low row bits, so that the 32 rows of
@@ -402,18 +493,22 @@ __global__ __launch_bounds__(kThreads, OCC) void gemm_tiled_kernel(
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int CPR, int OCC, bool KTAIL>
 void launch_tail(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
-                 int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am) {
+                 int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
+                 const ActEpilogue *ep) {
     const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
     const dim3 grid((unsigned)(tiles_m * tiles_n)), block(kThreads);
     const Addmm a = am ? *am : Addmm{nullptr, 1.0f, 0.0f};
-    if (out_i32)
-        gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, true, false>
+    if (ep)
+        gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, false, kAct>
+            <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, tiles_m, tiles_n, *ep);
+    else if (out_i32)
+        gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, true, kPlain>
             <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, tiles_m, tiles_n, a);
     else if (am)
-        gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, false, true>
+        gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, false, kAddmm>
             <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, tiles_m, tiles_n, a);
     else
-        gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, false, false>
+        gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, false, kPlain>
             <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, tiles_m, tiles_n, a);
 }
 
@@ -421,13 +516,14 @@ void launch_tail(const int8_t *xq, const float *xs, int M, const int8_t *wq, con
 // chunks past K.
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int CPR = 8, int OCC = 1>
 hipError_t launch_cfg(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
-                      int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am) {
+                      int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
+                      const ActEpilogue *ep) {
     if (K % (16 * CPR) == 0)
         launch_tail<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, false>(xq, xs, M, wq, ws, N, K, out,
-                                                                       out_i32, stream, am);
+                                                                       out_i32, stream, am, ep);
     else
         launch_tail<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, true>(xq, xs, M, wq, ws, N, K, out,
-                                                                      out_i32, stream, am);
+                                                                      out_i32, stream, am, ep);
     return hipGetLastError();
 }
 
@@ -435,11 +531,12 @@ hipError_t launch_cfg(const int8_t *xq, const float *xs, int M, const int8_t *wq
 
 hipError_t launch_gemm_decode(const int8_t *xq, const float *xs, int M, const int8_t *wq,
                               const float *ws, int N, int K, void *out, bool out_i32,
-                              hipStream_t stream, const Addmm *am);
+                              hipStream_t stream, const Addmm *am, const ActEpilogue *ep);
 
-hipError_t launch_gemm(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
-                       int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am) {
-    if (M <= 64) return launch_gemm_decode(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
+static hipError_t launch_any(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
+                             int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
+                             const ActEpilogue *ep) {
+    if (M <= 64) return launch_gemm_decode(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     // Many tiles (enough 256x256 ones to fill 256 CUs four times over): with
     // K up to 1024, two 256x128 workgroups per CU (64-byte K stages, 72 KB of
     // LDS and at most 256 registers each), so that one tile's prologue and
@@ -449,10 +546,20 @@ hipError_t launch_gemm(const int8_t *xq, const float *xs, int M, const int8_t *w
     const long t256 = (long)((M + 255) / 256) * ((N + 255) / 256);
     const long t128 = (long)((M + 255) / 256) * ((N + 127) / 128);
     if (t256 >= 4 * 256 && K <= 1024)
-        return launch_cfg<256, 128, 2, 2, 3, 4, 2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
-    if (t256 >= 4 * 256) return launch_cfg<256, 256, 2, 2, 2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
-    if (t128 >= 256) return launch_cfg<256, 128, 2, 2, 3>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
-    return launch_cfg<128, 128, 2, 2, 2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am);
+        return launch_cfg<256, 128, 2, 2, 3, 4, 2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+    if (t256 >= 4 * 256) return launch_cfg<256, 256, 2, 2, 2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+    if (t128 >= 256) return launch_cfg<256, 128, 2, 2, 3>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+    return launch_cfg<128, 128, 2, 2, 2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+}
+
+hipError_t launch_gemm(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
+                       int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am) {
+    return launch_any(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, nullptr);
+}
+
+hipError_t launch_gemm_act(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
+                           int N, int K, void *out, const ActEpilogue &ep, hipStream_t stream) {
+    return launch_any(xq, xs, M, wq, ws, N, K, out, false, stream, nullptr, &ep);
 }
 
 }  // namespace w8a8

@@ -21,6 +21,17 @@ hipError_t launch_gemm(const int8_t *xq, const float *xs, int M, const int8_t *w
                        int N, int K, void *out, bool out_i32, hipStream_t stream,
                        const Addmm *am = nullptr);
 
+// Epilogue act(acc * sa * sb + bias[n]) + residual[m, n] (bias and residual may be null; act an
+// act::Activation), and the product with it, on the same kernels.
+struct ActEpilogue {
+    const float *bias;
+    const void *residual;  // bf16 rows, row stride ldr
+    int64_t ldr;
+    int act;
+};
+hipError_t launch_gemm_act(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
+                           int N, int K, void *out, const ActEpilogue &ep, hipStream_t stream);
+
 // Single-launch linear for M <= 64: quantize_rows of bf16 X fused into the
 // weight-streaming GEMM, epilogue as launch_gemm's with am.
 hipError_t launch_linear_decode(const uint16_t *x, int M, const int8_t *wq, const float *ws, int N,
@@ -137,3 +148,39 @@ hipError_t launch_combine_backward(const void *d_out, int64_t ldd, const void *r
                                    hipStream_t stream);
 
 }  // namespace moe
+
+namespace block {
+
+struct Forward;
+struct Backward;
+
+// Row widths that stay in registers.
+constexpr int kMaxH = 16384;
+
+// The block norm (norm.hpp's arguments; dtype 0 bf16, 1 binary16, 2 binary32;
+// out 0 rows of dtype, 1 int8 rows, 2 MXFP4 rows) and its gradients.
+hipError_t launch_forward(const Forward &a, int dtype, int out, hipStream_t stream);
+
+// Most workgroups of the backward pass, each of which leaves partial sums.
+constexpr int kBackwardWorkgroups = 512;
+int64_t backward_workspace(int64_t T, int64_t H);
+hipError_t launch_backward(const Backward &a, int dtype, hipStream_t stream);
+
+}  // namespace block
+
+namespace linear16 {
+
+struct Epilogue;
+
+// 16-bit products (bf16, or binary16 when f16): x [M,K] with row stride ldx times w [N,K] with
+// the epilogue, and the gradients (null outputs are left out). d_pre is not written without an
+// activation (it is d_out then).
+int64_t forward_workspace(int64_t M, int64_t N, int64_t K);
+int64_t backward_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_forward(const void *x, int64_t ldx, int64_t M, const void *w, int64_t N, int64_t K, bool f16,
+                          const Epilogue &ep, void *workspace, hipStream_t stream);
+hipError_t launch_backward(const void *d_out, int64_t ldd, const void *x, int64_t ldx, const void *w,
+                           const void *pre, int64_t M, int64_t N, int64_t K, bool f16, int act, void *d_pre,
+                           void *d_x, void *d_w, float *d_bias, void *workspace, hipStream_t stream);
+
+}  // namespace linear16

@@ -13,10 +13,13 @@
 #include <cmath>
 #include <cstring>
 
+#include "activation.hpp"
 #include "common.hpp"
 #include "launch.hpp"
+#include "linear16.hpp"
 #include "mxfp4_epilogue.hpp"
 #include "mxfp4_form.hpp"
+#include "norm.hpp"
 
 namespace {
 
@@ -632,6 +635,197 @@ w8a8_status mxfp4_moe(const void *x, int64_t ldx, mxfp4_dtype dtype, int64_t T, 
         return s;
     return hip_status(moe::launch_combine_layer(reinterpret_cast<const float *>(ws + p.y), slot_pos, weights, T,
                                                 (int)top, (int)H, dt, out, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- around a layer
+
+static bool act_ok(int a) { return a >= W8A8_ACT_NONE && a <= W8A8_ACT_SILU; }
+
+w8a8_status w8a8_gemm_act(const int8_t *xq, const float *x_scale, int64_t M, const int8_t *wq,
+                          const float *w_scale, int64_t N, int64_t K, const float *bias,
+                          w8a8_activation activation, const void *residual, int64_t ldr, void *out,
+                          void *stream) {
+    if (M < 0 || N <= 0 || N % 16 != 0 || too_big(M, N)) return W8A8_ERR_SHAPE;
+    if (w8a8_status s = check_k(K)) return s;
+    const int a = selector(&activation);
+    if (!act_ok(a)) return W8A8_ERR_DTYPE;
+    if ((M + 127) / 128 > INT_MAX / ((N + 127) / 128)) return W8A8_ERR_SHAPE;  // grid.x
+    if (residual && (ldr < N || ldr > INT_MAX)) return W8A8_ERR_SHAPE;
+    if (M == 0) return W8A8_OK;
+    if (!xq || !x_scale || !wq || !w_scale || !out) return W8A8_ERR_NULL;
+    if (misaligned(xq) || misaligned(x_scale) || misaligned(wq) || misaligned(w_scale) ||
+        misaligned(out) || misaligned(bias) || misaligned(residual) || (residual && ldr % 8 != 0))
+        return W8A8_ERR_ALIGN;
+    const w8a8::ActEpilogue ep{bias, residual, ldr, a};
+    return hip_status(w8a8::launch_gemm_act(xq, x_scale, (int)M, wq, w_scale, (int)N, (int)K, out, ep,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+static w8a8_status linear16_shape(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || M >= (1 << 27) || N <= 0 || K <= 0 || N % 8 != 0 || K % 8 != 0 ||
+        N > W16A16_MAX_WIDTH || K > W16A16_MAX_WIDTH)
+        return W8A8_ERR_SHAPE;
+    const int64_t most = (int64_t)1 << 35;  // tiles are counted in 32 bits
+    if (M * N > most || M * K > most || N * K > most) return W8A8_ERR_SHAPE;
+    return W8A8_OK;
+}
+
+int64_t w16a16_linear_workspace(int64_t M, int64_t N, int64_t K) {
+    return linear16_shape(M, N, K) == W8A8_OK ? linear16::forward_workspace(M, N, K) : 0;
+}
+
+w8a8_status w16a16_linear(const void *x, int64_t ldx, int64_t M, const void *w, int64_t N,
+                          int64_t K, w4a16_dtype dtype, const float *bias,
+                          w8a8_activation activation, const void *residual, int64_t ldr, void *pre,
+                          void *out, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (w8a8_status s = linear16_shape(M, N, K)) return s;
+    const int dt = selector(&dtype), a = selector(&activation);
+    if ((dt != W4A16_BF16 && dt != W4A16_F16) || !act_ok(a)) return W8A8_ERR_DTYPE;
+    const int64_t need = linear16::forward_workspace(M, N, K);
+    if (ldx < K || ldx > INT_MAX || (residual && (ldr < N || ldr > INT_MAX)) || workspace_bytes < need)
+        return W8A8_ERR_SHAPE;
+    if (M == 0) return W8A8_OK;
+    if (!x || !w || !out || (need && !workspace)) return W8A8_ERR_NULL;
+    if (misaligned(x) || misaligned(w) || misaligned(out) || misaligned(bias) || misaligned(residual) ||
+        misaligned(pre) || misaligned(workspace) || ldx % 8 != 0 || (residual && ldr % 8 != 0))
+        return W8A8_ERR_ALIGN;
+    const linear16::Epilogue ep{bias, residual, ldr, pre, out, a};
+    return hip_status(linear16::launch_forward(x, ldx, M, w, N, K, dt == W4A16_F16, ep, workspace,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int64_t w16a16_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
+    return linear16_shape(M, N, K) == W8A8_OK ? linear16::backward_workspace(M, N, K) : 0;
+}
+
+w8a8_status w16a16_linear_backward(const void *d_out, int64_t ldd, const void *x, int64_t ldx,
+                                   const void *w, const void *pre, int64_t M, int64_t N, int64_t K,
+                                   w4a16_dtype dtype, w8a8_activation activation, void *d_pre,
+                                   void *d_x, void *d_w, float *d_bias, void *workspace,
+                                   int64_t workspace_bytes, void *stream) {
+    if (w8a8_status s = linear16_shape(M, N, K)) return s;
+    const int dt = selector(&dtype), a = selector(&activation);
+    if ((dt != W4A16_BF16 && dt != W4A16_F16) || !act_ok(a)) return W8A8_ERR_DTYPE;
+    const int64_t need = linear16::backward_workspace(M, N, K);
+    if (ldd < N || ldd > INT_MAX || ldx < K || ldx > INT_MAX || workspace_bytes < need)
+        return W8A8_ERR_SHAPE;
+    const bool slope = a != W8A8_ACT_NONE;
+    if (M > 0 && (!d_out || (d_w && !x) || (d_x && !w) || (slope && (!pre || !d_pre)) || (need && !workspace)))
+        return W8A8_ERR_NULL;
+    if (misaligned(d_out) || misaligned(x) || misaligned(w) || misaligned(pre) || misaligned(d_pre) ||
+        misaligned(d_x) || misaligned(d_w) || misaligned(d_bias) || misaligned(workspace) ||
+        ldd % 8 != 0 || ldx % 8 != 0)
+        return W8A8_ERR_ALIGN;
+    return hip_status(linear16::launch_backward(d_out, ldd, x, ldx, w, pre, M, N, K, dt == W4A16_F16, a,
+                                                d_pre, d_x, d_w, d_bias, workspace,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+// Sizes, type and scalars of a block norm.
+static w8a8_status norm_shape(int64_t T, int64_t H) {
+    // workgroups of up to 1024 threads per row above 4096 elements, 256 below
+    if (T < 0 || T >= (1 << 24) || H <= 0 || H > BLOCK_NORM_MAX_H || T * H > ((int64_t)1 << 34))
+        return W8A8_ERR_SHAPE;
+    return W8A8_OK;
+}
+
+static w8a8_status norm_scalars(float scale, float eps) {
+    return std::isfinite(scale) && std::isfinite(eps) && eps > 0 ? W8A8_OK : W8A8_ERR_VALUE;
+}
+
+static bool short_rows(const void *rows, int64_t ld, int64_t H) {
+    return rows && (ld < H || ld > INT_MAX);
+}
+
+static bool bad_gate(const void *gate, int64_t ldg, int64_t size) {
+    return gate && (ldg == 0 ? misaligned(gate) : odd(gate, size));
+}
+
+static w8a8_status norm_entry(block::Forward a, int dt, int out, void *stream) {
+    if (w8a8_status s = norm_shape(a.T, a.H)) return s;
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    if (w8a8_status s = norm_scalars(a.scale, a.eps)) return s;
+    if (a.ldr < a.H || a.ldr > INT_MAX || short_rows(a.y, a.ldy, a.H) ||
+        (a.y && a.ldg != 0 && short_rows(a.gate, a.ldg, a.H)))
+        return W8A8_ERR_SHAPE;
+    if (out != block::kSame && a.H % (out == block::kInt8 ? 16 : 32) != 0) return W8A8_ERR_SHAPE;
+    if (a.T == 0) return W8A8_OK;
+    if (!a.residual || (a.y && !a.new_residual) || !a.out || (out != block::kSame && !a.out_scale))
+        return W8A8_ERR_NULL;
+    const int64_t size = dtype_size(dt);
+    if (odd(a.residual, size) || odd(a.y, size) || odd(a.new_residual, size) ||
+        (a.y && bad_gate(a.gate, a.ldg, size)) || misaligned(a.weight) || misaligned(a.post_weight) ||
+        (out == block::kSame ? odd(a.out, size) : misaligned(a.out) || misaligned(a.out_scale)))
+        return W8A8_ERR_ALIGN;
+    if (!a.y) a.gate = nullptr, a.post = 0;
+    return hip_status(block::launch_forward(a, dt, out, static_cast<hipStream_t>(stream)));
+}
+
+static int clamp_h(int64_t H) { return H < 0 || H > INT_MAX ? 0 : (int)H; }  // 0 is refused
+
+w8a8_status block_norm(const void *residual, int64_t ldr, const void *y, int64_t ldy,
+                       int post_norm, const float *post_weight, const void *gate, int64_t ldg,
+                       float scale, const float *weight, float eps, int64_t T, int64_t H,
+                       mxfp4_dtype dtype, void *new_residual, void *out, void *stream) {
+    return norm_entry({residual, y, gate, ldr, ldy, ldg, post_weight, weight, post_norm, scale, eps, T,
+                       clamp_h(H), new_residual, out, nullptr},
+                      selector(&dtype), block::kSame, stream);
+}
+
+w8a8_status block_norm_w8a8(const void *residual, int64_t ldr, const void *y, int64_t ldy,
+                            int post_norm, const float *post_weight, const void *gate,
+                            int64_t ldg, float scale, const float *weight, float eps, int64_t T,
+                            int64_t H, mxfp4_dtype dtype, void *new_residual, int8_t *xq,
+                            float *x_scale, void *stream) {
+    return norm_entry({residual, y, gate, ldr, ldy, ldg, post_weight, weight, post_norm, scale, eps, T,
+                       clamp_h(H), new_residual, xq, x_scale},
+                      selector(&dtype), block::kInt8, stream);
+}
+
+w8a8_status block_norm_mxfp4(const void *residual, int64_t ldr, const void *y, int64_t ldy,
+                             int post_norm, const float *post_weight, const void *gate,
+                             int64_t ldg, float scale, const float *weight, float eps, int64_t T,
+                             int64_t H, mxfp4_dtype dtype, void *new_residual, uint8_t *codes,
+                             uint8_t *scales, void *stream) {
+    return norm_entry({residual, y, gate, ldr, ldy, ldg, post_weight, weight, post_norm, scale, eps, T,
+                       clamp_h(H), new_residual, codes, scales},
+                      selector(&dtype), block::kMxfp4, stream);
+}
+
+int64_t block_norm_backward_workspace(int64_t T, int64_t H) {
+    return norm_shape(T, H) == W8A8_OK ? block::backward_workspace(T, H) : 0;
+}
+
+w8a8_status block_norm_backward(const void *d_out, int64_t ldo, const void *d_new, int64_t ldn,
+                                const void *new_residual, int64_t ldr, const void *y, int64_t ldy,
+                                int post_norm, const float *post_weight, const void *gate,
+                                int64_t ldg, float scale, const float *weight, float eps,
+                                int64_t T, int64_t H, mxfp4_dtype dtype, void *d_residual,
+                                void *d_y, void *d_gate, float *d_weight, float *d_post_weight,
+                                void *workspace, int64_t workspace_bytes, void *stream) {
+    if (w8a8_status s = norm_shape(T, H)) return s;
+    const int dt = selector(&dtype);
+    if (!mx_dtype_ok(dt)) return W8A8_ERR_DTYPE;
+    if (w8a8_status s = norm_scalars(scale, eps)) return s;
+    if (!y && T > 0) gate = nullptr, post_norm = 0;
+    if (!gate) d_gate = nullptr;
+    if (!post_norm) d_post_weight = nullptr;
+    const int64_t need = block::backward_workspace(T, H);
+    if (ldo < H || ldo > INT_MAX || ldr < H || ldr > INT_MAX || short_rows(d_new, ldn, H) ||
+        short_rows(y, ldy, H) || (ldg != 0 && short_rows(gate, ldg, H)) || workspace_bytes < need)
+        return W8A8_ERR_SHAPE;
+    if (T > 0 && (!d_out || !new_residual || !d_residual || (y && !d_y) || !workspace))
+        return W8A8_ERR_NULL;
+    const int64_t size = dtype_size(dt);
+    if (odd(d_out, size) || odd(d_new, size) || odd(new_residual, size) || odd(y, size) ||
+        odd(d_residual, size) || odd(d_y, size) || bad_gate(gate, ldg, size) ||
+        bad_gate(d_gate, ldg, size) || misaligned(weight) || misaligned(post_weight) ||
+        misaligned(d_weight) || misaligned(d_post_weight) || misaligned(workspace))
+        return W8A8_ERR_ALIGN;
+    const block::Backward a{d_out, d_new, new_residual, y, gate, ldo, ldn, ldr, ldy, ldg, post_weight,
+                            weight, post_norm, scale, eps, T, (int)H, d_residual, d_y, d_gate, d_weight,
+                            d_post_weight, static_cast<float *>(workspace)};
+    return hip_status(block::launch_backward(a, dt, static_cast<hipStream_t>(stream)));
 }
 
 const char *w8a8_status_string(int status) {

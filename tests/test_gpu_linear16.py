@@ -1,0 +1,224 @@
+"""16-bit products with an epilogue, their gradients, and the int8 product's epilogue, on the GPU against
+their definitions in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+from quantized_gemm_quantize_amd import binding as b
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+# (rows, channels, inner): one token, a few, ragged sizes, sizes under and over every tile, long inner axes
+SIZES = [(1, 8, 8), (1, 64, 4096), (2, 1040, 1312), (3, 72, 40), (5, 4096, 512), (16, 136, 4104), (17, 520, 1000),
+         (33, 264, 2056), (64, 1024, 1024), (65, 256, 256), (127, 200, 328), (129, 136, 72), (257, 1040, 1312),
+         (300, 72, 8200), (513, 520, 136), (1000, 8, 1024), (1030, 2056, 200)]
+
+
+def case(M, N, K, dtype, seed):
+    rng = np.random.default_rng(seed)
+    v = {}
+    for name, shape, size in (("x", (M, K), 1.0), ("w", (N, K), K ** -0.5), ("residual", (M, N), 1.0),
+                              ("d_out", (M, N), 1.0), ("pre", (M, N), 1.5)):
+        v[name], v[name + "64"] = ref.rounded(rng.standard_normal(shape) * size, dtype)
+        v[name] = v[name].to(DEV)
+    v["bias"], v["bias64"] = ref.rounded(rng.standard_normal(N), "f32")
+    v["bias"] = v["bias"].to(DEV)
+    return v
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_forward(dtype, M, N, K):
+    v = case(M, N, K, dtype, seed=M + N)
+    a = ref.ACTIVATIONS[(M + N) // 8 % 5]
+    pre, e_pre, out, e_out = ref.linear(v["x64"], v["w64"], v["bias64"], a, v["residual64"])
+    got, got_pre = b.w16a16_linear(v["x"], v["w"], bias=v["bias"], activation=a, residual=v["residual"], pre=True)
+    ref.close(got_pre, pre, e_pre, dtype, "pre")
+    ref.close(got, out, e_out, dtype, "out")
+    _, _, out, e_out = ref.linear(v["x64"], v["w64"])
+    ref.close(b.w16a16_linear(v["x"], v["w"]), out, e_out, dtype, "product")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [1, 30, 200])
+@pytest.mark.parametrize("a", ref.ACTIVATIONS)
+def test_epilogues(dtype, M, a):
+    N, K = 136, 264
+    v = case(M, N, K, dtype, seed=11)
+    for bias in (False, True):
+        for residual in (False, True):
+            args = [v["x64"], v["w64"], v["bias64"] if bias else None, a, v["residual64"] if residual else None]
+            _, _, out, e = ref.linear(*args)
+            got = b.w16a16_linear(v["x"], v["w"], bias=v["bias"] if bias else None, activation=a,
+                                  residual=v["residual"] if residual else None)
+            ref.close(got, out, e, dtype, f"{bias} {residual}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_backward(dtype, M, N, K):
+    v = case(M, N, K, dtype, seed=M + K)
+    a = ref.ACTIVATIONS[1 + (M + K) // 8 % 4]
+    check_backward(v, dtype, a)
+    check_backward(v, dtype, "none")
+
+
+def check_backward(v, dtype, a, d_out=None, x=None):
+    x = v["x"] if x is None else x
+    d_out = v["d_out"] if d_out is None else d_out
+    d_x, d_w, d_bias, d_pre = b.w16a16_linear_backward(d_out, x, v["w"], pre=v["pre"] if a != "none" else None,
+                                                       activation=a)
+    f = ref.slope(v["pre64"], a)
+    d = v["d_out64"] * f
+    e = np.abs(v["d_out64"]) * (ref.SLOPE + ref.U * np.abs(f)) * (a != "none")
+    if a == "none":
+        assert d_pre is d_out
+    else:
+        ref.close(d_pre, d, e, dtype, "d_pre")
+    ref.close(d_bias, d.sum(axis=0), (e + ref.SUM * np.abs(d)).sum(axis=0), "f32", "d_bias")
+    got = d_pre.double().cpu().numpy()   # the operand of the products, as rounded
+    want, bound = ref.product(got, np.ascontiguousarray(v["w64"].T))
+    ref.close(d_x, want, bound, dtype, "d_x")
+    want, bound = ref.product(np.ascontiguousarray(got.T), np.ascontiguousarray(v["x64"].T))
+    ref.close(d_w, want, bound, dtype, "d_w")
+    again = b.w16a16_linear_backward(d_out, x, v["w"], pre=v["pre"] if a != "none" else None, activation=a)
+    assert all(torch.equal(p, q) for p, q in zip((d_x, d_w, d_bias, d_pre), again))
+
+
+def apart(t, extra):
+    """The same rows with a stride of width + extra elements; the gaps hold NaN."""
+    m, n = t.shape
+    rows = torch.full((m, n + extra), float("nan"), dtype=t.dtype, device=t.device)[:, :n]
+    rows.copy_(t)
+    return rows
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(1, 1040, 1312), (50, 264, 136), (300, 520, 328)])
+def test_rows_apart(dtype, M, N, K):
+    v = case(M, N, K, dtype, seed=12)
+    _, _, out, e = ref.linear(v["x64"], v["w64"], v["bias64"], "silu", v["residual64"])
+    got = b.w16a16_linear(apart(v["x"], 8), v["w"], bias=v["bias"], activation="silu", residual=apart(v["residual"], 24))
+    ref.close(got, out, e, dtype)
+    check_backward(v, dtype, "gelu", d_out=apart(v["d_out"], 8), x=apart(v["x"], 16))
+    check_backward(v, dtype, "none", d_out=apart(v["d_out"], 8), x=apart(v["x"], 16))
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_residual_in_place_and_rows_behind(M):
+    v = case(M, 264, 520, "bf16", seed=13)
+    want = b.w16a16_linear(v["x"], v["w"], bias=v["bias"], activation="gelu", residual=v["residual"])
+    buffer = torch.full((M + 5, 264), 7.0, dtype=torch.bfloat16, device=DEV)
+    buffer[:M] = v["residual"]
+    got = b.w16a16_linear(v["x"], v["w"], bias=v["bias"], activation="gelu", residual=buffer[:M], out=buffer[:M])
+    assert torch.equal(got, want) and (buffer[M:] == 7).all()
+
+
+def test_wanted_gradients_only():
+    v = case(70, 136, 264, "bf16", seed=14)
+    full = b.w16a16_linear_backward(v["d_out"], v["x"], v["w"], pre=v["pre"], activation="silu")
+    for i, name in enumerate(("d_x", "d_w", "d_bias")):
+        some = b.w16a16_linear_backward(v["d_out"], v["x"], v["w"], pre=v["pre"], activation="silu",
+                                        **{k: k == name for k in ("d_x", "d_w", "d_bias")})
+        assert all((g is None) if j != i and j < 3 else torch.equal(g, full[j]) for j, g in enumerate(some))
+    for a in ("none", "silu"):
+        nothing = b.w16a16_linear_backward(v["d_out"], v["x"], v["w"], pre=v["pre"], activation=a, d_x=False, d_w=False,
+                                           d_bias=False)
+        assert nothing[:3] == (None, None, None)
+
+
+def test_no_rows():
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
+    w = torch.ones((72, 64), dtype=torch.bfloat16, device=DEV)
+    d = torch.empty((0, 72), dtype=torch.bfloat16, device=DEV)
+    assert b.w16a16_linear(x, w).shape == (0, 72)
+    d_w, d_bias = torch.ones_like(w), torch.ones(72, device=DEV)
+    for a in ("none", "gelu"):
+        b.w16a16_linear_backward(d, x, w, pre=d, activation=a, d_w=d_w.fill_(1), d_bias=d_bias.fill_(1))
+        assert (d_w == 0).all() and (d_bias == 0).all()
+
+
+# values through an activation: x = [v, 0, ...], w = [1, 0, ...] give pre = v exactly
+VALUES = np.concatenate([-np.exp2(np.linspace(-20, 6.6, 400)), [0.0], np.exp2(np.linspace(-20, 16, 500))])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("a", ref.ACTIVATIONS)
+def test_activation_values(dtype, a):
+    """Both tails keep their relative precision down to the smallest normal number of the type."""
+    values = VALUES[np.abs(VALUES) < 6e4] if dtype == "f16" else VALUES
+    x, x64 = ref.rounded(np.pad(values[:, None], ((0, 0), (0, 7))), dtype)
+    w = torch.zeros((8, 8), dtype=ref.TYPES[dtype])
+    w[:, 0] = 1
+    want = np.repeat(ref.act(x64[:, :1], a), 8, axis=1)
+    got = b.w16a16_linear(x.to(DEV), w.to(DEV), activation=a)
+    ref.close(got, want, ref.ACT * np.abs(want), dtype)
+    pre = x[:, :1].repeat(1, 8).to(DEV)
+    f = ref.slope(x64[:, :1].repeat(8, axis=1), a)
+    d_pre = b.w16a16_linear_backward(torch.ones_like(pre), x.to(DEV), w.to(DEV), pre=pre, activation=a)[3]
+    ref.close(d_pre, f, ref.SLOPE * np.minimum(1.0, 1e3 * np.abs(f) + 1e-30), dtype)
+
+
+def test_not_finite():
+    """An infinity or NaN of a row stays in its row; of a channel, in its channel."""
+    for M in (4, 100):
+        v = case(M, 136, 264, "bf16", seed=15)
+        v["x"][1, 3], v["w"][5, 7] = float("nan"), float("inf")
+        out = b.w16a16_linear(v["x"], v["w"], activation="relu")
+        bad = torch.zeros((M, 136), dtype=torch.bool, device=DEV)
+        bad[1], bad[:, 5] = True, True
+        assert out[~bad].isfinite().all() and out[1].isnan().all()
+        assert not (out[:, 5].isfinite() & (out[:, 5] != 0)).any()   # -inf times a negative slope is 0
+
+
+# ------------------------------------------------------------------ the int8 product's epilogue
+
+@pytest.mark.parametrize("M,N,K", [(1, 16, 16), (1, 512, 4096), (7, 272, 1312), (16, 1040, 4096), (16, 272, 8192),
+                                   (17, 272, 512), (33, 528, 1040), (64, 272, 4096), (65, 144, 528), (257, 1040, 1312),
+                                   (1000, 16, 96), (2048, 1040, 1024), (8200, 8208, 256), (8200, 8208, 1040)])
+def test_w8a8_act(M, N, K):
+    rng = np.random.default_rng(M + K)
+    xq, wq = (rng.integers(-127, 128, s).astype(np.int8) for s in ((M, K), (N, K)))
+    sx, sw = (np.exp2(rng.uniform(-9, -5, n)).astype(np.float32) for n in (M, N))
+    sw /= np.float32(np.sqrt(K))
+    bias = rng.standard_normal(N).astype(np.float32)
+    res, res64 = ref.rounded(rng.standard_normal((M, N)), "bf16")
+    a = ref.ACTIVATIONS[(M + N + K) // 16 % 5]
+    t = [torch.from_numpy(v).to(DEV) for v in (xq, sx, wq, sw)]
+    # the products in binary32 are exact here: sums below 2^24 by parts of 1024
+    acc = np.zeros((M, N))
+    for k in range(0, K, 1024):
+        acc += xq[:, k:k + 1024].astype(np.float32) @ wq[:, k:k + 1024].astype(np.float32).T
+    pre = acc * sx[:, None].astype(np.float64) * sw.astype(np.float64)
+    for with_bias, with_residual in ((True, True), (False, False)):
+        p = pre + bias if with_bias else pre
+        e = 2.0 ** -22 * np.abs(pre) + ref.U * np.abs(p)
+        out = ref.act(p, a)
+        e = ref.STEEPEST * e + ref.ACT * np.abs(out)
+        if with_residual:
+            out = out + res64
+            e = e + ref.U * np.abs(out)
+        got = b.w8a8_gemm_act(*t, bias=torch.from_numpy(bias).to(DEV) if with_bias else None, activation=a,
+                              residual=res.to(DEV) if with_residual else None)
+        ref.close(got, out, e, "bf16", f"{with_bias}")
+    # in place, rows behind the last left as they were, rows apart
+    want = b.w8a8_gemm_act(*t, activation=a, residual=res.to(DEV))
+    buffer = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    buffer[:M] = res.to(DEV)
+    b.w8a8_gemm_act(*t, activation=a, residual=buffer[:M], out=buffer[:M])
+    assert torch.equal(buffer[:M], want) and (buffer[M:] == 7).all()
+    assert torch.equal(b.w8a8_gemm_act(*t, activation=a, residual=apart(res.to(DEV), 8)), want)
+    if a == "none":
+        assert torch.equal(b.w8a8_gemm_act(*t), b.w8a8_gemm(*t))
+
+
+def test_w8a8_act_huge_scales():
+    """Rows whose scaled product leaves binary32's range only in between."""
+    xq = torch.full((70, 64), 127, dtype=torch.int8, device=DEV)
+    wq = torch.full((32, 64), 127, dtype=torch.int8, device=DEV)
+    sx = torch.full((70,), 1e37, device=DEV)
+    sw = torch.full((32,), 1e-36, device=DEV)
+    for m in (5, 70):
+        out = b.w8a8_gemm_act(xq[:m], sx[:m], wq, sw)
+        assert torch.equal(out, b.w8a8_gemm(xq[:m], sx[:m], wq, sw)) and out.isfinite().all()
