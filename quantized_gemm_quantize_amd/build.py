@@ -25,7 +25,8 @@ PEAKS_SOURCE = "peaks.hip"
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["quantize_rows.hip", "gemm_tiled.hip", "gemm_decode.hip", "bsr_gemm.hip", "sparse24.hip",
            "w4a16.hip", "mxfp4_quantize.hip", "mxfp4_gemm.hip", "mxfp4_tiled.hip", "mxfp4_decode.hip", "moe_route.hip",
-           "norm.hip", "norm_backward.hip", "linear16.hip", "w8a8_abi.hip"]
+           "norm.hip", "norm_backward.hip", "linear16.hip", "linear16_tiled.hip", "linear16_decode.hip",
+           "w8a8_abi.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,11 +1,12 @@
-// 16-bit products with bias, activation and residual, and their gradients.
+// 16-bit products with bias, activation and residual, and their gradients:
+// which kernel computes a product, and the pass before the gradients' products.
 //
 //   forward   pre = x w^T + bias, out = act(pre) + residual
 //   backward  d_pre = d_out act'(pre), d_bias = sum_m d_out act'(pre),
 //             d_x = d_pre w, d_w = d_pre^T x
 //
-// One kernel for the three products: 64 x 64 tiles, 16 steps of k in LDS as
-// binary32, 4 x 4 outputs per thread.
+// d_pre is rounded to the rows' type: it is an operand of the matrix instructions,
+// and a result of its own. d_bias is summed from the unrounded values.
 #include <algorithm>
 
 #include "activation.hpp"
@@ -18,122 +19,177 @@ namespace {
 
 using namespace rows;
 
-constexpr int kTile = 64, kDepth = 16;
+// ---------------------------------------------------------------- plans
 
-template <Dtype D>
-__global__ __launch_bounds__(256) void product_kernel(Operand a, Operand b, int64_t M, int64_t N, int64_t K, Epilogue ep) {
-    __shared__ float ta[kDepth][kTile + 1], tb[kDepth][kTile + 1];
-    w8a8::lds_poison(ta);
-    w8a8::lds_poison(tb);
-    w8a8::lds_poison_done();
-    const int64_t tiles_n = (N + kTile - 1) / kTile;
-    const int64_t m0 = blockIdx.x / tiles_n * kTile, n0 = blockIdx.x % tiles_n * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    auto load = [&](const Operand &o, int64_t r0, int64_t rows, int64_t k0, float (&to)[kDepth][kTile + 1]) {
-        for (int i = threadIdx.x; i < kDepth * kTile; i += 256) {
-            const int r = o.k_major ? i % kTile : i / kDepth, k = o.k_major ? i / kTile : i % kDepth;
-            float v = 0.0f;
-            if (r0 + r < rows && k0 + k < K)
-                v = widen<D>(static_cast<const uint16_t *>(o.p)[o.k_major ? (k0 + k) * o.ld + r0 + r : (r0 + r) * o.ld + k0 + k]);
-            to[k][r] = v;
-        }
-    };
-    for (int64_t k0 = 0; k0 < K; k0 += kDepth) {
-        load(a, m0, M, k0, ta);
-        load(b, n0, N, k0, tb);
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(ta[k][ty * 4 + i], tb[k][tx + 16 * j], acc[i][j]);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + ty * 4 + i;
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tx + 16 * j;
-            v[j] = acc[i][j];
-            if (m < M && n < N) {
-                if (ep.bias) v[j] += ep.bias[n];
-                if (ep.pre) static_cast<uint16_t *>(ep.pre)[m * N + n] = narrow<D>(v[j]);
-            }
-        }
-        act::activate(ep.act, v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tx + 16 * j;
-            if (m >= M || n >= N) continue;
-            if (ep.residual) v[j] += widen<D>(static_cast<const uint16_t *>(ep.residual)[m * ep.ldr + n]);
-            static_cast<uint16_t *>(ep.out)[m * N + n] = narrow<D>(v[j]);
-        }
-    }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Time of a round of tiles (all that run at once) in us: a fixed part (first loads, epilogue) and a
+// part per 64 k, which grows from lo to hi as the chip fills (its power is shared). Measured in HIP
+// graphs with bf16 rows of random values, between 1/4 and all of the tiles that run at once, K 512 and 2048.
+struct FormTime {
+    int bm, bn, slots;          // tiles that run at once on 256 CUs
+    double fixed, lo, hi;
+};
+constexpr FormTime kTimes[kForms] = {
+    {64, 64, 768, 3.5, 0.24, 0.53},   // k64x64
+    {128, 128, 256, 4.8, 0.40, 0.49}, // k128x128deep
+    {128, 128, 512, 4.0, 0.64, 0.90}, // k128x128
+    {256, 128, 256, 6.0, 0.63, 0.82}, // k256x128
+    {256, 256, 256, 10.0, 1.10, 1.41} // k256x256
+};
+
+double round_time(const FormTime &f, int64_t units, int64_t stages) {
+    const double fill = (double)units / f.slots;
+    return f.fixed + stages * (f.lo + (f.hi - f.lo) * fill * fill);
 }
 
-template <int A, Dtype D>
-__device__ __forceinline__ float d_value(float d, float p) { return d * act::slope<A>(p); }
+struct Estimate {
+    Plan plan;
+    double us;
+};
 
-// d_pre and the column sums of d_out act'(pre): a workgroup takes every G-th
-// block of rows of 64 columns and leaves one partial sum per column.
+// The plan with the least estimated time: every tile, or all but the last whole rounds' rest, to one
+// workgroup; the rest's tiles are shared along k by as many workgroups as run at once (at least
+// two stages each), whose partial sums a second launch joins (3 us and their bytes at 4.5 TB/s).
+// What splitting the rest is worth: 16448 x 5120 x 1280 (1300 tiles of 256 x 256, 1280 of them in five
+// rounds) 207 -> 193 us, 16448 x 1280 x 5120 (325 tiles) 218 -> 181; 257 x 1040 x 1312 (85 tiles of
+// 64 x 64, three workgroups each) 12.8 -> 10.4.
+Estimate estimate(int64_t M, int64_t N, int64_t K) {
+    Estimate best{{k64x64, 0, 1, 0}, -1};
+    const int64_t stages = ceil_div(K, 64);
+    for (int i = 0; i < kForms; ++i) {
+        const FormTime &f = kTimes[i];
+        const int64_t tiles = ceil_div(M, f.bm) * ceil_div(N, f.bn), rounds = tiles / f.slots, rest = tiles % f.slots;
+        const double whole = rounds * round_time(f, f.slots, stages);
+        auto offer = [&](double us, int64_t splits) {
+            if (best.us >= 0 && us >= best.us) return;
+            const int64_t shared = splits > 1 ? rest : 0;
+            best = {{(Form)i, (int)(tiles - shared), (int)splits, shared * splits * f.bm * f.bn * 4}, us};
+        };
+        offer(whole + (rest ? round_time(f, rest, stages) : 0.0), 1);
+        if (!rest) continue;
+        const int64_t most = std::min(f.slots / rest, stages / 2);
+        for (int64_t s = 2; s <= most; ++s) {
+            // the largest number of workgroups for every number of stages in a part
+            if (s < most && ceil_div(stages, s) == ceil_div(stages, s + 1)) continue;
+            const double bytes = 2.0 * rest * s * f.bm * f.bn * 4;
+            offer(whole + round_time(f, rest * s, ceil_div(stages, s)) + 3.0 + bytes / 4.5e6, s);
+        }
+    }
+    return best;
+}
+
+// The kernel of few rows: up to 16 rows always (1 x 4096 x 4096 5.8 us against 13 in tiles), up to 64
+// where it is estimated to be quicker: 3 us and both operands of a workgroup at 65 GB/s a round
+// (64 rows: 4096 x 4096 11.7 us against 13.0, 8192 x 2048 14.9 / 12.2, 4096 x 11008 32.7 / 23.7).
+bool few_rows(int64_t M, int64_t N, int64_t K, const Estimate &tiled) {
+    if (M > kMaxRows) return false;
+    if (M <= 16) return true;
+    const int64_t rounds = ceil_div(ceil_div(N, 16), 256);
+    return rounds * (3.0 + 2.0 * K * 16 * (ceil_div(M, 16) + 1) / 65e3) < tiled.us;
+}
+
+hipError_t product(const Operand &a, const Operand &b, int64_t M, int64_t N, int64_t K, bool f16, const Epilogue &ep,
+                   void *workspace, hipStream_t stream) {
+    return launch_tiled(a, b, M, N, K, f16, estimate(M, N, K).plan, static_cast<float *>(workspace), ep, stream);
+}
+
+// ---------------------------------------------------------------- d_pre and d_bias
+
+// A thread takes 8 columns of every 32nd row of its workgroup's rows; a workgroup 64 columns
+// (8 threads) and 32 rows at a time, every G-th. Column sums are kept in registers, joined in LDS and left
+// as one partial per workgroup row.
+constexpr int kColumns = 64, kRowsAtOnce = 32;
+
+template <int A, Dtype D>
+__device__ __forceinline__ void slopes(float (&d)[8], uint4 pre) {
+    float p[8];
+    widen_chunk<D>(pre, p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] *= act::slope<A>(p[e]);
+}
+
 template <Dtype D>
-__global__ __launch_bounds__(256) void slope_kernel(const uint16_t *d_out, int64_t ldd, const uint16_t *pre, int64_t M,
-                                                    int64_t N, int a, uint16_t *d_pre, float *partial) {
+__global__ __launch_bounds__(256) void slope_kernel(const uint16_t *__restrict__ d_out, int64_t ldd,
+                                                    const uint16_t *__restrict__ pre, int64_t M, int64_t N, int a,
+                                                    uint16_t *__restrict__ d_pre, float *__restrict__ partial) {
+    __shared__ float red[kRowsAtOnce][kColumns];
+    w8a8::lds_poison(red);
+    w8a8::lds_poison_done();
+    const int c = threadIdx.x % 8 * 8, r = threadIdx.x / 8;
+    const int64_t n = (int64_t)blockIdx.x * kColumns + c;
+    float sum[8] = {};
+    if (n < N)
+        for (int64_t m = (int64_t)blockIdx.y * kRowsAtOnce + r; m < M; m += (int64_t)gridDim.y * kRowsAtOnce) {
+            float d[8];
+            widen_chunk<D>(w8a8::load16_stream(d_out + m * ldd + n), d);
+            if (a != act::kNone) {
+                const uint4 p = w8a8::load16_stream(pre + m * N + n);
+                switch (a) {
+                    case act::kRelu: slopes<act::kRelu, D>(d, p); break;
+                    case act::kGelu: slopes<act::kGelu, D>(d, p); break;
+                    case act::kGeluTanh: slopes<act::kGeluTanh, D>(d, p); break;
+                    default: slopes<act::kSilu, D>(d, p); break;
+                }
+                *reinterpret_cast<uint4 *>(d_pre + m * N + n) = narrow_chunk<D>(d);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += d[e];
+        }
+    if (!partial) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[r][c + e] = sum[e];
+    __syncthreads();
+    if (threadIdx.x >= kColumns || (int64_t)blockIdx.x * kColumns + threadIdx.x >= N) return;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRowsAtOnce; ++i) s += red[i][threadIdx.x];
+    partial[blockIdx.y * N + (int64_t)blockIdx.x * kColumns + threadIdx.x] = s;
+}
+
+// d_bias[n] = sum of the G partials of column n, in order within 4 slices, then the slices.
+__global__ __launch_bounds__(256) void sum_kernel(const float *__restrict__ partial, int G, int64_t N,
+                                                  float *__restrict__ out) {
     __shared__ float red[4][64];
     w8a8::lds_poison(red);
     w8a8::lds_poison_done();
-    const int c = threadIdx.x % 64, s = threadIdx.x / 64;
+    const int c = threadIdx.x % 64, slice = threadIdx.x / 64;
     const int64_t n = (int64_t)blockIdx.x * 64 + c;
-    float sum = 0.0f;
-    if (n < N)
-        for (int64_t m = blockIdx.y * 4 + s; m < M; m += gridDim.y * 4) {
-            float d = widen<D>(d_out[m * ldd + n]);
-            if (a != act::kNone) {
-                const float p = widen<D>(pre[m * N + n]);
-                d *= a == act::kRelu ? act::slope<act::kRelu>(p) : a == act::kGelu ? act::slope<act::kGelu>(p)
-                   : a == act::kGeluTanh ? act::slope<act::kGeluTanh>(p) : act::slope<act::kSilu>(p);
-                d_pre[m * N + n] = narrow<D>(d);
-            }
-            sum += d;
-        }
-    if (!partial) return;
-    red[s][c] = sum;
-    __syncthreads();
-    if (s || n >= N) return;
-    for (int i = 1; i < 4; ++i) sum += red[i][c];
-    partial[blockIdx.y * N + n] = sum;
-}
-
-__global__ __launch_bounds__(256) void sum_kernel(const float *partial, int G, int64_t N, float *out) {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= N) return;
     float s = 0.0f;
-    for (int g = 0; g < G; ++g) s += partial[g * N + n];
-    out[n] = s;
+    if (n < N)
+        for (int g = slice; g < G; g += 4) s += partial[g * N + n];
+    red[slice][c] = s;
+    __syncthreads();
+    if (slice || n >= N) return;
+    out[n] = ((s + red[1][c]) + red[2][c]) + red[3][c];
 }
 
-int sum_groups(int64_t M) { return (int)std::min<int64_t>(64, (M + 3) / 4); }
-
-hipError_t product(Operand a, Operand b, int64_t M, int64_t N, int64_t K, bool f16, const Epilogue &ep, hipStream_t stream) {
-    const dim3 grid((unsigned)(((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile)));
-    if (f16) product_kernel<kF16><<<grid, 256, 0, stream>>>(a, b, M, N, K, ep);
-    else product_kernel<kBf16><<<grid, 256, 0, stream>>>(a, b, M, N, K, ep);
-    return hipGetLastError();
+// Workgroup rows: enough to fill the chip eight times, at least one turn each.
+int sum_groups(int64_t M, int64_t N) {
+    return (int)std::min(ceil_div(M, kRowsAtOnce), std::max<int64_t>(1, 2048 / ceil_div(N, kColumns)));
 }
+
+int64_t sums_bytes(int64_t M, int64_t N) { return (4 * N * sum_groups(M, N) + 255) / 256 * 256; }
 
 }  // namespace
 
-int64_t forward_workspace(int64_t, int64_t, int64_t) { return 0; }
+int64_t forward_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M == 0) return 0;
+    const Estimate e = estimate(M, N, K);
+    return few_rows(M, N, K, e) ? 0 : e.plan.workspace;
+}
 
-int64_t backward_workspace(int64_t M, int64_t N, int64_t) { return 4 * N * sum_groups(M); }
+int64_t backward_workspace(int64_t M, int64_t N, int64_t K) {
+    // the products run one after the other; the column sums are done before them
+    const int64_t d_x = M ? estimate(M, K, N).plan.workspace : 0, d_w = estimate(N, K, M).plan.workspace;
+    return std::max(sums_bytes(M, N), std::max(d_x, d_w));
+}
 
 hipError_t launch_forward(const void *x, int64_t ldx, int64_t M, const void *w, int64_t N, int64_t K, bool f16,
-                          const Epilogue &ep, void *, hipStream_t stream) {
-    return product({x, ldx, false}, {w, K, false}, M, N, K, f16, ep, stream);
+                          const Epilogue &ep, void *workspace, hipStream_t stream) {
+    const Estimate e = estimate(M, N, K);
+    if (few_rows(M, N, K, e)) return launch_rows(x, ldx, (int)M, w, (int)N, (int)K, f16, ep, stream);
+    return launch_tiled({x, ldx, false}, {w, K, false}, M, N, K, f16, e.plan, static_cast<float *>(workspace), ep, stream);
 }
 
 hipError_t launch_backward(const void *d_out, int64_t ldd, const void *x, int64_t ldx, const void *w, const void *pre,
@@ -141,26 +197,26 @@ hipError_t launch_backward(const void *d_out, int64_t ldd, const void *x, int64_
                            float *d_bias, void *workspace, hipStream_t stream) {
     hipError_t e = hipSuccess;
     if (a != act::kNone || d_bias) {
-        const int G = sum_groups(M);
-        const dim3 grid((unsigned)((N + 63) / 64), (unsigned)G);
+        const int G = sum_groups(M, N);
         float *partial = d_bias ? static_cast<float *>(workspace) : nullptr;
-        const uint16_t *d = static_cast<const uint16_t *>(d_out), *p = static_cast<const uint16_t *>(pre);
-        uint16_t *to = static_cast<uint16_t *>(d_pre);
         if (G) {
+            const dim3 grid((unsigned)ceil_div(N, kColumns), (unsigned)G);
+            const uint16_t *d = static_cast<const uint16_t *>(d_out), *p = static_cast<const uint16_t *>(pre);
+            uint16_t *to = static_cast<uint16_t *>(d_pre);
             if (f16) slope_kernel<kF16><<<grid, 256, 0, stream>>>(d, ldd, p, M, N, a, to, partial);
             else slope_kernel<kBf16><<<grid, 256, 0, stream>>>(d, ldd, p, M, N, a, to, partial);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         if (d_bias) {
-            sum_kernel<<<dim3((unsigned)((N + 255) / 256)), 256, 0, stream>>>(partial, G, N, d_bias);
+            sum_kernel<<<dim3((unsigned)ceil_div(N, 64)), 256, 0, stream>>>(partial, G, N, d_bias);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
     }
-    if (a == act::kNone) d_pre = const_cast<void *>(d_out);
-    const int64_t ld = a == act::kNone ? ldd : N;
-    if (d_x && M && (e = product({d_pre, ld, false}, {w, K, true}, M, K, N, f16, Epilogue{nullptr, nullptr, 0, nullptr, d_x, 0}, stream)) != hipSuccess)
+    const Operand rows{a == act::kNone ? d_out : d_pre, a == act::kNone ? ldd : N, false};
+    auto plain = [](void *out) { return Epilogue{nullptr, nullptr, 0, nullptr, out, act::kNone}; };
+    if (d_x && M && (e = product(rows, {w, K, true}, M, K, N, f16, plain(d_x), workspace, stream)) != hipSuccess)
         return e;
-    if (d_w) return product({d_pre, ld, true}, {x, ldx, true}, N, K, M, f16, Epilogue{nullptr, nullptr, 0, nullptr, d_w, 0}, stream);
+    if (d_w) return product({rows.p, rows.ld, true}, {x, ldx, true}, N, K, M, f16, plain(d_w), workspace, stream);
     return hipSuccess;
 }
 

@@ -1,6 +1,7 @@
 // Arguments of the 16-bit products (linear16.hip) and their epilogue.
 #pragma once
 
+#include <hip/hip_runtime.h>
 #include <stdint.h>
 
 namespace linear16 {
@@ -22,5 +23,22 @@ struct Operand {
     int64_t ld;
     bool k_major;
 };
+
+// The tiles of a product, how many of them (the first ones in the tile order) one workgroup computes
+// whole, and how many workgroups share each other one along k.
+enum Form { k64x64, k128x128deep, k128x128, k256x128, k256x256, kForms };
+struct Plan {
+    Form form;
+    int whole, splits;
+    int64_t workspace;   // bytes of partial sums
+};
+
+hipError_t launch_tiled(const Operand &a, const Operand &b, int64_t M, int64_t N, int64_t K, bool f16, const Plan &plan,
+                        float *partial, const Epilogue &ep, hipStream_t stream);
+
+// The product of up to kMaxRows rows, in one launch without a workspace.
+constexpr int kMaxRows = 64;
+hipError_t launch_rows(const void *x, int64_t ldx, int M, const void *w, int N, int K, bool f16, const Epilogue &ep,
+                       hipStream_t stream);
 
 }  // namespace linear16

@@ -1,0 +1,416 @@
+// LDS-tiled 16-bit products with the epilogue fused, for the forward pass and
+// both gradients.
+//
+//   out[m, n] = epilogue( sum_k a(m, k) b(n, k) )
+//
+// An operand is row-major (k contiguous: x and w of the forward pass, d_pre of
+// d_x) or k-major (the rows contiguous: w of d_x, d_pre and x of d_w). No operand
+// is transposed in memory: a k-major tile is staged as it lies, 64 rows of k, and
+// its fragments are read with gfx950's transposing LDS read
+// (ds_read_b64_tr_b16: 16 lanes that address 4 rows of 16 elements receive a
+// column of 4 each), so both kinds take the same loads and matrix instructions.
+//
+//  - A workgroup of GM x GN wavefronts computes a BM x BN tile, each wavefront a
+//    part of 16 x 16 tiles of v_mfma_f32_16x16x32 (bf16 or binary16, fp32 accumulators).
+//  - Stages of 64 k travel global -> LDS with 16-byte direct-to-LDS loads through two
+//    buffers, each stage's loads between the MFMAs of the stage before.
+//    Row-major tiles: 128-byte rows, chunk c of row r at slot c ^ swz(r). k-major tiles:
+//    rows of BM or BN elements, chunk c of row k at slot c ^ 4 (k % 4): the
+//    four rows that half a wavefront reads at once lie in different banks.
+//  - Rows past the operand's end are read from its last row (never stored); k past its
+//    end is zeroed in LDS on both sides, whatever lies there in memory.
+//  - The MFMA takes b first: a lane ends with 4 consecutive outputs of a row. They
+//    are staged in fp32 in the wavefront's share of LDS, and bias, activation and
+//    residual act on 8 consecutive outputs per lane; the residual is read and the
+//    outputs written in whole 16-byte pieces by the same lane (in-place residuals).
+//  - With splits > 1, workgroups of one tile take ranges of the stages and leave fp32 partial
+//    tiles in a workspace, which join_kernel adds in order and finishes.
+//  - Tiles are assigned XCD-contiguously, in groups of 8 tile rows, so that tiles that
+//    run at once share operand rows in the same L2.
+#include "activation.hpp"
+#include "launch.hpp"
+#include "linear16.hpp"
+#include "linear16_mfma.hpp"
+#include "rows.hpp"
+
+namespace linear16 {
+namespace {
+
+using rows::kBf16;
+using rows::kF16;
+
+constexpr int kStep = 32;      // k of an MFMA
+constexpr int kStageK = 64;    // k of a stage: 8 chunks of 16 bytes per row
+constexpr int kSteps = kStageK / kStep;
+
+// Slot of chunk c of k row k of a k-major tile of ROWS rows: c ^ kswz(k). Half a wavefront reads
+// 32 bytes of k rows 0-3 and 8-11 (from a multiple of 4) at once: 8 distinct 32-byte blocks.
+template <int ROWS>
+__device__ __forceinline__ int kswz(int k) {
+    static_assert(ROWS >= 64, "at least half the banks");
+    return ROWS == 64 ? 2 * (((k >> 1) & 1) | ((k >> 2) & 2)) : 2 * ((k & 3) | ((k >> 1) & 4));
+}
+
+// A workgroup barrier that waits for all but this wavefront's last N loads and for its LDS
+// accesses (see gemm_tiled.hip: no memory fence, loads of later stages stay in flight).
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (0 << 8) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The loads of one operand's part of a stage: ROWS rows (of the tile) by 64 k, in 16-byte
+// chunks. Load l of wavefront w fills slots 64 (w + WAVES l) ... + 63.
+template <bool KM, int ROWS, int WAVES>
+struct Loads {
+    static constexpr int N = ROWS * 8 / (kWave * WAVES);
+    static_assert(N * kWave * WAVES == ROWS * 8, "whole loads");
+    const char *p[N];   // this lane's chunk of each load, in the stage to be loaded next
+    int k[N];           // its first k, relative to the stage
+    int64_t step;       // bytes from one stage to the next
+
+    __device__ __forceinline__ void init(const Operand &o, int64_t r0, int64_t last, int64_t k0, int wave, int lane) {
+        const char *base = static_cast<const char *>(o.p);
+        step = KM ? kStageK * 2 * o.ld : kStageK * 2;
+#pragma unroll
+        for (int l = 0; l < N; ++l) {
+            const int slot = kWave * (wave + WAVES * l) + lane;
+            if constexpr (KM) {
+                constexpr int per = ROWS / 8;   // chunks of a k row
+                const int kr = slot / per, c = (slot % per) ^ kswz<ROWS>(kr);
+                k[l] = kr;
+                p[l] = base + 2 * ((k0 + kr) * o.ld + min(r0 + 8 * c, last - 7));
+            } else {
+                const int row = slot / 8, c = (slot % 8) ^ swz(row);
+                k[l] = 8 * c;
+                p[l] = base + 2 * (min(r0 + row, last) * o.ld + k0 + 8 * c);
+            }
+        }
+    }
+    // Load l of the stage into buf (the operand's slots); k_left: k from this stage's first on.
+    template <bool TAIL>
+    __device__ __forceinline__ void issue(int l, uint4 *buf, int k_left, int wave, int lane) {
+        uint4 *dst = buf + kWave * (wave + WAVES * l);
+        if (!TAIL || k_left >= kStageK || k[l] < k_left)
+            __builtin_amdgcn_global_load_lds((global_void *)p[l], (lds_void *)dst, 16, 0, 0);
+        else
+            dst[lane] = make_uint4(0, 0, 0, 0);
+        p[l] += step;
+    }
+};
+
+// Fragment reads of one operand: 16 rows (tile i of this wavefront), MFMA step kk of a stage.
+template <bool KM, int ROWS, int TILES>
+struct Fragments {
+    int at[KM ? TILES : 1];   // in bytes (k-major) or 16-byte slots (row-major)
+    int group, fswz;
+
+    __device__ __forceinline__ void init(int first, int lane) {
+        group = lane >> 4;
+        const int i16 = lane & 15;
+        if constexpr (KM) {
+            const int kr = 8 * group + (i16 >> 2);
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) {
+                const int c = (first + 16 * i) / 8 + ((i16 & 3) >> 1);
+                at[i] = (kr * (ROWS / 8) + (c ^ kswz<ROWS>(kr))) * 16 + (i16 & 1) * 8;
+            }
+            fswz = 0;
+        } else {
+            at[0] = (first + i16) * 8;
+            fswz = swz(i16);
+        }
+    }
+    __device__ __forceinline__ v4i read(const uint4 *buf, int i, int kk) const {
+        if constexpr (KM) {
+            // (k + 4 and k + 32 have the same swizzle as k)
+            const char *p = reinterpret_cast<const char *>(buf) + at[i] + kk * kStep * ROWS * 2;
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p);
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * ROWS * 2));
+            return __builtin_bit_cast(v4i, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            return __builtin_bit_cast(v4i, buf[at[0] + i * 16 * 8 + ((kk * 4 + group) ^ fswz)]);
+        }
+    }
+};
+
+struct Tiles {
+    Operand a, b;
+    int64_t M, N, K;
+    int tiles_m, tiles_n;
+    int whole;              // tiles of one workgroup each, the first ones in the tile order
+    int splits;             // workgroups of each other tile
+    float *partial;         // their sums: [tile - whole][split][BM][BN]
+    Epilogue ep;
+};
+
+// The first row and column of tile t: in groups of 8 tile rows.
+__device__ __forceinline__ void tile_at(const Tiles &g, int t, int BM, int BN, int64_t &m0, int64_t &n0) {
+    constexpr int kGroup = 8;
+    const int per_group = kGroup * g.tiles_n, first_m = t / per_group * kGroup;
+    const int gsize = min(g.tiles_m - first_m, kGroup);
+    m0 = (int64_t)(first_m + t % per_group % gsize) * BM;
+    n0 = (int64_t)(t % per_group / gsize) * BN;
+}
+
+// Outputs (m, n ... n + 7) from their sums.
+template <bool F16, bool STREAM>
+__device__ __forceinline__ void finish(float (&v)[8], const float (&bias)[8], const Epilogue &ep, int64_t N, int64_t m,
+                                       int64_t n) {
+    constexpr auto D = F16 ? kF16 : kBf16;
+    auto store = [](void *to, uint4 u) {
+        if constexpr (STREAM) w8a8::store16_nt(to, u);
+        else *static_cast<uint4 *>(to) = u;
+    };
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += bias[e];
+    if (ep.pre) store(static_cast<uint16_t *>(ep.pre) + m * N + n, rows::narrow_chunk<D>(v));
+    act::activate(ep.act, v);
+    if (ep.residual) {
+        float r[8];
+        rows::widen_chunk<D>(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(ep.residual) + m * ep.ldr + n), r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += r[e];
+    }
+    store(static_cast<uint16_t *>(ep.out) + m * N + n, rows::narrow_chunk<D>(v));
+}
+
+// One K stage: multiply the stage in rd and read the first fragments of the next one from nx.
+// The barrier before the last MFMA step says that every wavefront has read all of rd (the last
+// step's fragments are in registers by then) and that the next stage has landed; from there on the stage NB
+// ahead is loaded into rd, an even share per MFMA step, the last shares beside the next stage's first
+// steps: a burst of loads would hold the wavefront's MFMAs. So the first steps here finish the
+// loads into `before`, the buffer of the stage before. Fragment reads and loads go out between the
+// MFMAs; scheduling barriers pin the order.
+struct Ahead {
+    bool full;           // all stages that the counted wait assumes are in flight
+    bool rest, begin;    // whether there are loads into the buffer before, into this one
+    int rest_k, begin_k; // k left from their stage's first on
+};
+template <bool F16, int TM, int TN, int BM, int NB, bool TAIL, typename LA, typename LB, typename FA, typename FB>
+__device__ __forceinline__ void stage(uint4 *__restrict__ rd, const uint4 *__restrict__ nx, uint4 *__restrict__ before, LA &la,
+                                      LB &lb, const FA &fa, const FB &fb, const Ahead &h, int wave, int lane,
+                                      v4f (&acc)[TM][TN], v4i (&xa)[2][TM], v4i (&wb)[2][TN]) {
+    constexpr int NLD = LA::N + LB::N, NMF = TM * TN, BSLOT = BM * 8;
+    constexpr int LPK = NB == 2 ? NLD : (NLD + kSteps - 1) / kSteps;   // loads per step
+    constexpr int GAP = NMF / LPK;                                     // MFMAs per load
+    static_assert(GAP >= 1 && kSteps == 2, "a load follows an MFMA; the fragments' two sets alternate");
+    constexpr int RPS = (TM + TN + NMF - 1) / NMF;                     // fragment reads per MFMA
+#pragma unroll
+    for (int kk = 0; kk < kSteps; ++kk) {
+        const int f = kk;
+        const bool last = kk == kSteps - 1;
+        if (last) {
+            if (h.full) stage_barrier<(NB - 2) * NLD>();
+            else stage_barrier<0>();
+        }
+        const uint4 *src = last ? nx : rd;
+        const int first = last ? 0 : (kk + 1) * LPK;   // of the step's loads
+#pragma unroll
+        for (int q = 0; q < NMF; ++q) {
+            const int i = q / TN, j = q % TN;
+            acc[i][j] = mfma<F16>(wb[f][j], xa[f][i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = 0; r < RPS; ++r) {
+                const int x = q * RPS + r;   // a fragment of the next step, in the order of their first use
+                if (x == 0) xa[f ^ 1][0] = fa.read(src, 0, (kk + 1) % kSteps);
+                else if (x <= TN) wb[f ^ 1][x - 1] = fb.read(src + BSLOT, x - 1, (kk + 1) % kSteps);
+                else if (x < TM + TN) xa[f ^ 1][x - TN] = fa.read(src, x - TN, (kk + 1) % kSteps);
+            }
+            if (q % GAP == GAP - 1 && q / GAP < LPK) {
+                const int l = first + q / GAP;
+                if (l < NLD && (last ? h.begin : h.rest)) {
+                    uint4 *to = last ? rd : before;
+                    const int left = last ? h.begin_k : h.rest_k;
+                    if (l < LA::N) la.template issue<TAIL>(l, to, left, wave, lane);
+                    else lb.template issue<TAIL>(l - LA::N, to + BSLOT, left, wave, lane);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+}
+
+// The largest of n, n / 2, n / 4 ... up to most.
+constexpr int rows_staged(int n, int most) { return n <= most ? n : rows_staged(n / 2, most); }
+
+template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC, bool KA, bool KB, bool TAIL>
+__global__ __launch_bounds__(GM *GN *kWave, GM *GN *OCC / 4) void tiled_kernel(const Tiles g) {
+    constexpr int WAVES = GM * GN, WM = BM / GM, WN = BN / GN, TM = WM / 16, TN = WN / 16;
+    constexpr int STAGE = (BM + BN) * 8, BSLOT = BM * 8;   // 16-byte slots
+    __shared__ uint4 lds[NB * STAGE];
+    w8a8::lds_poison(lds);
+    w8a8::lds_poison_done();
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / GN, wn = wave % GN;
+
+    // the whole tiles, then the parts of the others, each spread over the XCDs for themselves
+    const int block = blockIdx.x, tiles = g.tiles_m * g.tiles_n;
+    const bool split = block >= g.whole;
+    int t, unit = 0, s0 = 0, s1 = (int)((g.K + kStageK - 1) / kStageK);
+    if (split) {
+        unit = w8a8::xcd_contiguous(block - g.whole, (tiles - g.whole) * g.splits);
+        t = g.whole + unit / g.splits;
+        const int part = unit % g.splits, stages = s1;
+        s0 = (int)((int64_t)stages * part / g.splits);
+        s1 = (int)((int64_t)stages * (part + 1) / g.splits);
+    } else {
+        t = w8a8::xcd_contiguous(block, g.whole);
+    }
+    int64_t m0, n0;
+    tile_at(g, t, BM, BN, m0, n0);
+
+    Loads<KA, BM, WAVES> la;
+    Loads<KB, BN, WAVES> lb;
+    la.init(g.a, m0, g.M - 1, (int64_t)s0 * kStageK, wave, lane);
+    lb.init(g.b, n0, g.N - 1, (int64_t)s0 * kStageK, wave, lane);
+    Fragments<KA, BM, TM> fa;
+    Fragments<KB, BN, TN> fb;
+    fa.init(wm * WM, lane);
+    fb.init(wn * WN, lane);
+    auto left = [&](int s) { return (int)min(g.K - (int64_t)s * kStageK, (int64_t)kStageK); };
+
+    v4f acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = v4f{};
+    v4i xa[2][TM], wb[2][TN];
+    if (s0 < s1) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if (s0 + b >= s1) break;
+            uint4 *buf = lds + b * STAGE;
+#pragma unroll
+            for (int l = 0; l < la.N; ++l) la.template issue<TAIL>(l, buf, left(s0 + b), wave, lane);
+#pragma unroll
+            for (int l = 0; l < lb.N; ++l) lb.template issue<TAIL>(l, buf + BSLOT, left(s0 + b), wave, lane);
+        }
+        // a stage whose chunks lie past K has fewer loads than the counted waits assume: once the last
+        // stage is among those in flight, all are waited for
+        const int counted = s1 - (TAIL ? 1 : 0);
+        if (s0 + NB - 1 < counted) stage_barrier<(NB - 1) * (la.N + lb.N)>();
+        else stage_barrier<0>();
+#pragma unroll
+        for (int i = 0; i < TM; ++i) xa[0][i] = fa.read(lds, i, 0);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) wb[0][j] = fb.read(lds + BSLOT, j, 0);
+        int at = 0, before = NB - 1;
+        for (int s = s0; s < s1; ++s) {
+            const int next = at == NB - 1 ? 0 : at + 1;
+            const Ahead h{s + NB - 1 < counted, s > s0 && s + NB - 1 < s1, s + NB < s1, left(s + NB - 1), left(s + NB)};
+            stage<F16, TM, TN, BM, NB, TAIL>(lds + at * STAGE, lds + next * STAGE, lds + before * STAGE, la, lb, fa, fb, h, wave,
+                                             lane, acc, xa, wb);
+            before = at;
+            at = next;
+        }
+    }
+    __syncthreads();
+
+    // tile (i, j), element r of a lane: row 16 i + lane % 16 of the wavefront's part, column
+    // 16 j + 4 (lane / 16) + r
+    constexpr int kShare = NB * STAGE / WAVES;                       // 16-byte slots
+    constexpr int kPass = rows_staged(WM, kShare * 16 / (WN * 4));   // rows staged at a time
+    static_assert(kPass >= 16, "passes of whole tiles");
+    constexpr int CH = WN / 4, PM = CH - 1;
+    static_assert((CH & PM) == 0, "the row-chunk permutation needs a power of two");
+    float4 *st = reinterpret_cast<float4 *>(lds) + wave * kShare;
+    const int group = lane >> 4, row16 = lane & 15;
+    const int lane_n = lane % (WN / 8) * 8;
+    const int64_t n = n0 + wn * WN + lane_n;
+    float bias[8];
+    rows::load_vector<kBf16>(g.ep.bias, (int)n, (int)g.N, 0.0f, bias);
+#pragma unroll
+    for (int p = 0; p < WM / kPass; ++p) {
+        if (p) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPass / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int ml = i * 16 + row16;
+                st[ml * CH + ((j * 4 + group) ^ (ml & PM))] = __builtin_bit_cast(float4, acc[p * (kPass / 16) + i][j]);
+            }
+        __syncthreads();
+#pragma nounroll
+        for (int it = 0; it < kPass * (WN / 8) / kWave; ++it) {
+            const int ml = it * (kWave / (WN / 8)) + lane / (WN / 8), row = wm * WM + p * kPass + ml;
+            if (m0 + row >= g.M || n >= g.N) continue;
+            float v[8];
+            *reinterpret_cast<float4 *>(v) = st[ml * CH + ((lane_n / 4) ^ (ml & PM))];
+            *reinterpret_cast<float4 *>(v + 4) = st[ml * CH + ((lane_n / 4 + 1) ^ (ml & PM))];
+            if (split) {
+                float4 *to = reinterpret_cast<float4 *>(g.partial + ((int64_t)unit * BM + row) * BN + wn * WN + lane_n);
+                to[0] = *reinterpret_cast<float4 *>(v);
+                to[1] = *reinterpret_cast<float4 *>(v + 4);
+            } else {
+                finish<F16, true>(v, bias, g.ep, g.N, m0 + row, n);
+            }
+        }
+    }
+}
+
+// The sums of the parts of the split tiles, in order, and the epilogue: 8 outputs per thread.
+template <bool F16, int BM, int BN>
+__global__ __launch_bounds__(256) void join_kernel(const Tiles g) {
+    constexpr int kBlocks = BM * BN / 8 / 256;   // workgroups of a tile
+    const int tile = blockIdx.x / kBlocks, chunk = blockIdx.x % kBlocks * 256 + threadIdx.x;
+    const int row = chunk / (BN / 8), col = chunk % (BN / 8) * 8;
+    int64_t m0, n0;
+    tile_at(g, g.whole + tile, BM, BN, m0, n0);
+    const int64_t m = m0 + row, n = n0 + col;
+    if (m >= g.M || n >= g.N) return;
+    float v[8] = {}, bias[8];
+    rows::load_vector<kBf16>(g.ep.bias, (int)n, (int)g.N, 0.0f, bias);
+    const float *from = g.partial + ((int64_t)tile * g.splits * BM + row) * BN + col;
+    for (int s = 0; s < g.splits; ++s, from += BM * BN) {
+        const float4 lo = reinterpret_cast<const float4 *>(from)[0], hi = reinterpret_cast<const float4 *>(from)[1];
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+    }
+    finish<F16, false>(v, bias, g.ep, g.N, m, n);
+}
+
+template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC, bool KA, bool KB>
+hipError_t launch(Tiles g, hipStream_t stream) {
+    g.tiles_m = (int)((g.M + BM - 1) / BM);
+    g.tiles_n = (int)((g.N + BN - 1) / BN);
+    const int tiles = g.tiles_m * g.tiles_n;
+    const dim3 grid((unsigned)(g.whole + (tiles - g.whole) * g.splits)), block(GM * GN * kWave);
+    if (g.K % kStageK == 0) tiled_kernel<F16, BM, BN, GM, GN, NB, OCC, KA, KB, false><<<grid, block, 0, stream>>>(g);
+    else tiled_kernel<F16, BM, BN, GM, GN, NB, OCC, KA, KB, true><<<grid, block, 0, stream>>>(g);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || g.whole == tiles) return e;
+    join_kernel<F16, BM, BN><<<dim3((unsigned)((tiles - g.whole) * (BM * BN / 8 / 256))), 256, 0, stream>>>(g);
+    return hipGetLastError();
+}
+
+template <bool F16, bool KA, bool KB>
+hipError_t launch_form(const Tiles &g, int form, hipStream_t stream) {
+    switch (form) {
+        case k256x256: return launch<F16, 256, 256, 4, 2, 2, 1, KA, KB>(g, stream);
+        case k256x128: return launch<F16, 256, 128, 4, 2, 3, 1, KA, KB>(g, stream);
+        case k128x128: return launch<F16, 128, 128, 2, 4, 2, 2, KA, KB>(g, stream);
+        case k128x128deep: return launch<F16, 128, 128, 4, 2, 4, 1, KA, KB>(g, stream);
+        default: return launch<F16, 64, 64, 2, 2, 3, 3, KA, KB>(g, stream);
+    }
+}
+
+template <bool F16>
+hipError_t launch_type(const Tiles &g, int form, hipStream_t stream) {
+    if (g.a.k_major) return launch_form<F16, true, true>(g, form, stream);
+    return g.b.k_major ? launch_form<F16, false, true>(g, form, stream) : launch_form<F16, false, false>(g, form, stream);
+}
+
+}  // namespace
+
+hipError_t launch_tiled(const Operand &a, const Operand &b, int64_t M, int64_t N, int64_t K, bool f16, const Plan &plan,
+                        float *partial, const Epilogue &ep, hipStream_t stream) {
+    const Tiles g{a, b, M, N, K, 0, 0, plan.whole, plan.splits, partial, ep};
+    return f16 ? launch_type<true>(g, plan.form, stream) : launch_type<false>(g, plan.form, stream);
+}
+
+}  // namespace linear16
