@@ -771,10 +771,10 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 def _activation(activation) -> int:
-    try:
-        return ACTIVATIONS[activation]
-    except (KeyError, TypeError):
-        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}") from None
+    code = ACTIVATIONS.get(activation) if isinstance(activation, str) else None
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
+    return code
 
 
 def _vector(t, name, n):
@@ -787,27 +787,32 @@ def _vector(t, name, n):
     return t.data_ptr()
 
 
-def _like_rows(t, name, dtype, rows, width):
-    """(address, row stride) of rows [rows, width] of dtype that may lie apart, (None, 0) for none."""
+def _like_rows(t, name, dtype, shape):
+    """(address, row stride) of rows of dtype and shape that may lie apart, (None, 0) for none."""
     if t is None:
         return None, 0
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr(), shape[1]
     _, ld, m, n = _float_rows(t, name)
-    if t.dtype is not dtype or m != rows or n != width:
-        raise ValueError(f"{name} must be {dtype} {(rows, width)}, got {t.dtype} {(m, n)}")
-    if ld < width:
+    if t.dtype is not dtype or (m, n) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {(m, n)}")
+    if ld < n:
         raise ValueError(f"{name} must have rows of their own, not expanded ones")
     return t.data_ptr(), ld
 
 
-def _on_device(t, *others):
-    """Refuses tensors of several devices, and a device that is not the current one: the launch would go to
-    the current one."""
+def _current(t, stream, *others):
+    """The handle of `stream`, or of the current stream of t's device, on which every tensor has to be: a launch
+    goes to the current device."""
     d = t.get_device()
-    if d != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{d}, the current device is cuda:{torch.cuda.current_device()}")
+    if d != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on cuda:{d}, the current device is cuda:{torch._C._cuda_getDevice()}")
     for o in others:
-        if isinstance(o, torch.Tensor) and o.get_device() != d:
+        if o is not None and o.get_device() != d:
             raise ValueError("all tensors must be on one device")
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(d)
 
 
 def w8a8_gemm_act(xq, x_scale, wq, w_scale, bias=None, activation="none", residual=None, out=None,
@@ -824,12 +829,12 @@ def w8a8_gemm_act(xq, x_scale, wq, w_scale, bias=None, activation="none", residu
     N, K2 = wq.shape
     if K2 != K or x_scale.shape[0] != M or w_scale.shape[0] != N:
         raise ValueError("operand shapes")
-    _on_device(xq, x_scale, wq, w_scale, bias, residual, out)
-    bias = _vector(bias, "bias", N)
-    r, ldr = _like_rows(residual, "residual", torch.bfloat16, M, N)
+    b = _vector(bias, "bias", N)
+    r, ldr = _like_rows(residual, "residual", torch.bfloat16, (M, N))
+    s = _current(xq, stream, x_scale, wq, w_scale, bias, residual, out)
     out = _result(out, "out", (M, N), torch.bfloat16, xq, stream)
     _done(load().w8a8_gemm_act(xq.data_ptr(), x_scale.data_ptr(), M, wq.data_ptr(), w_scale.data_ptr(), N, K,
-                               bias, a, r, ldr, out.data_ptr(), _stream_of(xq, stream)), "w8a8_gemm_act")
+                               b, a, r, ldr, out.data_ptr(), s), "w8a8_gemm_act")
     return out
 
 
@@ -854,23 +859,23 @@ def w16a16_linear(x, w, bias=None, activation="none", residual=None, pre=None, o
     None)."""
     a = _activation(activation)
     code, ld, M, N, K = _linear16_operands(x, w)
-    _on_device(x, w, bias, residual, pre, out, workspace)
-    bias = _vector(bias, "bias", N)
-    r, ldr = _like_rows(residual, "residual", x.dtype, M, N)
-    lib = load()
+    b = _vector(bias, "bias", N)
+    r, ldr = _like_rows(residual, "residual", x.dtype, (M, N))
+    if pre is False or pre is True:
+        pre = _new((M, N), x.dtype, x, stream) if pre else None
+    s = _current(x, stream, w, bias, residual, pre, out, workspace)
+    p = None
+    if pre is not None:
+        p = _result(pre, "pre", (M, N), x.dtype, x, stream).data_ptr()
     out = _result(out, "out", (M, N), x.dtype, x, stream)
-    if pre is False:
-        pre = None
-    elif pre is not None:
-        pre = _result(None if pre is True else pre, "pre", (M, N), x.dtype, x, stream)
-    work, address, size = None, 0, 0
+    lib = load()
+    work, address, size = None, None, 0
     need = lib.w16a16_linear_workspace(M, N, K)
     if need or workspace is not None:
         work = _scratch(workspace, need, x, stream)
         address, size = work.data_ptr(), work.shape[0]
-    _done(lib.w16a16_linear(x.data_ptr(), ld, M, w.data_ptr(), N, K, code, bias, a, r, ldr,
-                            None if pre is None else pre.data_ptr(), out.data_ptr(), address, size,
-                            _stream_of(x, stream)), "w16a16_linear")
+    _done(lib.w16a16_linear(x.data_ptr(), ld, M, w.data_ptr(), N, K, code, b, a, r, ldr, p, out.data_ptr(),
+                            address, size, s), "w16a16_linear")
     return out if pre is None else (out, pre)
 
 
@@ -898,28 +903,33 @@ def w16a16_linear_backward(d_out, x, w, pre=None, activation="none", d_x=True, d
     the operand of the products (d_out itself without an activation). The residual's gradient is d_out."""
     a = _activation(activation)
     code, ld, M, N, K = _linear16_operands(x, w)
-    _on_device(x, w, d_out, pre, d_x, d_w, d_bias, d_pre, workspace)
-    d, ldd = _like_rows(d_out, "d_out", x.dtype, M, N)
+    d, ldd = _like_rows(d_out, "d_out", x.dtype, (M, N))
     if d is None:
         raise TypeError("d_out must be a torch.Tensor")
+    p = q = None
     if a:
         if pre is None:
             raise ValueError("the gradient of an activation needs pre")
         _check(pre, "pre", x.dtype, 2)
         if pre.shape != (M, N):
             raise ValueError(f"pre must have shape {(M, N)}, got {tuple(pre.shape)}")
+        p = pre.data_ptr()
         d_pre = _result(d_pre, "d_pre", (M, N), x.dtype, x, stream)
+        q = d_pre.data_ptr()
     else:
         pre, d_pre = None, d_out
-    lib = load()
     d_x = _wanted(d_x, "d_x", (M, K), x.dtype, x, stream)
     d_w = _wanted(d_w, "d_w", (N, K), x.dtype, x, stream)
     d_bias = _wanted(d_bias, "d_bias", (N,), torch.float32, x, stream)
-    work = _scratch(workspace, lib.w16a16_linear_backward_workspace(M, N, K), x, stream)
-    _done(lib.w16a16_linear_backward(d, ldd, x.data_ptr(), ld, w.data_ptr(), _address(pre), M, N, K, code, a,
-                                     d_pre.data_ptr() if a else None, _address(d_x), _address(d_w),
-                                     _address(d_bias), work.data_ptr(), work.shape[0],
-                                     _stream_of(x, stream)), "w16a16_linear_backward")
+    s = _current(x, stream, w, d_out, pre, d_pre, d_x, d_w, d_bias, workspace)
+    lib = load()
+    work, address, size = None, None, 0
+    need = lib.w16a16_linear_backward_workspace(M, N, K)
+    if need or workspace is not None:
+        work = _scratch(workspace, need, x, stream)
+        address, size = work.data_ptr(), work.shape[0]
+    _done(lib.w16a16_linear_backward(d, ldd, x.data_ptr(), ld, w.data_ptr(), p, M, N, K, code, a, q, _address(d_x),
+                                     _address(d_w), _address(d_bias), address, size, s), "w16a16_linear_backward")
     return d_x, d_w, d_bias, d_pre
 
 
@@ -928,29 +938,32 @@ def w16a16_linear_backward_workspace(M, N, K) -> int:
     return load().w16a16_linear_backward_workspace(M, N, K)
 
 
-def _gate(gate, dtype, T, H):
+def _gate(gate, dtype, shape):
     """(address, row stride) of a gate: none, one float32 value per channel (stride 0), or rows."""
     if gate is None:
         return None, 0
     if isinstance(gate, torch.Tensor) and gate.dim() == 1:
-        return _vector(gate, "gate", H), 0
-    return _like_rows(gate, "gate", dtype, T, H)
+        return _vector(gate, "gate", shape[1]), 0
+    return _like_rows(gate, "gate", dtype, shape)
 
 
-def _norm_operands(residual, weight, y, post_norm, post_weight, gate, new_residual, outputs, stream):
-    """The library's leading arguments, (dtype code, T, H) and the new residual of a block norm."""
+def _norm_operands(residual, weight, y, post_norm, post_weight, gate, scale, eps, new_residual, outputs, stream):
+    """The library's arguments of a block norm up to its outputs, the new residual and the stream's handle."""
     code, ld, T, H = _float_rows(residual, "residual")
-    _on_device(residual, weight, y, post_weight, gate, new_residual, *outputs)
-    y_at, ldy = _like_rows(y, "y", residual.dtype, T, H)
-    if y is None and (gate is not None or post_norm or post_weight is not None):
-        raise ValueError("gate and post norm need y")
-    gate_at, ldg = _gate(gate, residual.dtype, T, H)
-    if y is not None:
-        new_residual = _result(new_residual, "new_residual", (T, H), residual.dtype, residual, stream)
-    else:
-        new_residual = residual
-    return (residual.data_ptr(), ld, y_at, ldy, 1 if post_norm or post_weight is not None else 0,
-            _vector(post_weight, "post_weight", H), gate_at, ldg), _vector(weight, "weight", H), code, T, H, new_residual
+    dtype = residual.dtype
+    w = _vector(weight, "weight", H)
+    if y is None:
+        if gate is not None or post_norm or post_weight is not None:
+            raise ValueError("gate and post norm need y")
+        s = _current(residual, stream, weight, *outputs)
+        return (residual.data_ptr(), ld, None, 0, 0, None, None, 0, scale, w, eps, T, H, code, None), residual, s
+    y_at, ldy = _like_rows(y, "y", dtype, (T, H))
+    gate_at, ldg = _gate(gate, dtype, (T, H))
+    p = _vector(post_weight, "post_weight", H)
+    s = _current(residual, stream, weight, y, post_weight, gate, new_residual, *outputs)
+    new_residual = _result(new_residual, "new_residual", (T, H), dtype, residual, stream)
+    return (residual.data_ptr(), ld, y_at, ldy, 1 if post_norm or post_weight is not None else 0, p, gate_at, ldg, scale, w,
+            eps, T, H, code, new_residual.data_ptr()), new_residual, s
 
 
 def block_norm(residual, weight=None, y=None, post_norm=False, post_weight=None, gate=None, scale=1.0, eps=1e-6,
@@ -961,11 +974,10 @@ def block_norm(residual, weight=None, y=None, post_norm=False, post_weight=None,
     residual, y: rows [T,H] of bfloat16, float16 or float32 (they may lie apart); gate: None, float32 [H], or
     rows; weight, post_weight: float32 [H] or None (ones). Without y it is the plain norm, and new_residual is
     residual. new_residual may be the (contiguous) residual or y."""
-    args, weight, code, T, H, new_residual = _norm_operands(residual, weight, y, post_norm, post_weight, gate,
-                                                            new_residual, (out,), stream)
-    out = _result(out, "out", (T, H), residual.dtype, residual, stream)
-    _done(load().block_norm(*args, scale, weight, eps, T, H, code, new_residual.data_ptr(), out.data_ptr(),
-                            _stream_of(residual, stream)), "block_norm")
+    args, new_residual, s = _norm_operands(residual, weight, y, post_norm, post_weight, gate, scale, eps, new_residual,
+                                           (out,), stream)
+    out = _result(out, "out", residual.shape, residual.dtype, residual, stream)
+    _done(load().block_norm(*args, out.data_ptr(), s), "block_norm")
     return new_residual, out
 
 
@@ -973,12 +985,11 @@ def block_norm_w8a8(residual, weight=None, y=None, post_norm=False, post_weight=
                     eps=1e-6, new_residual=None, xq=None, x_scale=None, stream=None):
     """block_norm with its output quantized to int8 rows, as w8a8_quantize_rows would the unrounded output:
     (new_residual, xq int8 [T,H], x_scale float32 [T])."""
-    args, weight, code, T, H, new_residual = _norm_operands(residual, weight, y, post_norm, post_weight, gate,
-                                                            new_residual, (xq, x_scale), stream)
-    xq = _result(xq, "xq", (T, H), torch.int8, residual, stream)
-    x_scale = _result(x_scale, "x_scale", (T,), torch.float32, residual, stream)
-    _done(load().block_norm_w8a8(*args, scale, weight, eps, T, H, code, new_residual.data_ptr(), xq.data_ptr(),
-                                 x_scale.data_ptr(), _stream_of(residual, stream)), "block_norm_w8a8")
+    args, new_residual, s = _norm_operands(residual, weight, y, post_norm, post_weight, gate, scale, eps, new_residual,
+                                           (xq, x_scale), stream)
+    xq = _result(xq, "xq", residual.shape, torch.int8, residual, stream)
+    x_scale = _result(x_scale, "x_scale", residual.shape[:1], torch.float32, residual, stream)
+    _done(load().block_norm_w8a8(*args, xq.data_ptr(), x_scale.data_ptr(), s), "block_norm_w8a8")
     return new_residual, xq, x_scale
 
 
@@ -986,13 +997,12 @@ def block_norm_mxfp4(residual, weight=None, y=None, post_norm=False, post_weight
                      eps=1e-6, new_residual=None, codes=None, scales=None, stream=None):
     """block_norm with its output quantized to MXFP4 rows, as mxfp4_quantize_rows would the unrounded output:
     (new_residual, codes uint8 [T,H/2], scales uint8 [ceil(H/256),T,8])."""
-    args, weight, code, T, H, new_residual = _norm_operands(residual, weight, y, post_norm, post_weight, gate,
-                                                            new_residual, (codes, scales), stream)
+    args, new_residual, s = _norm_operands(residual, weight, y, post_norm, post_weight, gate, scale, eps, new_residual,
+                                           (codes, scales), stream)
+    T, H = residual.shape
     codes = _result(codes, "codes", (T, H // 2), torch.uint8, residual, stream)
     scales = _result(scales, "scales", ((H + 255) // 256, T, 8), torch.uint8, residual, stream)
-    _done(load().block_norm_mxfp4(*args, scale, weight, eps, T, H, code, new_residual.data_ptr(),
-                                  codes.data_ptr(), scales.data_ptr(), _stream_of(residual, stream)),
-          "block_norm_mxfp4")
+    _done(load().block_norm_mxfp4(*args, codes.data_ptr(), scales.data_ptr(), s), "block_norm_mxfp4")
     return new_residual, codes, scales
 
 
@@ -1003,33 +1013,32 @@ def block_norm_backward(d_out, new_residual, weight=None, d_residual=None, y=Non
     d_y [T,H], d_post_weight float32 [H], d_gate [T,H] or float32 [H]), None for those without an input (the
     weights' gradients are given for absent weights, too, as those of ones; d_post_weight with a post norm)."""
     code, ldr, T, H = _float_rows(new_residual, "new_residual")
-    dtype = new_residual.dtype
-    _on_device(new_residual, d_out, weight, d_residual, y, post_weight, gate, workspace)
-    o, ldo = _like_rows(d_out, "d_out", dtype, T, H)
+    dtype, shape = new_residual.dtype, (T, H)
+    o, ldo = _like_rows(d_out, "d_out", dtype, shape)
     if o is None:
         raise TypeError("d_out must be a torch.Tensor")
-    n, ldn = _like_rows(d_residual, "d_residual", dtype, T, H)
-    y_at, ldy = _like_rows(y, "y", dtype, T, H)
+    n, ldn = _like_rows(d_residual, "d_residual", dtype, shape)
+    y_at, ldy = _like_rows(y, "y", dtype, shape)
     post = post_norm or post_weight is not None
     if y is None and (gate is not None or post):
         raise ValueError("gate and post norm need y")
-    gate_at, ldg = _gate(gate, dtype, T, H)
-    weight, post_weight = _vector(weight, "weight", H), _vector(post_weight, "post_weight", H)
+    gate_at, ldg = _gate(gate, dtype, shape)
+    w, p = _vector(weight, "weight", H), _vector(post_weight, "post_weight", H)
+    s = _current(new_residual, stream, d_out, weight, d_residual, y, post_weight, gate, workspace)
     lib = load()
-    d_r = _new((T, H), dtype, new_residual, stream)
+    d_r = _new(shape, dtype, new_residual, stream)
     d_weight = _new((H,), torch.float32, new_residual, stream)
     d_y = d_post_weight = d_gate = None
     if y is not None:
-        d_y = _new((T, H), dtype, new_residual, stream)
+        d_y = _new(shape, dtype, new_residual, stream)
     if post:
         d_post_weight = _new((H,), torch.float32, new_residual, stream)
     if gate is not None:
-        d_gate = _new((T, H) if ldg else (H,), dtype if ldg else torch.float32, new_residual, stream)
+        d_gate = _new(shape if ldg else (H,), dtype if ldg else torch.float32, new_residual, stream)
     work = _scratch(workspace, lib.block_norm_backward_workspace(T, H), new_residual, stream)
-    _done(lib.block_norm_backward(o, ldo, n, ldn, new_residual.data_ptr(), ldr, y_at, ldy, 1 if post else 0,
-                                  post_weight, gate_at, ldg, scale, weight, eps, T, H, code, d_r.data_ptr(),
-                                  _address(d_y), _address(d_gate), d_weight.data_ptr(), _address(d_post_weight),
-                                  work.data_ptr(), work.shape[0], _stream_of(new_residual, stream)),
+    _done(lib.block_norm_backward(o, ldo, n, ldn, new_residual.data_ptr(), ldr, y_at, ldy, 1 if post else 0, p, gate_at,
+                                  ldg, scale, w, eps, T, H, code, d_r.data_ptr(), _address(d_y), _address(d_gate),
+                                  d_weight.data_ptr(), _address(d_post_weight), work.data_ptr(), work.shape[0], s),
           "block_norm_backward")
     return d_r, d_weight, d_y, d_post_weight, d_gate
 

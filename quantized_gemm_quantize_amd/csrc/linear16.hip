@@ -69,11 +69,12 @@ Estimate estimate(int64_t M, int64_t N, int64_t K) {
         offer(whole + (rest ? round_time(f, rest, stages) : 0.0), 1);
         if (!rest) continue;
         const int64_t most = std::min(f.slots / rest, stages / 2);
-        for (int64_t s = 2; s <= most; ++s) {
-            // the largest number of workgroups for every number of stages in a part
-            if (s < most && ceil_div(stages, s) == ceil_div(stages, s + 1)) continue;
+        for (int64_t s : {2, 3, 4, 6, 8, 12, 16, 24, 32, 64}) {
+            s = std::min(s, most);
+            if (s < 2) break;
             const double bytes = 2.0 * rest * s * f.bm * f.bn * 4;
             offer(whole + round_time(f, rest * s, ceil_div(stages, s)) + 3.0 + bytes / 4.5e6, s);
+            if (s == most) break;
         }
     }
     return best;
@@ -82,9 +83,12 @@ Estimate estimate(int64_t M, int64_t N, int64_t K) {
 // The kernel of few rows: up to 16 rows always (1 x 4096 x 4096 5.8 us against 13 in tiles), up to 64
 // where it is estimated to be quicker: 3 us and both operands of a workgroup at 65 GB/s a round
 // (64 rows: 4096 x 4096 11.7 us against 13.0, 8192 x 2048 14.9 / 12.2, 4096 x 11008 32.7 / 23.7).
-bool few_rows(int64_t M, int64_t N, int64_t K, const Estimate &tiled) {
-    if (M > kMaxRows) return false;
+// Otherwise, the plan in tiles.
+bool few_rows(int64_t M, int64_t N, int64_t K, Plan &plan) {
     if (M <= 16) return true;
+    const Estimate tiled = estimate(M, N, K);
+    plan = tiled.plan;
+    if (M > kMaxRows) return false;
     const int64_t rounds = ceil_div(ceil_div(N, 16), 256);
     return rounds * (3.0 + 2.0 * K * 16 * (ceil_div(M, 16) + 1) / 65e3) < tiled.us;
 }
@@ -96,10 +100,10 @@ hipError_t product(const Operand &a, const Operand &b, int64_t M, int64_t N, int
 
 // ---------------------------------------------------------------- d_pre and d_bias
 
-// A thread takes 8 columns of every 32nd row of its workgroup's rows; a workgroup 64 columns
-// (8 threads) and 32 rows at a time, every G-th. Column sums are kept in registers, joined in LDS and left
-// as one partial per workgroup row.
-constexpr int kColumns = 64, kRowsAtOnce = 32;
+// A workgroup takes 64 columns, ROWS rows at a time (8 threads a row, 8 columns each), every
+// G-th ROWS rows. Column sums are kept in registers, joined in LDS and left as one partial sum per
+// workgroup, or, with one workgroup for all rows, as the result.
+constexpr int kColumns = 64;
 
 template <int A, Dtype D>
 __device__ __forceinline__ void slopes(float (&d)[8], uint4 pre) {
@@ -109,18 +113,18 @@ __device__ __forceinline__ void slopes(float (&d)[8], uint4 pre) {
     for (int e = 0; e < 8; ++e) d[e] *= act::slope<A>(p[e]);
 }
 
-template <Dtype D>
-__global__ __launch_bounds__(256) void slope_kernel(const uint16_t *__restrict__ d_out, int64_t ldd,
+template <Dtype D, int ROWS>
+__global__ __launch_bounds__(8 * ROWS) void slope_kernel(const uint16_t *__restrict__ d_out, int64_t ldd,
                                                     const uint16_t *__restrict__ pre, int64_t M, int64_t N, int a,
                                                     uint16_t *__restrict__ d_pre, float *__restrict__ partial) {
-    __shared__ float red[kRowsAtOnce][kColumns];
+    __shared__ float red[ROWS][kColumns];
     w8a8::lds_poison(red);
     w8a8::lds_poison_done();
     const int c = threadIdx.x % 8 * 8, r = threadIdx.x / 8;
     const int64_t n = (int64_t)blockIdx.x * kColumns + c;
     float sum[8] = {};
     if (n < N)
-        for (int64_t m = (int64_t)blockIdx.y * kRowsAtOnce + r; m < M; m += (int64_t)gridDim.y * kRowsAtOnce) {
+        for (int64_t m = (int64_t)blockIdx.y * ROWS + r; m < M; m += (int64_t)gridDim.y * ROWS) {
             float d[8];
             widen_chunk<D>(w8a8::load16_stream(d_out + m * ldd + n), d);
             if (a != act::kNone) {
@@ -143,7 +147,7 @@ __global__ __launch_bounds__(256) void slope_kernel(const uint16_t *__restrict__
     if (threadIdx.x >= kColumns || (int64_t)blockIdx.x * kColumns + threadIdx.x >= N) return;
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kRowsAtOnce; ++i) s += red[i][threadIdx.x];
+    for (int i = 0; i < ROWS; ++i) s += red[i][threadIdx.x];
     partial[blockIdx.y * N + (int64_t)blockIdx.x * kColumns + threadIdx.x] = s;
 }
 
@@ -164,19 +168,42 @@ __global__ __launch_bounds__(256) void sum_kernel(const float *__restrict__ part
     out[n] = ((s + red[1][c]) + red[2][c]) + red[3][c];
 }
 
-// Workgroup rows: enough to fill the chip eight times, at least one turn each.
+// Up to kOneGroup rows go to one workgroup of 1024 threads per 64 columns, which needs no partial sums
+// (257 x 1040 SMALL_US); more to workgroups of 256 threads, enough to fill the chip eight times.
+constexpr int kOneGroup = 512, kFewRows = 128, kManyRows = 32;
+
 int sum_groups(int64_t M, int64_t N) {
-    return (int)std::min(ceil_div(M, kRowsAtOnce), std::max<int64_t>(1, 2048 / ceil_div(N, kColumns)));
+    if (M <= kOneGroup) return 1;
+    return (int)std::min(ceil_div(M, kManyRows), std::max<int64_t>(1, 2048 / ceil_div(N, kColumns)));
 }
 
-int64_t sums_bytes(int64_t M, int64_t N) { return (4 * N * sum_groups(M, N) + 255) / 256 * 256; }
+int64_t sums_bytes(int64_t M, int64_t N) {
+    return M <= kOneGroup ? 0 : (4 * N * sum_groups(M, N) + 255) / 256 * 256;
+}
+
+template <Dtype D>
+hipError_t launch_slope(const void *d_out, int64_t ldd, const void *pre, int64_t M, int64_t N, int a, void *d_pre,
+                        float *d_bias, float *partial, hipStream_t stream) {
+    const int G = sum_groups(M, N);
+    const dim3 grid((unsigned)ceil_div(N, kColumns), (unsigned)G);
+    const uint16_t *d = static_cast<const uint16_t *>(d_out), *p = static_cast<const uint16_t *>(pre);
+    uint16_t *to = static_cast<uint16_t *>(d_pre);
+    if (M <= kOneGroup) {
+        slope_kernel<D, kFewRows><<<grid, 8 * kFewRows, 0, stream>>>(d, ldd, p, M, N, a, to, d_bias);
+        return hipGetLastError();
+    }
+    slope_kernel<D, kManyRows><<<grid, 8 * kManyRows, 0, stream>>>(d, ldd, p, M, N, a, to, d_bias ? partial : nullptr);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !d_bias) return e;
+    sum_kernel<<<dim3((unsigned)ceil_div(N, 64)), 256, 0, stream>>>(partial, G, N, d_bias);
+    return hipGetLastError();
+}
 
 }  // namespace
 
 int64_t forward_workspace(int64_t M, int64_t N, int64_t K) {
-    if (M == 0) return 0;
-    const Estimate e = estimate(M, N, K);
-    return few_rows(M, N, K, e) ? 0 : e.plan.workspace;
+    Plan plan;
+    return few_rows(M, N, K, plan) ? 0 : plan.workspace;
 }
 
 int64_t backward_workspace(int64_t M, int64_t N, int64_t K) {
@@ -187,30 +214,20 @@ int64_t backward_workspace(int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_forward(const void *x, int64_t ldx, int64_t M, const void *w, int64_t N, int64_t K, bool f16,
                           const Epilogue &ep, void *workspace, hipStream_t stream) {
-    const Estimate e = estimate(M, N, K);
-    if (few_rows(M, N, K, e)) return launch_rows(x, ldx, (int)M, w, (int)N, (int)K, f16, ep, stream);
-    return launch_tiled({x, ldx, false}, {w, K, false}, M, N, K, f16, e.plan, static_cast<float *>(workspace), ep, stream);
+    Plan plan;
+    if (few_rows(M, N, K, plan)) return launch_rows(x, ldx, (int)M, w, (int)N, (int)K, f16, ep, stream);
+    return launch_tiled({x, ldx, false}, {w, K, false}, M, N, K, f16, plan, static_cast<float *>(workspace), ep, stream);
 }
 
 hipError_t launch_backward(const void *d_out, int64_t ldd, const void *x, int64_t ldx, const void *w, const void *pre,
                            int64_t M, int64_t N, int64_t K, bool f16, int a, void *d_pre, void *d_x, void *d_w,
                            float *d_bias, void *workspace, hipStream_t stream) {
     hipError_t e = hipSuccess;
-    if (a != act::kNone || d_bias) {
-        const int G = sum_groups(M, N);
-        float *partial = d_bias ? static_cast<float *>(workspace) : nullptr;
-        if (G) {
-            const dim3 grid((unsigned)ceil_div(N, kColumns), (unsigned)G);
-            const uint16_t *d = static_cast<const uint16_t *>(d_out), *p = static_cast<const uint16_t *>(pre);
-            uint16_t *to = static_cast<uint16_t *>(d_pre);
-            if (f16) slope_kernel<kF16><<<grid, 256, 0, stream>>>(d, ldd, p, M, N, a, to, partial);
-            else slope_kernel<kBf16><<<grid, 256, 0, stream>>>(d, ldd, p, M, N, a, to, partial);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
-        if (d_bias) {
-            sum_kernel<<<dim3((unsigned)ceil_div(N, 64)), 256, 0, stream>>>(partial, G, N, d_bias);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
+    if (d_bias || (a != act::kNone && M)) {
+        float *partial = static_cast<float *>(workspace);
+        e = f16 ? launch_slope<kF16>(d_out, ldd, pre, M, N, a, d_pre, d_bias, partial, stream)
+                : launch_slope<kBf16>(d_out, ldd, pre, M, N, a, d_pre, d_bias, partial, stream);
+        if (e != hipSuccess) return e;
     }
     const Operand rows{a == act::kNone ? d_out : d_pre, a == act::kNone ? ldd : N, false};
     auto plain = [](void *out) { return Epilogue{nullptr, nullptr, 0, nullptr, out, act::kNone}; };
