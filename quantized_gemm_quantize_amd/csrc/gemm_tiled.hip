@@ -400,29 +400,43 @@ __global__ __launch_bounds__(kThreads, OCC) void gemm_tiled_kernel(
                     }
                 }
             __syncthreads();
+            // kAhead rows' residuals are on their way while as many rows are finished
+            constexpr int kTurns = kPass * (WN / 8) / kWave, kAhead = 4;
+            static_assert(kTurns % kAhead == 0, "whole groups of turns");
+            auto row_of = [&](int it) { return it * (kWave / (WN / 8)) + lane / (WN / 8); };
+            auto residual_of = [&](int it) {
+                const int m = mw0 + p * kPass + row_of(it);
+                if (!am.residual || m >= M || n >= N) return make_uint4(0, 0, 0, 0);
+                return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(am.residual) + m * am.ldr + n);
+            };
+            uint4 res[kAhead];
 #pragma unroll
-            for (int it = 0; it < kPass * (WN / 8) / kWave; ++it) {
-                const int ml = it * (kWave / (WN / 8)) + lane / (WN / 8);
-                const int m = mw0 + p * kPass + ml;
-                if (m >= M || n >= N) continue;
-                float v[8];
-                *reinterpret_cast<float4 *>(v) = st[ml * CH + ((lane_n / 4) ^ (ml & PM))];
-                *reinterpret_cast<float4 *>(v + 4) = st[ml * CH + ((lane_n / 4 + 1) ^ (ml & PM))];
+            for (int u = 0; u < kAhead; ++u) res[u] = residual_of(u);
+#pragma nounroll
+            for (int it0 = 0; it0 < kTurns; it0 += kAhead) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += bv[e];
-                act::activate(am.act, v);
-                if (am.residual) {
-                    const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(am.residual) + m * am.ldr + n);
-                    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+                for (int u = 0; u < kAhead; ++u) {
+                    const int ml = row_of(it0 + u), m = mw0 + p * kPass + ml;
+                    const uint32_t w[4] = {res[u].x, res[u].y, res[u].z, res[u].w};
+                    if (it0 + u + kAhead < kTurns) res[u] = residual_of(it0 + u + kAhead);
+                    if (m >= M || n >= N) continue;
+                    float v[8];
+                    *reinterpret_cast<float4 *>(v) = st[ml * CH + ((lane_n / 4) ^ (ml & PM))];
+                    *reinterpret_cast<float4 *>(v + 4) = st[ml * CH + ((lane_n / 4 + 1) ^ (ml & PM))];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[2 * e] += bf16_lo(w[e]);
-                        v[2 * e + 1] += bf16_hi(w[e]);
+                    for (int e = 0; e < 8; ++e) v[e] += bv[e];
+                    act::activate(am.act, v);
+                    if (am.residual) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            v[2 * e] += bf16_lo(w[e]);
+                            v[2 * e + 1] += bf16_hi(w[e]);
+                        }
                     }
+                    store16_nt(static_cast<__bf16 *>(out) + (int64_t)m * N + n,
+                               make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
                 }
-                store16_nt(static_cast<__bf16 *>(out) + (int64_t)m * N + n,
-                           make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
             }
         }
     } else {

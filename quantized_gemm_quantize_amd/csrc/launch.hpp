@@ -161,8 +161,7 @@ constexpr int kMaxH = 16384;
 // out 0 rows of dtype, 1 int8 rows, 2 MXFP4 rows) and its gradients.
 hipError_t launch_forward(const Forward &a, int dtype, int out, hipStream_t stream);
 
-// Most workgroups of the backward pass, each of which leaves partial sums.
-constexpr int kBackwardWorkgroups = 512;
+// Bytes for the partial sums that the backward pass's workgroups leave.
 int64_t backward_workspace(int64_t T, int64_t H);
 hipError_t launch_backward(const Backward &a, int dtype, hipStream_t stream);
 

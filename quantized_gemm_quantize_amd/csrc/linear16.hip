@@ -100,11 +100,10 @@ hipError_t product(const Operand &a, const Operand &b, int64_t M, int64_t N, int
 
 // ---------------------------------------------------------------- d_pre and d_bias
 
-// A workgroup takes 64 columns, ROWS rows at a time (8 threads a row, 8 columns each), every
-// G-th ROWS rows. Column sums are kept in registers, joined in LDS and left as one partial sum per
-// workgroup, or, with one workgroup for all rows, as the result.
-constexpr int kColumns = 64;
-
+// A workgroup takes COLUMNS columns, 8 of them a thread, THREADS / (COLUMNS / 8) rows at a time, every
+// G-th turn of the rows, U turns in flight. Column sums are kept in registers, joined with shuffles
+// and LDS in a fixed order and left as one partial sum per workgroup, or, with one workgroup for
+// all rows, as the result.
 template <int A, Dtype D>
 __device__ __forceinline__ void slopes(float (&d)[8], uint4 pre) {
     float p[8];
@@ -113,68 +112,96 @@ __device__ __forceinline__ void slopes(float (&d)[8], uint4 pre) {
     for (int e = 0; e < 8; ++e) d[e] *= act::slope<A>(p[e]);
 }
 
-template <Dtype D, int ROWS>
-__global__ __launch_bounds__(8 * ROWS) void slope_kernel(const uint16_t *__restrict__ d_out, int64_t ldd,
-                                                    const uint16_t *__restrict__ pre, int64_t M, int64_t N, int a,
-                                                    uint16_t *__restrict__ d_pre, float *__restrict__ partial) {
-    __shared__ float red[ROWS][kColumns];
+template <Dtype D, int COLUMNS, int THREADS, int U>
+__global__ __launch_bounds__(THREADS) void slope_kernel(const uint16_t *__restrict__ d_out, int64_t ldd,
+                                                        const uint16_t *__restrict__ pre, int64_t M, int64_t N, int a,
+                                                        uint16_t *__restrict__ d_pre, float *__restrict__ partial) {
+    constexpr int PER = COLUMNS / 8, ROWS = THREADS / PER, WAVES = THREADS / kWave;
+    static_assert(PER <= kWave, "a wavefront holds whole rows");
+    __shared__ float red[WAVES][COLUMNS];
     w8a8::lds_poison(red);
     w8a8::lds_poison_done();
-    const int c = threadIdx.x % 8 * 8, r = threadIdx.x / 8;
-    const int64_t n = (int64_t)blockIdx.x * kColumns + c;
+    const int c = threadIdx.x % PER * 8, r = threadIdx.x / PER;
+    const int64_t n = (int64_t)blockIdx.x * COLUMNS + c;
     float sum[8] = {};
-    if (n < N)
-        for (int64_t m = (int64_t)blockIdx.y * ROWS + r; m < M; m += (int64_t)gridDim.y * ROWS) {
-            float d[8];
-            widen_chunk<D>(w8a8::load16_stream(d_out + m * ldd + n), d);
-            if (a != act::kNone) {
-                const uint4 p = w8a8::load16_stream(pre + m * N + n);
-                switch (a) {
-                    case act::kRelu: slopes<act::kRelu, D>(d, p); break;
-                    case act::kGelu: slopes<act::kGelu, D>(d, p); break;
-                    case act::kGeluTanh: slopes<act::kGeluTanh, D>(d, p); break;
-                    default: slopes<act::kSilu, D>(d, p); break;
-                }
-                *reinterpret_cast<uint4 *>(d_pre + m * N + n) = narrow_chunk<D>(d);
+    if (n < N) {
+        const int64_t step = (int64_t)gridDim.y * ROWS;
+        for (int64_t m = (int64_t)blockIdx.y * ROWS + r; m < M; m += U * step) {
+            uint4 du[U], pu[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = min(m + u * step, M - 1);
+                du[u] = w8a8::load16_stream(d_out + row * ldd + n);
+                if (a != act::kNone) pu[u] = w8a8::load16_stream(pre + row * N + n);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += d[e];
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = m + u * step;
+                if (row >= M) break;
+                float d[8];
+                widen_chunk<D>(du[u], d);
+                if (a != act::kNone) {
+                    switch (a) {
+                        case act::kRelu: slopes<act::kRelu, D>(d, pu[u]); break;
+                        case act::kGelu: slopes<act::kGelu, D>(d, pu[u]); break;
+                        case act::kGeluTanh: slopes<act::kGeluTanh, D>(d, pu[u]); break;
+                        default: slopes<act::kSilu, D>(d, pu[u]); break;
+                    }
+                    *reinterpret_cast<uint4 *>(d_pre + row * N + n) = narrow_chunk<D>(d);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += d[e];
+            }
         }
+    }
     if (!partial) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[r][c + e] = sum[e];
+    for (int off = PER; off < kWave; off <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor(sum[e], off, kWave);
+    if (threadIdx.x % kWave < PER)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) red[threadIdx.x / kWave][c + e] = sum[e];
     __syncthreads();
-    if (threadIdx.x >= kColumns || (int64_t)blockIdx.x * kColumns + threadIdx.x >= N) return;
+    const int64_t at = (int64_t)blockIdx.x * COLUMNS + threadIdx.x;
+    if (threadIdx.x >= COLUMNS || at >= N) return;
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) s += red[i][threadIdx.x];
-    partial[blockIdx.y * N + (int64_t)blockIdx.x * kColumns + threadIdx.x] = s;
+    for (int i = 0; i < WAVES; ++i) s += red[i][threadIdx.x];
+    partial[blockIdx.y * N + at] = s;
 }
 
-// d_bias[n] = sum of the G partials of column n, in order within 4 slices, then the slices.
-__global__ __launch_bounds__(256) void sum_kernel(const float *__restrict__ partial, int G, int64_t N,
-                                                  float *__restrict__ out) {
-    __shared__ float red[4][64];
+// d_bias[n] = sum of the G partials of column n: 16 slices in order, then the slices.
+constexpr int kSlices = 16;
+
+__global__ __launch_bounds__(64 * kSlices) void sum_kernel(const float *__restrict__ partial, int G, int64_t N,
+                                                           float *__restrict__ out) {
+    __shared__ float red[kSlices][64];
     w8a8::lds_poison(red);
     w8a8::lds_poison_done();
     const int c = threadIdx.x % 64, slice = threadIdx.x / 64;
     const int64_t n = (int64_t)blockIdx.x * 64 + c;
     float s = 0.0f;
     if (n < N)
-        for (int g = slice; g < G; g += 4) s += partial[g * N + n];
+#pragma unroll 4
+        for (int g = slice; g < G; g += kSlices) s += partial[g * N + n];
     red[slice][c] = s;
     __syncthreads();
     if (slice || n >= N) return;
-    out[n] = ((s + red[1][c]) + red[2][c]) + red[3][c];
+#pragma unroll
+    for (int i = 1; i < kSlices; ++i) s += red[i][c];
+    out[n] = s;
 }
 
-// Up to kOneGroup rows go to one workgroup of 1024 threads per 64 columns, which needs no partial sums
-// (257 x 1040 SMALL_US); more to workgroups of 256 threads, enough to fill the chip eight times.
-constexpr int kOneGroup = 512, kFewRows = 128, kManyRows = 32;
+// Up to kOneGroup rows go to one workgroup of 1024 threads per 16 columns, which needs no partial sums
+// (257 x 1040 with 64 columns a workgroup 7.3 us, so SMALL_US); more to workgroups of 256 threads and 64
+// columns, up to 256 beside each other and enough to fill the chip eight times.
+constexpr int kOneGroup = 512, kNarrow = 16, kWide = 64, kManyRows = 32;
 
 int sum_groups(int64_t M, int64_t N) {
     if (M <= kOneGroup) return 1;
-    return (int)std::min(ceil_div(M, kManyRows), std::max<int64_t>(1, 2048 / ceil_div(N, kColumns)));
+    return (int)std::min<int64_t>(std::min<int64_t>(ceil_div(M, kManyRows), 256),
+                                  std::max<int64_t>(1, 2048 / ceil_div(N, kWide)));
 }
 
 int64_t sums_bytes(int64_t M, int64_t N) {
@@ -185,17 +212,17 @@ template <Dtype D>
 hipError_t launch_slope(const void *d_out, int64_t ldd, const void *pre, int64_t M, int64_t N, int a, void *d_pre,
                         float *d_bias, float *partial, hipStream_t stream) {
     const int G = sum_groups(M, N);
-    const dim3 grid((unsigned)ceil_div(N, kColumns), (unsigned)G);
     const uint16_t *d = static_cast<const uint16_t *>(d_out), *p = static_cast<const uint16_t *>(pre);
     uint16_t *to = static_cast<uint16_t *>(d_pre);
     if (M <= kOneGroup) {
-        slope_kernel<D, kFewRows><<<grid, 8 * kFewRows, 0, stream>>>(d, ldd, p, M, N, a, to, d_bias);
+        slope_kernel<D, kNarrow, 1024, 1><<<dim3((unsigned)ceil_div(N, kNarrow)), 1024, 0, stream>>>(d, ldd, p, M, N, a, to, d_bias);
         return hipGetLastError();
     }
-    slope_kernel<D, kManyRows><<<grid, 8 * kManyRows, 0, stream>>>(d, ldd, p, M, N, a, to, d_bias ? partial : nullptr);
+    slope_kernel<D, kWide, 8 * kManyRows, 4><<<dim3((unsigned)ceil_div(N, kWide), (unsigned)G), 8 * kManyRows, 0, stream>>>(
+        d, ldd, p, M, N, a, to, d_bias ? partial : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !d_bias) return e;
-    sum_kernel<<<dim3((unsigned)ceil_div(N, 64)), 256, 0, stream>>>(partial, G, N, d_bias);
+    sum_kernel<<<dim3((unsigned)ceil_div(N, 64)), 64 * kSlices, 0, stream>>>(partial, G, N, d_bias);
     return hipGetLastError();
 }
 

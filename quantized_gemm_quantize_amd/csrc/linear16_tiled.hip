@@ -17,8 +17,9 @@
 //    Row-major tiles: 128-byte rows, chunk c of row r at slot c ^ swz(r). k-major tiles:
 //    rows of BM or BN elements, chunk c of row k at slot c ^ 4 (k % 4): the
 //    four rows that half a wavefront reads at once lie in different banks.
-//  - Rows past the operand's end are read from its last row (never stored); k past its
-//    end is zeroed in LDS on both sides, whatever lies there in memory.
+//  - Rows past the operand's end are read from its last row (never stored). A last stage of
+//    fewer than 64 k is multiplied first, outside the pipeline, with what lies past K masked in
+//    the fragments of both operands.
 //  - The MFMA takes b first: a lane ends with 4 consecutive outputs of a row. They
 //    are staged in fp32 in the wavefront's share of LDS, and bias, activation and
 //    residual act on 8 consecutive outputs per lane; the residual is read and the
@@ -69,10 +70,12 @@ struct Loads {
     static constexpr int N = ROWS * 8 / (kWave * WAVES);
     static_assert(N * kWave * WAVES == ROWS * 8, "whole loads");
     const char *p[N];   // this lane's chunk of each load, in the stage to be loaded next
-    int k[N];           // its first k, relative to the stage
     int64_t step;       // bytes from one stage to the next
 
-    __device__ __forceinline__ void init(const Operand &o, int64_t r0, int64_t last, int64_t k0, int wave, int lane) {
+    // k_left: k of the first stage, where that is short: chunks past them are read from the last
+    // ones (and masked as they are used).
+    __device__ __forceinline__ void init(const Operand &o, int64_t r0, int64_t last, int64_t k0, int wave, int lane,
+                                         int k_left = kStageK) {
         const char *base = static_cast<const char *>(o.p);
         step = KM ? kStageK * 2 * o.ld : kStageK * 2;
 #pragma unroll
@@ -81,24 +84,22 @@ struct Loads {
             if constexpr (KM) {
                 constexpr int per = ROWS / 8;   // chunks of a k row
                 const int kr = slot / per, c = (slot % per) ^ kswz<ROWS>(kr);
-                k[l] = kr;
-                p[l] = base + 2 * ((k0 + kr) * o.ld + min(r0 + 8 * c, last - 7));
+                p[l] = base + 2 * ((k0 + min(kr, k_left - 1)) * o.ld + min(r0 + 8 * c, last - 7));
             } else {
                 const int row = slot / 8, c = (slot % 8) ^ swz(row);
-                k[l] = 8 * c;
-                p[l] = base + 2 * (min(r0 + row, last) * o.ld + k0 + 8 * c);
+                p[l] = base + 2 * (min(r0 + row, last) * o.ld + k0 + min(8 * c, k_left - 8));
             }
         }
     }
-    // Load l of the stage into buf (the operand's slots); k_left: k from this stage's first on.
-    template <bool TAIL>
-    __device__ __forceinline__ void issue(int l, uint4 *buf, int k_left, int wave, int lane) {
+    // Load l of the stage into buf (the operand's slots).
+    __device__ __forceinline__ void issue(int l, uint4 *buf, int wave) {
         uint4 *dst = buf + kWave * (wave + WAVES * l);
-        if (!TAIL || k_left >= kStageK || k[l] < k_left)
-            __builtin_amdgcn_global_load_lds((global_void *)p[l], (lds_void *)dst, 16, 0, 0);
-        else
-            dst[lane] = make_uint4(0, 0, 0, 0);
+        __builtin_amdgcn_global_load_lds((global_void *)p[l], (lds_void *)dst, 16, 0, 0);
         p[l] += step;
+    }
+    __device__ __forceinline__ void issue_all(uint4 *buf, int wave) {
+#pragma unroll
+        for (int l = 0; l < N; ++l) issue(l, buf, wave);
     }
 };
 
@@ -156,10 +157,16 @@ __device__ __forceinline__ void tile_at(const Tiles &g, int t, int BM, int BN, i
     n0 = (int64_t)(t % per_group / gsize) * BN;
 }
 
+// Eight residual values (0 without a residual), as stored.
+__device__ __forceinline__ uint4 residual_at(const Epilogue &ep, int64_t m, int64_t n, bool in) {
+    if (!ep.residual || !in) return make_uint4(0, 0, 0, 0);
+    return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(ep.residual) + m * ep.ldr + n);
+}
+
 // Outputs (m, n ... n + 7) from their sums.
 template <bool F16, bool STREAM>
-__device__ __forceinline__ void finish(float (&v)[8], const float (&bias)[8], const Epilogue &ep, int64_t N, int64_t m,
-                                       int64_t n) {
+__device__ __forceinline__ void finish(float (&v)[8], const float (&bias)[8], uint4 residual, const Epilogue &ep, int64_t N,
+                                       int64_t m, int64_t n) {
     constexpr auto D = F16 ? kF16 : kBf16;
     auto store = [](void *to, uint4 u) {
         if constexpr (STREAM) w8a8::store16_nt(to, u);
@@ -171,7 +178,7 @@ __device__ __forceinline__ void finish(float (&v)[8], const float (&bias)[8], co
     act::activate(ep.act, v);
     if (ep.residual) {
         float r[8];
-        rows::widen_chunk<D>(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(ep.residual) + m * ep.ldr + n), r);
+        rows::widen_chunk<D>(residual, r);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += r[e];
     }
@@ -186,14 +193,14 @@ __device__ __forceinline__ void finish(float (&v)[8], const float (&bias)[8], co
 // loads into `before`, the buffer of the stage before. Fragment reads and loads go out between the
 // MFMAs; scheduling barriers pin the order.
 struct Ahead {
-    bool full;           // all stages that the counted wait assumes are in flight
-    bool rest, begin;    // whether there are loads into the buffer before, into this one
-    int rest_k, begin_k; // k left from their stage's first on
+    bool full;         // the stages that the counted wait assumes are in flight
+    bool rest, begin;  // whether there are loads into the buffer before, into this one
 };
-template <bool F16, int TM, int TN, int BM, int NB, bool TAIL, typename LA, typename LB, typename FA, typename FB>
+
+template <bool F16, int TM, int TN, int BM, int NB, typename LA, typename LB, typename FA, typename FB>
 __device__ __forceinline__ void stage(uint4 *__restrict__ rd, const uint4 *__restrict__ nx, uint4 *__restrict__ before, LA &la,
-                                      LB &lb, const FA &fa, const FB &fb, const Ahead &h, int wave, int lane,
-                                      v4f (&acc)[TM][TN], v4i (&xa)[2][TM], v4i (&wb)[2][TN]) {
+                                      LB &lb, const FA &fa, const FB &fb, const Ahead &h, int wave, v4f (&acc)[TM][TN],
+                                      v4i (&xa)[2][TM], v4i (&wb)[2][TN]) {
     constexpr int NLD = LA::N + LB::N, NMF = TM * TN, BSLOT = BM * 8;
     constexpr int LPK = NB == 2 ? NLD : (NLD + kSteps - 1) / kSteps;   // loads per step
     constexpr int GAP = NMF / LPK;                                     // MFMAs per load
@@ -225,12 +232,38 @@ __device__ __forceinline__ void stage(uint4 *__restrict__ rd, const uint4 *__res
                 const int l = first + q / GAP;
                 if (l < NLD && (last ? h.begin : h.rest)) {
                     uint4 *to = last ? rd : before;
-                    const int left = last ? h.begin_k : h.rest_k;
-                    if (l < LA::N) la.template issue<TAIL>(l, to, left, wave, lane);
-                    else lb.template issue<TAIL>(l - LA::N, to + BSLOT, left, wave, lane);
+                    if (l < LA::N) la.issue(l, to, wave);
+                    else lb.issue(l - LA::N, to + BSLOT, wave);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+}
+
+// The words of a fragment with elements past `valid` zeroed.
+__device__ __forceinline__ v4i first_elements(v4i f, int valid) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) f[w] = 2 * w + 1 < valid ? f[w] : 2 * w < valid ? f[w] & 0xFFFF : 0;
+    return f;
+}
+
+// The products of a stage of k_left < 64 k, outside the pipeline: what lies past them counts as 0 on both
+// sides, whatever was read there.
+template <bool F16, int TM, int TN, int BM, typename FA, typename FB>
+__device__ __forceinline__ void short_stage(const uint4 *__restrict__ rd, const FA &fa, const FB &fb, int k_left, int lane,
+                                            v4f (&acc)[TM][TN]) {
+#pragma unroll
+    for (int kk = 0; kk < kSteps; ++kk) {
+        const int valid = k_left - kStep * kk - 8 * (lane >> 4);
+        v4i w[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) w[j] = first_elements(fb.read(rd + BM * 8, j, kk), valid);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const v4i x = first_elements(fa.read(rd, i, kk), valid);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<F16>(w[j], x, acc[i][j]);
         }
     }
 }
@@ -251,11 +284,12 @@ __global__ __launch_bounds__(GM *GN *kWave, GM *GN *OCC / 4) void tiled_kernel(c
     // the whole tiles, then the parts of the others, each spread over the XCDs for themselves
     const int block = blockIdx.x, tiles = g.tiles_m * g.tiles_n;
     const bool split = block >= g.whole;
-    int t, unit = 0, s0 = 0, s1 = (int)((g.K + kStageK - 1) / kStageK);
+    const int stages = (int)((g.K + kStageK - 1) / kStageK);
+    int t, unit = 0, s0 = 0, s1 = stages;
     if (split) {
         unit = w8a8::xcd_contiguous(block - g.whole, (tiles - g.whole) * g.splits);
         t = g.whole + unit / g.splits;
-        const int part = unit % g.splits, stages = s1;
+        const int part = unit % g.splits;
         s0 = (int)((int64_t)stages * part / g.splits);
         s1 = (int)((int64_t)stages * (part + 1) / g.splits);
     } else {
@@ -264,47 +298,69 @@ __global__ __launch_bounds__(GM *GN *kWave, GM *GN *OCC / 4) void tiled_kernel(c
     int64_t m0, n0;
     tile_at(g, t, BM, BN, m0, n0);
 
-    Loads<KA, BM, WAVES> la;
-    Loads<KB, BN, WAVES> lb;
-    la.init(g.a, m0, g.M - 1, (int64_t)s0 * kStageK, wave, lane);
-    lb.init(g.b, n0, g.N - 1, (int64_t)s0 * kStageK, wave, lane);
     Fragments<KA, BM, TM> fa;
     Fragments<KB, BN, TN> fb;
     fa.init(wm * WM, lane);
     fb.init(wn * WN, lane);
-    auto left = [&](int s) { return (int)min(g.K - (int64_t)s * kStageK, (int64_t)kStageK); };
-
     v4f acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = v4f{};
-    v4i xa[2][TM], wb[2][TN];
-    if (s0 < s1) {
+
+    Loads<KA, BM, WAVES> la;
+    Loads<KB, BN, WAVES> lb;
+    constexpr int NLD = la.N + lb.N;
+    int at = 0;   // buffer of the first stage
+    if (TAIL && s1 == stages) {
+        // the product's last, short stage goes first, through buffer 0, while the whole ones arrive
+        --s1;
+        const int k_left = (int)(g.K - (int64_t)s1 * kStageK);
+        la.init(g.a, m0, g.M - 1, (int64_t)s1 * kStageK, wave, lane, k_left);
+        lb.init(g.b, n0, g.N - 1, (int64_t)s1 * kStageK, wave, lane, k_left);
+        la.issue_all(lds, wave);
+        lb.issue_all(lds + BSLOT, wave);
+        la.init(g.a, m0, g.M - 1, (int64_t)s0 * kStageK, wave, lane);
+        lb.init(g.b, n0, g.N - 1, (int64_t)s0 * kStageK, wave, lane);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            if (s0 + b >= s1) break;
-            uint4 *buf = lds + b * STAGE;
-#pragma unroll
-            for (int l = 0; l < la.N; ++l) la.template issue<TAIL>(l, buf, left(s0 + b), wave, lane);
-#pragma unroll
-            for (int l = 0; l < lb.N; ++l) lb.template issue<TAIL>(l, buf + BSLOT, left(s0 + b), wave, lane);
-        }
-        // a stage whose chunks lie past K has fewer loads than the counted waits assume: once the last
-        // stage is among those in flight, all are waited for
-        const int counted = s1 - (TAIL ? 1 : 0);
-        if (s0 + NB - 1 < counted) stage_barrier<(NB - 1) * (la.N + lb.N)>();
+        for (int b = 1; b < NB; ++b)
+            if (s0 + b - 1 < s1) {
+                la.issue_all(lds + b * STAGE, wave);
+                lb.issue_all(lds + b * STAGE + BSLOT, wave);
+            }
+        if (s0 + NB - 1 <= s1) stage_barrier<(NB - 1) * NLD>();
         else stage_barrier<0>();
+        short_stage<F16, TM, TN, BM>(lds, fa, fb, k_left, lane, acc);
+        if (s0 + NB - 1 <= s1) stage_barrier<(NB - 2) * NLD>();
+        else stage_barrier<0>();
+        if (s0 + NB - 1 < s1) {
+            la.issue_all(lds, wave);
+            lb.issue_all(lds + BSLOT, wave);
+        }
+        at = 1;
+    } else if (s0 < s1) {
+        la.init(g.a, m0, g.M - 1, (int64_t)s0 * kStageK, wave, lane);
+        lb.init(g.b, n0, g.N - 1, (int64_t)s0 * kStageK, wave, lane);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) xa[0][i] = fa.read(lds, i, 0);
+        for (int b = 0; b < NB; ++b)
+            if (s0 + b < s1) {
+                la.issue_all(lds + b * STAGE, wave);
+                lb.issue_all(lds + b * STAGE + BSLOT, wave);
+            }
+        if (s0 + NB - 1 < s1) stage_barrier<(NB - 1) * NLD>();
+        else stage_barrier<0>();
+    }
+    if (s0 < s1) {
+        v4i xa[2][TM], wb[2][TN];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) wb[0][j] = fb.read(lds + BSLOT, j, 0);
-        int at = 0, before = NB - 1;
+        for (int i = 0; i < TM; ++i) xa[0][i] = fa.read(lds + at * STAGE, i, 0);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) wb[0][j] = fb.read(lds + at * STAGE + BSLOT, j, 0);
+        int before = at == 0 ? NB - 1 : at - 1;
         for (int s = s0; s < s1; ++s) {
             const int next = at == NB - 1 ? 0 : at + 1;
-            const Ahead h{s + NB - 1 < counted, s > s0 && s + NB - 1 < s1, s + NB < s1, left(s + NB - 1), left(s + NB)};
-            stage<F16, TM, TN, BM, NB, TAIL>(lds + at * STAGE, lds + next * STAGE, lds + before * STAGE, la, lb, fa, fb, h, wave,
-                                             lane, acc, xa, wb);
+            const Ahead h{s + NB - 1 < s1, s > s0 && s + NB - 1 < s1, s + NB < s1};
+            stage<F16, TM, TN, BM, NB>(lds + at * STAGE, lds + next * STAGE, lds + before * STAGE, la, lb, fa, fb, h, wave, acc, xa, wb);
             before = at;
             at = next;
         }
@@ -323,7 +379,7 @@ __global__ __launch_bounds__(GM *GN *kWave, GM *GN *OCC / 4) void tiled_kernel(c
     const int lane_n = lane % (WN / 8) * 8;
     const int64_t n = n0 + wn * WN + lane_n;
     float bias[8];
-    rows::load_vector<kBf16>(g.ep.bias, (int)n, (int)g.N, 0.0f, bias);
+    rows::load_vector<kBf16, true>(g.ep.bias, (int)n, (int)g.N, 0.0f, bias);
 #pragma unroll
     for (int p = 0; p < WM / kPass; ++p) {
         if (p) __syncthreads();
@@ -335,43 +391,91 @@ __global__ __launch_bounds__(GM *GN *kWave, GM *GN *OCC / 4) void tiled_kernel(c
                 st[ml * CH + ((j * 4 + group) ^ (ml & PM))] = __builtin_bit_cast(float4, acc[p * (kPass / 16) + i][j]);
             }
         __syncthreads();
+        // kAhead rows' residuals are on their way while as many rows are finished
+        constexpr int kTurns = kPass * (WN / 8) / kWave, kAhead = kTurns < 4 ? kTurns : 4;
+        static_assert(kTurns % kAhead == 0, "whole groups of turns");
+        auto row_of = [&](int it) { return it * (kWave / (WN / 8)) + lane / (WN / 8); };
+        auto residual_of = [&](int it) {
+            const int64_t m = m0 + wm * WM + p * kPass + row_of(it);
+            return residual_at(g.ep, m, n, !split && m < g.M && n < g.N);
+        };
+        uint4 res[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) res[u] = residual_of(u);
 #pragma nounroll
-        for (int it = 0; it < kPass * (WN / 8) / kWave; ++it) {
-            const int ml = it * (kWave / (WN / 8)) + lane / (WN / 8), row = wm * WM + p * kPass + ml;
-            if (m0 + row >= g.M || n >= g.N) continue;
-            float v[8];
-            *reinterpret_cast<float4 *>(v) = st[ml * CH + ((lane_n / 4) ^ (ml & PM))];
-            *reinterpret_cast<float4 *>(v + 4) = st[ml * CH + ((lane_n / 4 + 1) ^ (ml & PM))];
-            if (split) {
-                float4 *to = reinterpret_cast<float4 *>(g.partial + ((int64_t)unit * BM + row) * BN + wn * WN + lane_n);
-                to[0] = *reinterpret_cast<float4 *>(v);
-                to[1] = *reinterpret_cast<float4 *>(v + 4);
-            } else {
-                finish<F16, true>(v, bias, g.ep, g.N, m0 + row, n);
+        for (int it0 = 0; it0 < kTurns; it0 += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int it = it0 + u, ml = row_of(it), row = wm * WM + p * kPass + ml;
+                const uint4 r = res[u];
+                if (it + kAhead < kTurns) res[u] = residual_of(it + kAhead);
+                if (m0 + row >= g.M || n >= g.N) continue;
+                float v[8];
+                *reinterpret_cast<float4 *>(v) = st[ml * CH + ((lane_n / 4) ^ (ml & PM))];
+                *reinterpret_cast<float4 *>(v + 4) = st[ml * CH + ((lane_n / 4 + 1) ^ (ml & PM))];
+                if (split) {
+                    float4 *to = reinterpret_cast<float4 *>(g.partial + ((int64_t)unit * BM + row) * BN + wn * WN + lane_n);
+                    to[0] = *reinterpret_cast<float4 *>(v);
+                    to[1] = *reinterpret_cast<float4 *>(v + 4);
+                } else {
+                    finish<F16, true>(v, bias, r, g.ep, g.N, m0 + row, n);
+                }
             }
         }
     }
 }
 
-// The sums of the parts of the split tiles, in order, and the epilogue: 8 outputs per thread.
-template <bool F16, int BM, int BN>
+// The sums of the parts of the split tiles and the epilogue: 8 outputs per thread of the first
+// slice. SLICES slices of the parts are summed in order, then the slices.
+template <bool F16, int BM, int BN, int SLICES>
 __global__ __launch_bounds__(256) void join_kernel(const Tiles g) {
-    constexpr int kBlocks = BM * BN / 8 / 256;   // workgroups of a tile
-    const int tile = blockIdx.x / kBlocks, chunk = blockIdx.x % kBlocks * 256 + threadIdx.x;
+    constexpr int kChunks = 256 / SLICES, kBlocks = BM * BN / 8 / kChunks;   // workgroups of a tile
+    __shared__ float4 red[SLICES > 1 ? SLICES - 1 : 1][kChunks][2];
+    w8a8::lds_poison(red);
+    w8a8::lds_poison_done();
+    const int i = threadIdx.x % kChunks, slice = threadIdx.x / kChunks;
+    const int tile = blockIdx.x / kBlocks, chunk = blockIdx.x % kBlocks * kChunks + i;
     const int row = chunk / (BN / 8), col = chunk % (BN / 8) * 8;
     int64_t m0, n0;
     tile_at(g, g.whole + tile, BM, BN, m0, n0);
     const int64_t m = m0 + row, n = n0 + col;
-    if (m >= g.M || n >= g.N) return;
+    const bool in = m < g.M && n < g.N;
     float v[8] = {}, bias[8];
-    rows::load_vector<kBf16>(g.ep.bias, (int)n, (int)g.N, 0.0f, bias);
-    const float *from = g.partial + ((int64_t)tile * g.splits * BM + row) * BN + col;
-    for (int s = 0; s < g.splits; ++s, from += BM * BN) {
-        const float4 lo = reinterpret_cast<const float4 *>(from)[0], hi = reinterpret_cast<const float4 *>(from)[1];
-        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+    rows::load_vector<kBf16, true>(slice ? nullptr : g.ep.bias, (int)n, (int)g.N, 0.0f, bias);
+    const uint4 residual = residual_at(g.ep, m, n, in && !slice);
+    if (in) {
+        const float *from = g.partial + ((int64_t)tile * g.splits * BM + row) * BN + col;
+#pragma unroll 4
+        for (int s = slice; s < g.splits; s += SLICES) {
+            const float4 *p = reinterpret_cast<const float4 *>(from + (int64_t)s * (BM * BN));
+            const float4 lo = p[0], hi = p[1];
+            v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+            v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+        }
     }
-    finish<F16, false>(v, bias, g.ep, g.N, m, n);
+    if constexpr (SLICES > 1) {
+        if (slice) {
+            red[slice - 1][i][0] = make_float4(v[0], v[1], v[2], v[3]);
+            red[slice - 1][i][1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+        __syncthreads();
+        if (slice) return;
+#pragma unroll
+        for (int s = 0; s < SLICES - 1; ++s) {
+            const float4 lo = red[s][i][0], hi = red[s][i][1];
+            v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+            v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+        }
+    }
+    if (in) finish<F16, false>(v, bias, residual, g.ep, g.N, m, n);
+}
+
+// Many parts of few tiles are summed in 8 slices.
+template <bool F16, int BM, int BN>
+hipError_t launch_join(const Tiles &g, int tiles, hipStream_t stream) {
+    if (g.splits > 8) join_kernel<F16, BM, BN, 8><<<dim3((unsigned)(tiles * (BM * BN / 8 / 32))), 256, 0, stream>>>(g);
+    else join_kernel<F16, BM, BN, 1><<<dim3((unsigned)(tiles * (BM * BN / 8 / 256))), 256, 0, stream>>>(g);
+    return hipGetLastError();
 }
 
 template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC, bool KA, bool KB>
@@ -384,8 +488,7 @@ hipError_t launch(Tiles g, hipStream_t stream) {
     else tiled_kernel<F16, BM, BN, GM, GN, NB, OCC, KA, KB, true><<<grid, block, 0, stream>>>(g);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || g.whole == tiles) return e;
-    join_kernel<F16, BM, BN><<<dim3((unsigned)((tiles - g.whole) * (BM * BN / 8 / 256))), 256, 0, stream>>>(g);
-    return hipGetLastError();
+    return launch_join<F16, BM, BN>(g, tiles - g.whole, stream);
 }
 
 template <bool F16, bool KA, bool KB>

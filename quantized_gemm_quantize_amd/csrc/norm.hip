@@ -11,10 +11,11 @@
 // next product reads, without a pass of their own.
 //
 // Bound by HBM: y, r (and the gate) are read once and r', o written once, with
-// a row in registers between. A row belongs to TPR threads (a wavefront, or a
-// workgroup), chunk c * TPR + t of 16 bytes to thread t; both sums of squares
-// and the row's largest magnitude are reduced with shuffles, and through
-// LDS beyond a wavefront.
+// a row in registers between. A row belongs to TPR threads (16 of a wavefront, a
+// wavefront, or a workgroup), chunk c * TPR + t of 16 bytes to thread t; both
+// sums of squares and the row's largest magnitude are reduced with shuffles, and
+// through LDS beyond a wavefront. Weights (and a gate vector) are loaded beside the row,
+// not after its sums.
 #include "launch.hpp"
 #include "norm.hpp"
 #include "quant_math.hpp"
@@ -47,11 +48,11 @@ __device__ __forceinline__ uint32_t mx_block(const float (&v)[V], uint32_t &code
     return code;
 }
 
-template <Dtype D, Out O, int TPR, int C>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const Forward a) {
+template <Dtype D, Out O, int TPR, int C, bool WHOLE>
+__global__ __launch_bounds__(TPR <= kWave ? 256 : TPR) void norm_kernel(const Forward a) {
     typedef typename Element<D>::type E;
     constexpr int V = kPer<D>;
-    constexpr int kThreads = TPR < 256 ? 256 : TPR;
+    constexpr int kThreads = TPR <= kWave ? 256 : TPR;
     constexpr int kRows = kThreads / TPR;
     __shared__ float red[2][kThreads / kWave][1];
     __shared__ uint32_t red_max[kThreads / kWave];
@@ -72,12 +73,37 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const Forwa
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int k = (c * TPR + t) * V;
-        ru[c] = yu[c] = gu[c] = make_uint4(0, 0, 0, 0);
-        if (k < H) {
-            if (has_y) yu[c] = load_chunk<D, true>(y_row, k, H);
-            ru[c] = load_chunk<D, true>(r_row, k, H);
-            if (gate_rows) gu[c] = load_chunk<D, true>(g_row, k, H);
+        yu[c] = gu[c] = make_uint4(0, 0, 0, 0);
+        if (has_y) yu[c] = load_chunk<D, WHOLE, true>(y_row, k, H);
+        ru[c] = load_chunk<D, WHOLE, true>(r_row, k, H);
+        if (gate_rows) gu[c] = load_chunk<D, WHOLE, true>(g_row, k, H);
+    }
+    // the vectors: with the row where there is room for them
+    constexpr bool kEarly = C <= 2 && TPR < 1024;
+    const float *const vectors[3] = {a.weight, a.post ? a.post_weight : nullptr,
+                                     gate_vector ? static_cast<const float *>(a.gate) : nullptr};
+    float kept[kEarly ? 3 : 1][C][V];
+    if constexpr (kEarly) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+            for (int c = 0; c < C; ++c) load_vector<D, WHOLE>(vectors[i], (c * TPR + t) * V, H, 1.0f, kept[i][c]);
+    }
+    auto vector = [&](int i, int c, float (&f)[V]) {
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[e] = kept[i][c][e];
+        } else {
+            load_vector<D, WHOLE>(vectors[i], (c * TPR + t) * V, H, 1.0f, f);
         }
+    };
+    // (the elements behind the row's end are 0: r, y and gate are cleared there)
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int k = (c * TPR + t) * V;
+        yu[c] = settle<D, WHOLE>(yu[c], k, H);
+        ru[c] = settle<D, WHOLE>(ru[c], k, H);
+        if (gate_rows) gu[c] = settle<D, WHOLE>(gu[c], k, H);
     }
     float v[C][V];  // the new residual, then the output
     float sum[1] = {0.0f};
@@ -86,9 +112,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const Forwa
         if (a.post) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                widen_chunk<D>(yu[c], v[c]);
+                float y[V];
+                widen_chunk<D>(yu[c], y);
 #pragma unroll
-                for (int e = 0; e < V; ++e) sum[0] = __builtin_fmaf(v[c][e], v[c][e], sum[0]);
+                for (int e = 0; e < V; ++e) sum[0] = __builtin_fmaf(y[e], y[e], sum[0]);
             }
             row_sums<TPR>(sum, red[0]);
             inv = 1.0f / __builtin_sqrtf(sum[0] / (float)H + a.eps);
@@ -101,29 +128,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const Forwa
                 for (int e = 0; e < V; ++e) v[c][e] = 0.0f;
                 continue;
             }
+            float r[V], f[V], pw[V];
             widen_chunk<D>(yu[c], v[c]);
-            float r[V], f[V];
             widen_chunk<D>(ru[c], r);
-            if (a.post) {
-                load_vector<D>(a.post_weight, k, H, 1.0f, f);
+            vector(1, c, pw);
+            if (gate_rows) widen_chunk<D>(gu[c], f);
+            else vector(2, c, f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[c][e] = v[c][e] * inv * f[e];
-            }
-            if (gate_rows) {
-                widen_chunk<D>(gu[c], f);
-            } else {
-                load_vector<D>(gate_vector ? static_cast<const float *>(a.gate) : nullptr, k, H, 1.0f, f);
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[c][e] = __builtin_fmaf(a.scale * f[e], v[c][e], r[e]);
-            store_chunk<D>(static_cast<E *>(a.new_residual) + row * H, k, H, narrow_chunk<D>(v[c]));
+            for (int e = 0; e < V; ++e) v[c][e] = __builtin_fmaf(a.scale * f[e], v[c][e] * inv * pw[e], r[e]);
+            store_chunk<D, WHOLE>(static_cast<E *>(a.new_residual) + row * H, k, H, narrow_chunk<D>(v[c]));
         }
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c) widen_chunk<D>(ru[c], v[c]);
     }
 
-    // (the elements behind the row's end are 0: r, y and gate were cleared there)
     sum[0] = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -134,13 +153,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const Forwa
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int k = (c * TPR + t) * V;
-        float w[V];
         if (k >= H) continue;
-        load_vector<D>(a.weight, k, H, 1.0f, w);
+        float w[V];
+        vector(0, c, w);
 #pragma unroll
         for (int e = 0; e < V; ++e) v[c][e] = v[c][e] * inv * w[e];
         if constexpr (O == kSame)
-            store_chunk<D>(static_cast<E *>(a.out) + row * H, k, H, narrow_chunk<D>(v[c]));
+            store_chunk<D, WHOLE>(static_cast<E *>(a.out) + row * H, k, H, narrow_chunk<D>(v[c]));
     }
     if constexpr (O == kInt8) {
         uint32_t top = 0;
@@ -148,8 +167,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const Forwa
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(v[c][e]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, kWave));
+        top = across_row<TPR>(top, [](uint32_t x, uint32_t y) { return max(x, y); });
         if constexpr (TPR > kWave) {
             if (threadIdx.x % kWave == 0) red_max[threadIdx.x / kWave] = top;
             __syncthreads();
@@ -193,21 +211,34 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const Forwa
 
 template <Dtype D, Out O, int TPR, int C>
 hipError_t launch(const Forward &a, hipStream_t stream) {
-    constexpr int kThreads = TPR < 256 ? 256 : TPR, kRows = kThreads / TPR;
-    norm_kernel<D, O, TPR, C>
-        <<<dim3((unsigned)((a.T + kRows - 1) / kRows)), dim3(kThreads), 0, stream>>>(a);
+    constexpr int kThreads = TPR <= kWave ? 256 : TPR, kRows = kThreads / TPR;
+    const dim3 grid((unsigned)((a.T + kRows - 1) / kRows)), block(kThreads);
+    // (quantized rows have whole chunks by their rules on widths)
+    if (O != kSame || a.H % kPer<D> == 0) norm_kernel<D, O, TPR, C, true><<<grid, block, 0, stream>>>(a);
+    else norm_kernel<D, O, TPR, C, O != kSame><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
+
+// Up to so many rows, a row's latency counts more than the rows at once.
+constexpr int kFewRows = 512;
 
 template <Dtype D, Out O>
 hipError_t launch_row(const Forward &a, hipStream_t stream) {
     constexpr int V = kPer<D>;
     const int chunks = (a.H + V - 1) / V;
+    // a chunk or two per thread; few rows over more threads each (one step of 16 rows of 4096: FEW_US)
+    if constexpr (O != kMxfp4) {   // (whose scales are padded to 256 elements)
+        if (chunks <= 16) return launch<D, O, 16, 1>(a, stream);
+    }
     if (chunks <= 64) return launch<D, O, 64, 1>(a, stream);
+    if (chunks <= 256 && a.T <= kFewRows) return launch<D, O, 256, 1>(a, stream);
     if (chunks <= 128) return launch<D, O, 64, 2>(a, stream);
-    if (chunks <= 256) return launch<D, O, 64, 4>(a, stream);
-    if (chunks <= 512) return launch<D, O, 256, 2>(a, stream);
-    if (chunks <= 1024) return launch<D, O, 256, 4>(a, stream);
+    if (chunks <= 256) return launch<D, O, 128, 2>(a, stream);
+    if (chunks <= 512) {
+        if (a.T <= kFewRows) return launch<D, O, 512, 1>(a, stream);
+        return launch<D, O, 256, 2>(a, stream);
+    }
+    if (chunks <= 1024) return launch<D, O, 512, 2>(a, stream);
     if constexpr (D == kF32) {
         if (chunks > 2048) return launch<D, O, 1024, 4>(a, stream);
     }

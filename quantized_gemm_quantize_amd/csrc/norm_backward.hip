@@ -27,12 +27,54 @@ namespace {
 
 using namespace rows;
 
-template <Dtype D, int TPR, int C>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void backward_kernel(const Backward a) {
+// Most workgroups that leave partial sums (narrow rows, several to a workgroup, take more).
+int most_partials(int64_t H) { return H <= 2048 ? 768 : 512; }
+
+constexpr int kOneWorkgroup = 4;   // rows
+
+// A row's operands as loaded.
+template <Dtype D, bool WHOLE, int TPR, int C>
+struct Row {
+    uint4 o[C], n[C], r[C], y[C], g[C];
+
+    // chunk c of this thread
+    template <bool STREAM>
+    __device__ __forceinline__ void load(const Backward &a, int64_t row, int t, int c, bool gate_rows) {
+        typedef typename Element<D>::type E;
+        const int k = (c * TPR + t) * kPer<D>;
+        n[c] = y[c] = g[c] = make_uint4(0, 0, 0, 0);
+        o[c] = load_chunk<D, WHOLE, STREAM>(static_cast<const E *>(a.d_out) + row * a.ldo, k, a.H);
+        r[c] = load_chunk<D, WHOLE, STREAM>(static_cast<const E *>(a.residual) + row * a.ldr, k, a.H);
+        if (a.y) y[c] = load_chunk<D, WHOLE, STREAM>(static_cast<const E *>(a.y) + row * a.ldy, k, a.H);
+        if (a.d_new) n[c] = load_chunk<D, WHOLE, STREAM>(static_cast<const E *>(a.d_new) + row * a.ldn, k, a.H);
+        if (gate_rows) g[c] = load_chunk<D, WHOLE, STREAM>(static_cast<const E *>(a.gate) + row * a.ldg, k, a.H);
+    }
+    __device__ __forceinline__ void settled(int t, int c, int H) {
+        const int k = (c * TPR + t) * kPer<D>;
+        o[c] = settle<D, WHOLE>(o[c], k, H);
+        n[c] = settle<D, WHOLE>(n[c], k, H);
+        r[c] = settle<D, WHOLE>(r[c], k, H);
+        y[c] = settle<D, WHOLE>(y[c], k, H);
+        g[c] = settle<D, WHOLE>(g[c], k, H);
+    }
+};
+
+// POST: a post norm; GATE: none, a vector or rows. (Their sums and vectors would cost registers where
+// they are not there: 16448 rows of 1280 GENERIC_US with all of them in one kernel, so TEMPL_US.)
+enum Gate { kNone, kVector, kRowsOf };
+
+template <Dtype D, bool WHOLE, int TPR, int C, bool POST, Gate GATE>
+__global__ __launch_bounds__(TPR <= kWave ? 256 : TPR) void backward_kernel(const Backward a) {
     typedef typename Element<D>::type E;
     constexpr int V = kPer<D>;
-    constexpr int kThreads = TPR < 256 ? 256 : TPR;
+    constexpr int kThreads = TPR <= kWave ? 256 : TPR;
     constexpr int kRows = kThreads / TPR;
+    // a row's loads are on their way while the one before is computed, where registers allow it
+    // (4096 x 5120 AHEAD_US us); of one chunk per thread the vectors stay in registers, too
+    constexpr bool kKept = C == 1, kAhead = kKept || (WHOLE && TPR < 1024);
+    // Rows of several chunks to each of 1024 threads do not fit in registers beside their sums; they
+    // are read again where they are used (1000 x 16384: spilled 253 us, read again WIDE_US us).
+    constexpr bool kAgain = C > 1 && TPR == 1024;
     __shared__ float red[2][2][kThreads / kWave][3];  // by iteration parity and reduction
     __shared__ float columns[kRows > 1 ? (kRows - 1) * TPR * C * V : 1];
     w8a8::lds_poison(red);
@@ -40,29 +82,47 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void backward_kernel(const B
     w8a8::lds_poison_done();
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int H = a.H;
-    const bool has_y = a.y != nullptr, gate_rows = a.gate && a.ldg != 0, gate_vector = a.gate && a.ldg == 0;
+    const bool has_y = a.y != nullptr;
+    const float *const gate = static_cast<const float *>(a.gate);   // GATE == kVector
     const float per = 1.0f / (float)H;
 
-    float sw[C][V], sp[C][V], sg[C][V];
+    float sw[C][V] = {}, sp[C][V] = {}, sg[C][V] = {};   // of weight, post weight, a gate vector
+    float kept[kKept ? 3 : 1][V];   // weight, post weight, gate
+    if constexpr (kKept) {
+        load_vector<D, WHOLE>(a.weight, t * V, H, 1.0f, kept[0]);
+        if constexpr (POST) load_vector<D, WHOLE>(a.post_weight, t * V, H, 1.0f, kept[1]);
+        if constexpr (GATE == kVector) load_vector<D, WHOLE>(gate, t * V, H, 1.0f, kept[2]);
+    }
+    auto vector = [&](int which, const float *p, int k, float (&v)[V]) {
+        if constexpr (kKept) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int e = 0; e < V; ++e) sw[c][e] = sp[c][e] = sg[c][e] = 0.0f;
+            for (int e = 0; e < V; ++e) v[e] = kept[which][e];
+        } else {
+            load_vector<D, WHOLE>(p, k, H, 1.0f, v);
+        }
+    };
 
-    int parity = 0;
-    for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.T; row += (int64_t)gridDim.x * kRows, parity ^= 1) {
-        uint4 ou[C], nu[C], ru[C], yu[C], gu[C];
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + sub;
+    Row<D, WHOLE, TPR, C> u, ahead;
+    auto load = [&](Row<D, WHOLE, TPR, C> &into, int64_t row) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int k = (c * TPR + t) * V;
-            ou[c] = nu[c] = ru[c] = yu[c] = gu[c] = make_uint4(0, 0, 0, 0);
-            if (k < H) {
-                ou[c] = load_chunk<D, true>(static_cast<const E *>(a.d_out) + row * a.ldo, k, H);
-                ru[c] = load_chunk<D, true>(static_cast<const E *>(a.residual) + row * a.ldr, k, H);
-                if (has_y) yu[c] = load_chunk<D, true>(static_cast<const E *>(a.y) + row * a.ldy, k, H);
-                if (a.d_new) nu[c] = load_chunk<D, true>(static_cast<const E *>(a.d_new) + row * a.ldn, k, H);
-                if (gate_rows) gu[c] = load_chunk<D, true>(static_cast<const E *>(a.gate) + row * a.ldg, k, H);
-            }
+        for (int c = 0; c < C; ++c) into.template load<true>(a, row, t, c, GATE == kRowsOf);
+    };
+    auto again = [&](int64_t row, int c) {
+        if constexpr (kAgain) {
+            asm volatile("" ::: "memory");   // one chunk at a time
+            u.template load<false>(a, row, t, c, GATE == kRowsOf);
+            u.settled(t, c, H);
+        }
+    };
+    if (!kAgain && row < a.T) load(ahead, row);
+    for (int parity = 0; row < a.T; row += step, parity ^= 1) {
+        if constexpr (!kAgain) {
+            u = ahead;
+#pragma unroll
+            for (int c = 0; c < C; ++c) u.settled(t, c, H);
+            if (kAhead && row + step < a.T) load(ahead, row + step);
         }
         // <r', r'>, <y, y>, <d_o weight, r'>
         float sums[3] = {0.0f, 0.0f, 0.0f};
@@ -70,17 +130,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void backward_kernel(const B
         for (int c = 0; c < C; ++c) {
             const int k = (c * TPR + t) * V;
             if (k >= H) continue;
+            again(row, c);
             float o[V], r[V], y[V], w[V];
-            widen_chunk<D>(ou[c], o);
-            widen_chunk<D>(ru[c], r);
-            widen_chunk<D>(yu[c], y);
-            load_vector<D>(a.weight, k, H, 1.0f, w);
+            widen_chunk<D>(u.o[c], o);
+            widen_chunk<D>(u.r[c], r);
+            widen_chunk<D>(u.y[c], y);
+            vector(0, a.weight, k, w);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 sums[0] = __builtin_fmaf(r[e], r[e], sums[0]);
-                sums[1] = __builtin_fmaf(y[e], y[e], sums[1]);
+                if constexpr (POST) sums[1] = __builtin_fmaf(y[e], y[e], sums[1]);
                 sums[2] = __builtin_fmaf(o[e] * w[e], r[e], sums[2]);
             }
+            forget(u.o[c]);
+            forget(u.r[c]);
+            forget(u.y[c]);
         }
         row_sums<TPR>(sums, red[parity][0]);
         const float s = 1.0f / __builtin_sqrtf(sums[0] * per + a.eps);
@@ -92,56 +156,67 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void backward_kernel(const B
         for (int c = 0; c < C; ++c) {
             const int k = (c * TPR + t) * V;
             if (k >= H) continue;
+            again(row, c);
             float o[V], r[V], w[V], n[V], d[V];
-            widen_chunk<D>(ou[c], o);
-            widen_chunk<D>(ru[c], r);
-            widen_chunk<D>(nu[c], n);
-            load_vector<D>(a.weight, k, H, 1.0f, w);
+            widen_chunk<D>(u.o[c], o);
+            widen_chunk<D>(u.r[c], r);
+            widen_chunk<D>(u.n[c], n);
+            vector(0, a.weight, k, w);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 d[e] = __builtin_fmaf(s, o[e] * w[e] - r[e] * along, n[e]);
                 sw[c][e] = __builtin_fmaf(o[e], r[e] * s, sw[c][e]);
             }
-            store_chunk<D>(static_cast<E *>(a.d_residual) + row * H, k, H, narrow_chunk<D>(d));
+            store_chunk<D, WHOLE>(static_cast<E *>(a.d_residual) + row * H, k, H, narrow_chunk<D>(d));
             if (!has_y) continue;
             float y[V], pw[V], f[V];
-            widen_chunk<D>(yu[c], y);
-            load_vector<D>(a.post ? a.post_weight : nullptr, k, H, 1.0f, pw);
-            if (gate_rows) widen_chunk<D>(gu[c], f);
-            else load_vector<D>(gate_vector ? static_cast<const float *>(a.gate) : nullptr, k, H, 1.0f, f);
-            const float unit = a.post ? z : 1.0f;
+            widen_chunk<D>(u.y[c], y);
+            if constexpr (POST) vector(1, a.post_weight, k, pw);
+            if constexpr (GATE == kRowsOf) widen_chunk<D>(u.g[c], f);
+            if constexpr (GATE == kVector) vector(2, gate, k, f);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float q = a.scale * d[e], j = y[e] * unit, g = q * f[e];
-                d[e] = q * (j * pw[e]);                        // the gate's gradient
-                sg[c][e] += d[e];
-                sp[c][e] = __builtin_fmaf(g, j, sp[c][e]);
-                p[c][e] = g * pw[e];
-                dot[0] = __builtin_fmaf(p[c][e], y[e], dot[0]);
+                const float q = a.scale * d[e], j = POST ? y[e] * z : y[e], g = GATE != kNone ? q * f[e] : q;
+                if constexpr (GATE != kNone) d[e] = q * (POST ? j * pw[e] : j);   // the gate's gradient
+                if constexpr (GATE == kVector) sg[c][e] += d[e];
+                p[c][e] = g;
+                if constexpr (POST) {
+                    sp[c][e] = __builtin_fmaf(g, j, sp[c][e]);
+                    p[c][e] = g * pw[e];
+                    dot[0] = __builtin_fmaf(p[c][e], y[e], dot[0]);
+                }
             }
-            if (gate_rows && a.d_gate)
-                store_chunk<D>(static_cast<E *>(a.d_gate) + row * H, k, H, narrow_chunk<D>(d));
+            if (GATE == kRowsOf && a.d_gate)
+                store_chunk<D, WHOLE>(static_cast<E *>(a.d_gate) + row * H, k, H, narrow_chunk<D>(d));
         }
-        if (!has_y) continue;
-        if (a.post) row_sums<TPR>(dot, reinterpret_cast<float (*)[1]>(red[parity][1]));
-        const float back = z * z * dot[0] * per;
+        if (has_y) {
+            if constexpr (POST) row_sums<TPR>(dot, reinterpret_cast<float (*)[1]>(red[parity][1]));
+            const float back = z * z * dot[0] * per;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int k = (c * TPR + t) * V;
-            if (k >= H) continue;
-            if (a.post) {
-                float y[V];
-                widen_chunk<D>(yu[c], y);
+            for (int c = 0; c < C; ++c) {
+                const int k = (c * TPR + t) * V;
+                if (k >= H) continue;
+                if constexpr (POST) {
+                    float y[V];
+                    forget(u.y[c]);
+                    if constexpr (kAgain) {
+                        asm volatile("" ::: "memory");
+                        u.y[c] = load_chunk<D, WHOLE, false>(static_cast<const E *>(a.y) + row * a.ldy, k, H);
+                        u.y[c] = settle<D, WHOLE>(u.y[c], k, H);
+                    }
+                    widen_chunk<D>(u.y[c], y);
 #pragma unroll
-                for (int e = 0; e < V; ++e) p[c][e] = z * (p[c][e] - y[e] * back);
+                    for (int e = 0; e < V; ++e) p[c][e] = z * (p[c][e] - y[e] * back);
+                }
+                store_chunk<D, WHOLE>(static_cast<E *>(a.d_y) + row * H, k, H, narrow_chunk<D>(p[c]));
             }
-            store_chunk<D>(static_cast<E *>(a.d_y) + row * H, k, H, narrow_chunk<D>(p[c]));
         }
+        if (!kAhead && !kAgain && row + step < a.T) load(ahead, row + step);
     }
 
-    // the rows of one workgroup, then its partial sums
+    // the rows of one workgroup, then its partial sums (the results, where it is alone)
     int at = 0;
-    auto give = [&](float (&s)[C][V]) {
+    auto give = [&](float (&s)[C][V], float *alone) {
         if constexpr (kRows > 1) {
             __syncthreads();
             if (sub > 0)
@@ -161,7 +236,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void backward_kernel(const B
 #pragma unroll
                     for (int e = 0; e < V; ++e) s[c][e] += columns[(o * C * V + c * V + e) * TPR + t];
         }
-        float *to = a.partial + ((int64_t)at * gridDim.x + blockIdx.x) * H;
+        float *to = gridDim.x == 1 ? alone : a.partial + ((int64_t)at * gridDim.x + blockIdx.x) * H;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int k = (c * TPR + t) * V;
@@ -171,17 +246,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void backward_kernel(const B
         }
         ++at;
     };
-    if (a.d_weight) give(sw);
-    if (a.d_post_weight) give(sp);
-    if (a.d_gate && gate_vector) give(sg);
+    if (a.d_weight) give(sw, a.d_weight);
+    if (POST && a.d_post_weight) give(sp, a.d_post_weight);
+    if (GATE == kVector && a.d_gate) give(sg, static_cast<float *>(a.d_gate));
 }
 
-// out[h] = sum over G partials of column h, in a fixed order: SLICES slices of
-// the partials, each in order, then the slices.
+// out[h] = sum over G partials of column h, in a fixed order: slices of the partials, each in
+// order, then the slices.
 struct Sums {
     float *out[3];
 };
-constexpr int kColumns = 64, kSlices = 16;
+constexpr int kColumns = 32, kSlices = 32;
 
 __global__ __launch_bounds__(kColumns *kSlices) void sum_partials(const float *__restrict__ partial, int G, int H,
                                                                   Sums to) {
@@ -193,6 +268,7 @@ __global__ __launch_bounds__(kColumns *kSlices) void sum_partials(const float *_
     const float *from = partial + (int64_t)blockIdx.y * G * H + h;
     float s = 0.0f;
     if (h < H)
+#pragma unroll 8
         for (int g = slice; g < G; g += kSlices) s += from[(int64_t)g * H];
     red[slice][c] = s;
     __syncthreads();
@@ -202,16 +278,29 @@ __global__ __launch_bounds__(kColumns *kSlices) void sum_partials(const float *_
     to.out[blockIdx.y][h] = s;
 }
 
-int workgroups(int64_t T, int rows) {
-    return (int)std::min<int64_t>((T + rows - 1) / rows, kBackwardWorkgroups);
+// Workgroups: enough to fill the chip's registers, each with the rows that it takes at once; a few
+// rows go to one, which needs no second launch.
+int workgroups(int64_t T, int64_t H, int rows) {
+    if (T <= std::max(rows, kOneWorkgroup)) return T > 0;
+    return (int)std::min<int64_t>((T + rows - 1) / rows, most_partials(H));
+}
+
+template <Dtype D, bool WHOLE, int TPR, int C, bool POST>
+void launch_gate(const Backward &a, int G, hipStream_t stream) {
+    constexpr int kThreads = TPR <= kWave ? 256 : TPR;
+    const dim3 grid((unsigned)G), block(kThreads);
+    if (!a.gate) backward_kernel<D, WHOLE, TPR, C, POST, kNone><<<grid, block, 0, stream>>>(a);
+    else if (a.ldg == 0) backward_kernel<D, WHOLE, TPR, C, POST, kVector><<<grid, block, 0, stream>>>(a);
+    else backward_kernel<D, WHOLE, TPR, C, POST, kRowsOf><<<grid, block, 0, stream>>>(a);
 }
 
 template <Dtype D, int TPR, int C>
 hipError_t launch(const Backward &a, hipStream_t stream) {
-    constexpr int kThreads = TPR < 256 ? 256 : TPR;
-    const int G = workgroups(a.T, kThreads / TPR);
+    constexpr int kThreads = TPR <= kWave ? 256 : TPR;
+    const int G = workgroups(a.T, a.H, kThreads / TPR);
     if (G) {
-        backward_kernel<D, TPR, C><<<dim3((unsigned)G), dim3(kThreads), 0, stream>>>(a);
+        if (a.H % kPer<D> == 0) a.post ? launch_gate<D, true, TPR, C, true>(a, G, stream) : launch_gate<D, true, TPR, C, false>(a, G, stream);
+        else a.post ? launch_gate<D, false, TPR, C, true>(a, G, stream) : launch_gate<D, false, TPR, C, false>(a, G, stream);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -220,7 +309,7 @@ hipError_t launch(const Backward &a, hipStream_t stream) {
     if (a.d_weight) to.out[n++] = a.d_weight;
     if (a.d_post_weight) to.out[n++] = a.d_post_weight;
     if (a.d_gate && a.ldg == 0) to.out[n++] = static_cast<float *>(a.d_gate);
-    if (!n) return hipSuccess;
+    if (!n || G == 1) return hipSuccess;
     sum_partials<<<dim3((unsigned)((a.H + kColumns - 1) / kColumns), (unsigned)n), dim3(kColumns * kSlices), 0,
                    stream>>>(a.partial, G, a.H, to);
     return hipGetLastError();
@@ -230,13 +319,15 @@ template <Dtype D>
 hipError_t launch_row(const Backward &a, hipStream_t stream) {
     constexpr int V = kPer<D>;
     const int chunks = (a.H + V - 1) / V;
+    if (chunks <= 16) return launch<D, 16, 1>(a, stream);
     if (chunks <= 64) return launch<D, 64, 1>(a, stream);
-    if (chunks <= 128) return launch<D, 64, 2>(a, stream);
     if (chunks <= 256) return launch<D, 256, 1>(a, stream);
-    if (chunks <= 512) return launch<D, 256, 2>(a, stream);
-    if (chunks <= 1024) return launch<D, 256, 4>(a, stream);
+    if (chunks <= 512) return launch<D, 512, 1>(a, stream);
     if constexpr (D == kF32) {
+        if (chunks <= 1024) return launch<D, 1024, 1>(a, stream);
         if (chunks > 2048) return launch<D, 1024, 4>(a, stream);
+    } else {
+        if (chunks <= 1024) return launch<D, 512, 2>(a, stream);
     }
     return launch<D, 1024, 2>(a, stream);
 }
@@ -244,7 +335,7 @@ hipError_t launch_row(const Backward &a, hipStream_t stream) {
 }  // namespace
 
 int64_t backward_workspace(int64_t T, int64_t H) {
-    return 4 * 3 * H * std::min<int64_t>(T, kBackwardWorkgroups);
+    return 4 * 3 * H * std::min<int64_t>(T, most_partials(H));
 }
 
 hipError_t launch_backward(const Backward &a, int dtype, hipStream_t stream) {
