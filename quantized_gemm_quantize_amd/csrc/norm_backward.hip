@@ -15,7 +15,8 @@
 // end they go to partial[b], and a second kernel adds the G partials of each
 // column in a fixed order, so repeated runs agree bit for bit.
 // Bound by HBM: five (six with a gate row) reads and two (three) writes of
-// T x H elements.
+// T x H elements. Measured: 8192 x 4096 bf16 with post norm and gate rows 94 us (5.7 TB/s),
+// 16448 x 1280 with a gate vector 65 us (3.9 TB/s), 4096 x 8192 109 us (3.7); a single row 5 us.
 #include <algorithm>
 
 #include "launch.hpp"
@@ -27,8 +28,8 @@ namespace {
 
 using namespace rows;
 
-// Most workgroups that leave partial sums (narrow rows, several to a workgroup, take more).
-int most_partials(int64_t H) { return H <= 2048 ? 768 : 512; }
+// Most workgroups that leave partial sums.
+int most_partials(int64_t H) { return H <= 2048 ? 768 : H <= 4096 ? 512 : 256; }
 
 constexpr int kOneWorkgroup = 4;   // rows
 
@@ -60,7 +61,7 @@ struct Row {
 };
 
 // POST: a post norm; GATE: none, a vector or rows. (Their sums and vectors would cost registers where
-// they are not there: 16448 rows of 1280 GENERIC_US with all of them in one kernel, so TEMPL_US.)
+// they are not there: 101 of 16-bit rows without either, 140 with both.)
 enum Gate { kNone, kVector, kRowsOf };
 
 template <Dtype D, bool WHOLE, int TPR, int C, bool POST, Gate GATE>
@@ -70,10 +71,10 @@ __global__ __launch_bounds__(TPR <= kWave ? 256 : TPR) void backward_kernel(cons
     constexpr int kThreads = TPR <= kWave ? 256 : TPR;
     constexpr int kRows = kThreads / TPR;
     // a row's loads are on their way while the one before is computed, where registers allow it
-    // (4096 x 5120 AHEAD_US us); of one chunk per thread the vectors stay in registers, too
+    // (4096 x 5120: 126 -> 103 us); of one chunk per thread the vectors stay in registers, too
     constexpr bool kKept = C == 1, kAhead = kKept || (WHOLE && TPR < 1024);
     // Rows of several chunks to each of 1024 threads do not fit in registers beside their sums; they
-    // are read again where they are used (1000 x 16384: spilled 253 us, read again WIDE_US us).
+    // are read again where they are used (1000 x 16384: held and spilled 253 us, read again 175).
     constexpr bool kAgain = C > 1 && TPR == 1024;
     __shared__ float red[2][2][kThreads / kWave][3];  // by iteration parity and reduction
     __shared__ float columns[kRows > 1 ? (kRows - 1) * TPR * C * V : 1];
@@ -241,8 +242,8 @@ __global__ __launch_bounds__(TPR <= kWave ? 256 : TPR) void backward_kernel(cons
         for (int c = 0; c < C; ++c) {
             const int k = (c * TPR + t) * V;
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (k + e < H) to[k + e] = s[c][e];
+            for (int q = 0; q < V; q += 4)
+                store_chunk<kF32, WHOLE>(to, k + q, H, narrow_chunk<kF32>(reinterpret_cast<float (&)[4]>(s[c][q])));
         }
         ++at;
     };
@@ -278,11 +279,17 @@ __global__ __launch_bounds__(kColumns *kSlices) void sum_partials(const float *_
     to.out[blockIdx.y][h] = s;
 }
 
-// Workgroups: enough to fill the chip's registers, each with the rows that it takes at once; a few
-// rows go to one, which needs no second launch.
-int workgroups(int64_t T, int64_t H, int rows) {
+// Workgroups: as many as are resident at once (of 12 wavefronts per CU that their registers allow, 16
+// of 32-bit rows), each with the same number of rows (1000 x 16384, 512 workgroups with a row or two
+// each 175 us, 250 with four each 109; 615 x 2692 33 -> 20); a few rows go to one, which needs no
+// second launch (one row of 4096 8 -> 5 us).
+template <Dtype D>
+int workgroups(int64_t T, int64_t H, int threads, int rows) {
     if (T <= std::max(rows, kOneWorkgroup)) return T > 0;
-    return (int)std::min<int64_t>((T + rows - 1) / rows, most_partials(H));
+    const int64_t resident = 256 * std::max(1, (D == kF32 ? 16 : 12) * kWave / threads);
+    const int64_t most = std::min<int64_t>(resident, most_partials(H));
+    const int64_t steps = (T + rows * most - 1) / (rows * most);
+    return (int)((T + rows * steps - 1) / (rows * steps));
 }
 
 template <Dtype D, bool WHOLE, int TPR, int C, bool POST>
@@ -297,7 +304,7 @@ void launch_gate(const Backward &a, int G, hipStream_t stream) {
 template <Dtype D, int TPR, int C>
 hipError_t launch(const Backward &a, hipStream_t stream) {
     constexpr int kThreads = TPR <= kWave ? 256 : TPR;
-    const int G = workgroups(a.T, a.H, kThreads / TPR);
+    const int G = workgroups<D>(a.T, a.H, kThreads, kThreads / TPR);
     if (G) {
         if (a.H % kPer<D> == 0) a.post ? launch_gate<D, true, TPR, C, true>(a, G, stream) : launch_gate<D, true, TPR, C, false>(a, G, stream);
         else a.post ? launch_gate<D, false, TPR, C, true>(a, G, stream) : launch_gate<D, false, TPR, C, false>(a, G, stream);

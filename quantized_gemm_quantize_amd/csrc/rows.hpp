@@ -44,7 +44,7 @@ __device__ __forceinline__ typename Element<D>::type narrow(float f) {
 // only this once. WHOLE: rows of whole chunks. Other rows are loaded in two parts: a load that every
 // thread makes without a branch, of the row's last kPer elements where the chunk ends behind it, and,
 // when the chunk is used, the shift of those into their places. (Element loads in a branch wait there,
-// which ends what is in flight: 2864 x 1189 backward BACK_US us. Rows of whole chunks have no use for
+// which ends what is in flight: 2864 x 1189 backward 52 us, without 31. Rows of whole chunks have no use for
 // it: 8192 x 4096 backward 103, with it 128.) Rows shorter than a chunk are loaded by elements.
 template <Dtype D, bool WHOLE, bool STREAM>
 __device__ __forceinline__ uint4 load_chunk(const typename Element<D>::type *row, int k, int width) {
