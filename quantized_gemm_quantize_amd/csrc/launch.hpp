@@ -174,6 +174,7 @@ struct Epilogue;
 // 16-bit products (bf16, or binary16 when f16): x [M,K] with row stride ldx times w [N,K] with
 // the epilogue, and the gradients (null outputs are left out). d_pre is not written without an
 // activation (it is d_out then).
+int debug_form(int64_t M, int64_t N, int64_t K, bool forward);
 int64_t forward_workspace(int64_t M, int64_t N, int64_t K);
 int64_t backward_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_forward(const void *x, int64_t ldx, int64_t M, const void *w, int64_t N, int64_t K, bool f16,

@@ -228,6 +228,12 @@ hipError_t launch_slope(const void *d_out, int64_t ldd, const void *pre, int64_t
 
 }  // namespace
 
+int debug_form(int64_t M, int64_t N, int64_t K, bool forward) {
+    Plan plan = estimate(M, N, K).plan;
+    if (forward && few_rows(M, N, K, plan)) return 1000000;
+    return plan.form * 100000 + (plan.whole > 0) * 10000 + plan.splits;
+}
+
 int64_t forward_workspace(int64_t M, int64_t N, int64_t K) {
     Plan plan;
     return few_rows(M, N, K, plan) ? 0 : plan.workspace;

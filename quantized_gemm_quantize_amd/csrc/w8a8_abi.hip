@@ -670,6 +670,12 @@ static w8a8_status linear16_shape(int64_t M, int64_t N, int64_t K) {
     return W8A8_OK;
 }
 
+// Not part of the interface (the tests ask it which sizes reach which kernel): of a 16-bit product, 10^6
+// for the kernel of few rows, otherwise the tiles' form * 10^5 + (whole tiles) * 10^4 + splits.
+int w16a16_debug_form(int64_t M, int64_t N, int64_t K, int forward) {
+    return linear16::debug_form(M, N, K, forward != 0);
+}
+
 int64_t w16a16_linear_workspace(int64_t M, int64_t N, int64_t K) {
     return linear16_shape(M, N, K) == W8A8_OK ? linear16::forward_workspace(M, N, K) : 0;
 }
@@ -838,7 +844,7 @@ const char *w8a8_status_string(int status) {
         case W8A8_ERR_BLOCKSIZE: return "BSR block size must be 64";
         case W8A8_ERR_DTYPE: return "unknown output dtype";
         case W8A8_ERR_HIP: return "HIP launch error (see w8a8_last_hip_error)";
-        case W8A8_ERR_VALUE: return "alpha or beta is not finite";
+        case W8A8_ERR_VALUE: return "a scalar is not finite or out of range";
         default: return "unknown status";
     }
 }

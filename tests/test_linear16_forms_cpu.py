@@ -1,0 +1,60 @@
+"""The sizes of the GPU tests reach every compiled variant of the 16-bit products, without a GPU."""
+import os
+import re
+
+import pytest
+
+from linear16_sizes import FORMS, ROWS, TILED, form
+from quantized_gemm_quantize_amd import binding, build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(binding.LIB_PATH):
+        pytest.skip("libw8a8.so not built")
+    return binding.load()
+
+
+def test_every_tile_is_reached(lib):
+    text = open(os.path.join(build.CSRC, "linear16_tiled.hip")).read()
+    assert len(set(re.findall(r"return launch<F16, (\d+, \d+, \d, \d, \d), \d, KA, KB>", text))) == FORMS
+    for forward in (True, False):
+        reached = {form(lib, *size, forward) for size in TILED}
+        assert {r[0] for r in reached} == set(range(FORMS))
+        for f in range(FORMS):
+            for tail in (False, True):
+                # all tiles whole, all shared, and some of each where a round of tiles does not hold them all
+                assert (f, True, False, tail) in reached and (f, False, True, tail) in reached
+                assert f == 0 or (f, True, True, tail) in reached
+
+
+def test_gradients_reach_every_tile_too(lib):
+    """The same three sizes as (rows, inner, channels) and (channels, inner, rows) of a layer's gradients."""
+    for m, n, k in TILED:
+        assert m % 8 == n % 8 == k % 8 == 0
+        assert lib.w16a16_linear_backward_workspace(m, k, n) >= 0
+
+
+def test_few_rows(lib):
+    assert {-(-m // 16) for m, _, _ in ROWS} == {1, 2, 3, 4}
+    assert all(form(lib, *size) == ("rows",) for size in ROWS)
+    # past 16 rows only where few workgroups of it run one after the other
+    assert form(lib, 16, 65536, 4096) == ("rows",) and form(lib, 17, 65536, 4096) != ("rows",)
+    assert form(lib, 65, 64, 64) != ("rows",)
+
+
+def test_workspaces_hold_the_shared_tiles(lib):
+    tile = [64 * 64, 128 * 128, 128 * 128, 256 * 128, 256 * 256]
+    sides = [(64, 64), (128, 128), (128, 128), (256, 128), (256, 256)]
+    for m, n, k in TILED:
+        f, whole, shared, _ = form(lib, m, n, k)
+        need = lib.w16a16_linear_workspace(m, n, k)
+        if not shared:
+            assert need == 0
+            continue
+        bm, bn = sides[f]
+        tiles = -(-m // bm) * -(-n // bn)
+        slots = [768, 256, 512, 256, 256][f]
+        rest = tiles % slots if whole else tiles
+        assert need % (4 * tile[f] * rest) == 0 and 2 <= need // (4 * tile[f] * rest) <= 64
+        assert lib.w16a16_linear_workspace(m, n, k + 4) == 0      # a refused size
