@@ -170,16 +170,15 @@ hipError_t launch_backward(const Backward &a, int dtype, hipStream_t stream);
 namespace linear16 {
 
 struct Epilogue;
+struct ForwardPlan;
+struct BackwardPlan;
 
 // 16-bit products (bf16, or binary16 when f16): x [M,K] with row stride ldx times w [N,K] with
-// the epilogue, and the gradients (null outputs are left out). d_pre is not written without an
-// activation (it is d_out then).
-int debug_form(int64_t M, int64_t N, int64_t K, bool forward);
-int64_t forward_workspace(int64_t M, int64_t N, int64_t K);
-int64_t backward_workspace(int64_t M, int64_t N, int64_t K);
-hipError_t launch_forward(const void *x, int64_t ldx, int64_t M, const void *w, int64_t N, int64_t K, bool f16,
-                          const Epilogue &ep, void *workspace, hipStream_t stream);
-hipError_t launch_backward(const void *d_out, int64_t ldd, const void *x, int64_t ldx, const void *w,
+// the epilogue, and the gradients (null outputs are left out), by the plans of linear16.hpp for their
+// sizes. d_pre is not written without an activation (it is d_out then).
+hipError_t launch_forward(const ForwardPlan &plan, const void *x, int64_t ldx, int64_t M, const void *w, int64_t N, int64_t K,
+                          bool f16, const Epilogue &ep, void *workspace, hipStream_t stream);
+hipError_t launch_backward(const BackwardPlan &plan, const void *d_out, int64_t ldd, const void *x, int64_t ldx, const void *w,
                            const void *pre, int64_t M, int64_t N, int64_t K, bool f16, int act, void *d_pre,
                            void *d_x, void *d_w, float *d_bias, void *workspace, hipStream_t stream);
 

@@ -80,6 +80,61 @@ Estimate estimate(int64_t M, int64_t N, int64_t K) {
     return best;
 }
 
+struct PairEstimate {
+    PairPlan plan;
+    double us;
+};
+
+// The plan with the least estimated time for both gradients in one launch. The product of the longer k goes
+// first, its tiles whole or all of them shared by s workgroups; the other's tiles follow on workgroup
+// slots as they come free, whole, or whole up to the end of one of their rounds and the rest shared.
+// With p slots free from `from` on, q from `later` on (a round of the first product more), and
+// `each` a tile: the rounds that hold n tiles, and the tiles done at a time.
+PairEstimate estimate_pair(int64_t M, int64_t N, int64_t K) {
+    PairEstimate best{{}, -1};
+    const bool w_first = M >= N;
+    // rows, columns and stages of the first product and the second
+    const int64_t rows[2] = {w_first ? N : M, w_first ? M : N}, stages[2] = {ceil_div(w_first ? M : N, 64), ceil_div(w_first ? N : M, 64)};
+    for (const Form form : {k64x64, k128x128, k256x256}) {
+        const FormTime &f = kTimes[form];
+        const int64_t columns = ceil_div(K, f.bn), first = ceil_div(rows[0], f.bm) * columns, second = ceil_div(rows[1], f.bm) * columns;
+        const double join = 2.0 * f.bm * f.bn * 4 / 4.5e6;   // of one part
+        for (int64_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+            if (s > 1 && s > stages[0] / 2) break;
+            const int64_t units = first * s, q = units % f.slots, p = f.slots - q;
+            const double fill = std::min(1.0, (double)(units + second) / f.slots), per = f.lo + (f.hi - f.lo) * fill * fill;
+            const double one = f.fixed + ceil_div(stages[0], s) * per, each = f.fixed + stages[1] * per;
+            const double from = units / f.slots * one, later = q ? from + one : from;
+            const double joined = s > 1 ? 3.0 + units * join : 0.0, behind = q ? one / each : 0.0;
+            auto done = [&](double t) {
+                return p * (int64_t)std::max(0.0, (t - from) / each + 1e-9) + q * (int64_t)std::max(0.0, (t - later) / each + 1e-9);
+            };
+            auto offer = [&](double us, int64_t whole, int64_t splits) {
+                if (best.us >= 0 && us >= best.us) return;
+                const int64_t bytes = (int64_t)f.bm * f.bn * 4;
+                const Plan a{form, s > 1 ? 0 : (int)first, (int)s, s > 1 ? units * bytes : 0};
+                const Plan b{form, (int)whole, (int)splits, (second - whole) * splits * bytes};
+                best = w_first ? PairEstimate{{b, a, true}, us} : PairEstimate{{a, b, false}, us};
+            };
+            // ends after k rounds from `from` on (some before `later`), or from `later` on
+            const int64_t early = ceil_div(second, p);
+            const int64_t k0 = early <= behind ? early : (int64_t)std::ceil((second + q * std::ceil(behind)) / f.slots);
+            const int64_t k1 = std::max<int64_t>(0, ceil_div(second - p * (int64_t)behind, f.slots));
+            for (const double end : {from + k0 * each, later + k1 * each}) {
+                if (done(end) >= second) offer(std::max(end, later) + joined, second, 1);
+                const double before = end - each;
+                const int64_t whole = before < later ? 0 : done(before), rest = second - whole;
+                if (rest <= 0 || before < later) continue;
+                for (int64_t splits : {2, 4, 8, 16, 32}) {
+                    if (splits * rest > f.slots || splits > stages[1] / 2) break;
+                    offer(before + f.fixed + ceil_div(stages[1], splits) * per + 3.0 + rest * splits * join + joined, whole, splits);
+                }
+            }
+        }
+    }
+    return best;
+}
+
 // The kernel of few rows: up to 16 rows always (1 x 4096 x 4096 5.8 us against 13 in tiles), up to 64
 // where it is estimated to be quicker: 3 us and both operands of a workgroup at 65 GB/s a round
 // (64 rows: 4096 x 4096 11.7 us against 13.0, 8192 x 2048 14.9 / 12.2, 4096 x 11008 32.7 / 23.7).
@@ -91,11 +146,6 @@ bool few_rows(int64_t M, int64_t N, int64_t K, Plan &plan) {
     if (M > kMaxRows) return false;
     const int64_t rounds = ceil_div(ceil_div(N, 16), 256);
     return rounds * (3.0 + 2.0 * K * 16 * (ceil_div(M, 16) + 1) / 65e3) < tiled.us;
-}
-
-hipError_t product(const Operand &a, const Operand &b, int64_t M, int64_t N, int64_t K, bool f16, const Epilogue &ep,
-                   void *workspace, hipStream_t stream) {
-    return launch_tiled(a, b, M, N, K, f16, estimate(M, N, K).plan, static_cast<float *>(workspace), ep, stream);
 }
 
 // ---------------------------------------------------------------- d_pre and d_bias
@@ -228,46 +278,55 @@ hipError_t launch_slope(const void *d_out, int64_t ldd, const void *pre, int64_t
 
 }  // namespace
 
-int debug_form(int64_t M, int64_t N, int64_t K, bool forward) {
-    Plan plan = estimate(M, N, K).plan;
-    if (forward && few_rows(M, N, K, plan)) return 1000000;
-    return plan.form * 100000 + (plan.whole > 0) * 10000 + plan.splits;
+ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K) {
+    ForwardPlan p{};
+    p.rows = few_rows(M, N, K, p.tiles);
+    return p;
 }
 
-int64_t forward_workspace(int64_t M, int64_t N, int64_t K) {
-    Plan plan;
-    return few_rows(M, N, K, plan) ? 0 : plan.workspace;
+// Both gradients in one launch where that is estimated to be quicker than one after the other, with 2 us
+// between them: 257 x 1040 x 1312 with silu 20.2 -> 14.0 us in all, 3611 x 304 x 1024 34.7 -> 29.7,
+// 16448 x 5120 x 1280 525 -> 484.
+BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K) {
+    BackwardPlan p{};
+    const Estimate w = estimate(N, K, M);
+    p.w = w.plan;
+    p.workspace = std::max(sums_bytes(M, N), p.w.workspace);
+    if (!M) return p;
+    const Estimate x = estimate(M, K, N);
+    const PairEstimate both = estimate_pair(M, N, K);
+    p.x = x.plan;
+    p.together = both.us < x.us + w.us + 2.0;
+    p.both = both.plan;
+    p.workspace = std::max(p.workspace, p.x.workspace);   // (the column sums are done before the products)
+    if (p.together) p.workspace = std::max(p.workspace, p.both.x.workspace + p.both.w.workspace);
+    return p;
 }
 
-int64_t backward_workspace(int64_t M, int64_t N, int64_t K) {
-    // the products run one after the other; the column sums are done before them
-    const int64_t d_x = M ? estimate(M, K, N).plan.workspace : 0, d_w = estimate(N, K, M).plan.workspace;
-    return std::max(sums_bytes(M, N), std::max(d_x, d_w));
+hipError_t launch_forward(const ForwardPlan &plan, const void *x, int64_t ldx, int64_t M, const void *w, int64_t N, int64_t K,
+                          bool f16, const Epilogue &ep, void *workspace, hipStream_t stream) {
+    if (plan.rows) return launch_rows(x, ldx, (int)M, w, (int)N, (int)K, f16, ep, stream);
+    return launch_tiled({x, ldx, false}, {w, K, false}, M, N, K, f16, plan.tiles, static_cast<float *>(workspace), ep, stream);
 }
 
-hipError_t launch_forward(const void *x, int64_t ldx, int64_t M, const void *w, int64_t N, int64_t K, bool f16,
-                          const Epilogue &ep, void *workspace, hipStream_t stream) {
-    Plan plan;
-    if (few_rows(M, N, K, plan)) return launch_rows(x, ldx, (int)M, w, (int)N, (int)K, f16, ep, stream);
-    return launch_tiled({x, ldx, false}, {w, K, false}, M, N, K, f16, plan, static_cast<float *>(workspace), ep, stream);
-}
-
-hipError_t launch_backward(const void *d_out, int64_t ldd, const void *x, int64_t ldx, const void *w, const void *pre,
-                           int64_t M, int64_t N, int64_t K, bool f16, int a, void *d_pre, void *d_x, void *d_w,
-                           float *d_bias, void *workspace, hipStream_t stream) {
+hipError_t launch_backward(const BackwardPlan &plan, const void *d_out, int64_t ldd, const void *x, int64_t ldx, const void *w,
+                           const void *pre, int64_t M, int64_t N, int64_t K, bool f16, int a, void *d_pre, void *d_x,
+                           void *d_w, float *d_bias, void *workspace, hipStream_t stream) {
+    float *const partial = static_cast<float *>(workspace);
     hipError_t e = hipSuccess;
     if (d_bias || (a != act::kNone && M)) {
-        float *partial = static_cast<float *>(workspace);
         e = f16 ? launch_slope<kF16>(d_out, ldd, pre, M, N, a, d_pre, d_bias, partial, stream)
                 : launch_slope<kBf16>(d_out, ldd, pre, M, N, a, d_pre, d_bias, partial, stream);
         if (e != hipSuccess) return e;
     }
     const Operand rows{a == act::kNone ? d_out : d_pre, a == act::kNone ? ldd : N, false};
+    const Operand weight{w, K, true}, columns{rows.p, rows.ld, true}, inputs{x, ldx, true};
+    if (d_x && d_w && plan.together)
+        return launch_pair({rows, weight, M, K, N, d_x}, {columns, inputs, N, K, M, d_w}, f16, plan.both, partial, stream);
     auto plain = [](void *out) { return Epilogue{nullptr, nullptr, 0, nullptr, out, act::kNone}; };
-    if (d_x && M && (e = product(rows, {w, K, true}, M, K, N, f16, plain(d_x), workspace, stream)) != hipSuccess)
-        return e;
-    if (d_w) return product({rows.p, rows.ld, true}, {x, ldx, true}, N, K, M, f16, plain(d_w), workspace, stream);
-    return hipSuccess;
+    if (d_x && M) e = launch_tiled(rows, weight, M, K, N, f16, plan.x, partial, plain(d_x), stream);
+    if (d_w && e == hipSuccess) e = launch_tiled(columns, inputs, N, K, M, f16, plan.w, partial, plain(d_w), stream);
+    return e;
 }
 
 }  // namespace linear16

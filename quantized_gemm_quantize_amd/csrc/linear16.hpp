@@ -36,6 +36,36 @@ struct Plan {
 hipError_t launch_tiled(const Operand &a, const Operand &b, int64_t M, int64_t N, int64_t K, bool f16, const Plan &plan,
                         float *partial, const Epilogue &ep, hipStream_t stream);
 
+// d_x and d_w in one launch: plain products of one form, b k-major, a of w too. The workgroups of one
+// come first.
+struct Product {
+    Operand a, b;
+    int64_t M, N, K;
+    void *out;
+};
+struct PairPlan {
+    Plan x, w;
+    bool w_first;
+};
+
+hipError_t launch_pair(const Product &x, const Product &w, bool f16, const PairPlan &plan, float *partial,
+                       hipStream_t stream);
+
+// What a call launches, and the workspace that it needs.
+struct ForwardPlan {
+    bool rows;              // launch_rows
+    Plan tiles;
+    int64_t workspace() const { return rows ? 0 : tiles.workspace; }
+};
+struct BackwardPlan {
+    bool together;          // `both` where both gradients are wanted
+    PairPlan both;
+    Plan x, w;
+    int64_t workspace;
+};
+ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K);
+BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K);
+
 // The product of up to kMaxRows rows, in one launch without a workspace.
 constexpr int kMaxRows = 64;
 hipError_t launch_rows(const void *x, int64_t ldx, int M, const void *w, int N, int K, bool f16, const Epilogue &ep,

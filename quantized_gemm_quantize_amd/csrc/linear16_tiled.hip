@@ -271,18 +271,19 @@ __device__ __forceinline__ void short_stage(const uint4 *__restrict__ rd, const 
 // The largest of n, n / 2, n / 4 ... up to most.
 constexpr int rows_staged(int n, int most) { return n <= most ? n : rows_staged(n / 2, most); }
 
-template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC, bool KA, bool KB, bool TAIL>
-__global__ __launch_bounds__(GM *GN *kWave, GM *GN *OCC / 4) void tiled_kernel(const Tiles g) {
+// 16-byte slots of a workgroup's stages.
+template <int BM, int BN, int NB> constexpr int kSlots = NB * (BM + BN) * 8;
+
+// Workgroup `block` of a product.
+template <bool F16, int BM, int BN, int GM, int GN, int NB, bool KA, bool KB, bool TAIL>
+__device__ __forceinline__ void tile(const Tiles &g, const int block, uint4 *__restrict__ lds) {
     constexpr int WAVES = GM * GN, WM = BM / GM, WN = BN / GN, TM = WM / 16, TN = WN / 16;
     constexpr int STAGE = (BM + BN) * 8, BSLOT = BM * 8;   // 16-byte slots
-    __shared__ uint4 lds[NB * STAGE];
-    w8a8::lds_poison(lds);
-    w8a8::lds_poison_done();
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / GN, wn = wave % GN;
 
     // the whole tiles, then the parts of the others, each spread over the XCDs for themselves
-    const int block = blockIdx.x, tiles = g.tiles_m * g.tiles_n;
+    const int tiles = g.tiles_m * g.tiles_n;
     const bool split = block >= g.whole;
     const int stages = (int)((g.K + kStageK - 1) / kStageK);
     int t, unit = 0, s0 = 0, s1 = stages;
@@ -425,6 +426,32 @@ __global__ __launch_bounds__(GM *GN *kWave, GM *GN *OCC / 4) void tiled_kernel(c
     }
 }
 
+template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC, bool KA, bool KB, bool TAIL>
+__global__ __launch_bounds__(GM *GN *kWave, GM *GN *OCC / 4) void tiled_kernel(const Tiles g) {
+    __shared__ uint4 lds[kSlots<BM, BN, NB>];
+    w8a8::lds_poison(lds);
+    w8a8::lds_poison_done();
+    tile<F16, BM, BN, GM, GN, NB, KA, KB, TAIL>(g, blockIdx.x, lds);
+}
+
+// Both gradients in one launch: the workgroups of one fill the chip where those of the other leave it
+// idle at their end.
+struct Pair {
+    Tiles x, w;             // d_x and d_w
+    int x_first, w_first;   // their first workgroups
+    int w_blocks;
+};
+
+template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC, bool TX, bool TW>
+__global__ __launch_bounds__(GM *GN *kWave, GM *GN *OCC / 4) void pair_kernel(const Pair p) {
+    __shared__ uint4 lds[kSlots<BM, BN, NB>];
+    w8a8::lds_poison(lds);
+    w8a8::lds_poison_done();
+    const int w = (int)blockIdx.x - p.w_first;
+    if (w >= 0 && w < p.w_blocks) tile<F16, BM, BN, GM, GN, NB, true, true, TW>(p.w, w, lds);
+    else tile<F16, BM, BN, GM, GN, NB, false, true, TX>(p.x, (int)blockIdx.x - p.x_first, lds);
+}
+
 // The sums of the parts of the split tiles and the epilogue: 8 outputs per thread of the first
 // slice. SLICES slices of the parts are summed in order, then the slices.
 template <bool F16, int BM, int BN, int SLICES>
@@ -478,12 +505,36 @@ hipError_t launch_join(const Tiles &g, int tiles, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC, bool KA, bool KB>
-hipError_t launch(Tiles g, hipStream_t stream) {
+// Counts a product's tiles; the workgroups that they take.
+template <int BM, int BN>
+int blocks_of(Tiles &g) {
     g.tiles_m = (int)((g.M + BM - 1) / BM);
     g.tiles_n = (int)((g.N + BN - 1) / BN);
+    return g.whole + (g.tiles_m * g.tiles_n - g.whole) * g.splits;
+}
+
+template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC>
+hipError_t launch_both(Tiles x, Tiles w, bool w_first, hipStream_t stream) {
+    const int nx = blocks_of<BM, BN>(x), nw = blocks_of<BM, BN>(w);
+    const Pair p{x, w, w_first ? nw : 0, w_first ? 0 : nx, nw};
+    const dim3 grid((unsigned)(nx + nw)), block(GM * GN * kWave);
+    const bool tx = x.K % kStageK != 0, tw = w.K % kStageK != 0;
+    if (tx && tw) pair_kernel<F16, BM, BN, GM, GN, NB, OCC, true, true><<<grid, block, 0, stream>>>(p);
+    else if (tx) pair_kernel<F16, BM, BN, GM, GN, NB, OCC, true, false><<<grid, block, 0, stream>>>(p);
+    else if (tw) pair_kernel<F16, BM, BN, GM, GN, NB, OCC, false, true><<<grid, block, 0, stream>>>(p);
+    else pair_kernel<F16, BM, BN, GM, GN, NB, OCC, false, false><<<grid, block, 0, stream>>>(p);
+    hipError_t e = hipGetLastError();
+    for (const Tiles *g : {&x, &w}) {
+        const int shared = g->tiles_m * g->tiles_n - g->whole;
+        if (e == hipSuccess && shared) e = launch_join<F16, BM, BN>(*g, shared, stream);
+    }
+    return e;
+}
+
+template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC, bool KA, bool KB>
+hipError_t launch(Tiles g, hipStream_t stream) {
+    const dim3 grid((unsigned)blocks_of<BM, BN>(g)), block(GM * GN * kWave);
     const int tiles = g.tiles_m * g.tiles_n;
-    const dim3 grid((unsigned)(g.whole + (tiles - g.whole) * g.splits)), block(GM * GN * kWave);
     if (g.K % kStageK == 0) tiled_kernel<F16, BM, BN, GM, GN, NB, OCC, KA, KB, false><<<grid, block, 0, stream>>>(g);
     else tiled_kernel<F16, BM, BN, GM, GN, NB, OCC, KA, KB, true><<<grid, block, 0, stream>>>(g);
     hipError_t e = hipGetLastError();
@@ -503,6 +554,15 @@ hipError_t launch_form(const Tiles &g, int form, hipStream_t stream) {
 }
 
 template <bool F16>
+hipError_t launch_pair_form(const Tiles &x, const Tiles &w, int form, bool w_first, hipStream_t stream) {
+    switch (form) {
+        case k256x256: return launch_both<F16, 256, 256, 4, 2, 2, 1>(x, w, w_first, stream);
+        case k128x128: return launch_both<F16, 128, 128, 2, 4, 2, 2>(x, w, w_first, stream);
+        default: return launch_both<F16, 64, 64, 2, 2, 3, 3>(x, w, w_first, stream);
+    }
+}
+
+template <bool F16>
 hipError_t launch_type(const Tiles &g, int form, hipStream_t stream) {
     if (g.a.k_major) return launch_form<F16, true, true>(g, form, stream);
     return g.b.k_major ? launch_form<F16, false, true>(g, form, stream) : launch_form<F16, false, false>(g, form, stream);
@@ -514,6 +574,17 @@ hipError_t launch_tiled(const Operand &a, const Operand &b, int64_t M, int64_t N
                         float *partial, const Epilogue &ep, hipStream_t stream) {
     const Tiles g{a, b, M, N, K, 0, 0, plan.whole, plan.splits, partial, ep};
     return f16 ? launch_type<true>(g, plan.form, stream) : launch_type<false>(g, plan.form, stream);
+}
+
+hipError_t launch_pair(const Product &x, const Product &w, bool f16, const PairPlan &plan, float *partial,
+                       hipStream_t stream) {
+    auto tiles = [](const Product &p, const Plan &plan, float *partial) {
+        return Tiles{p.a, p.b, p.M, p.N, p.K, 0, 0, plan.whole, plan.splits, partial,
+                     Epilogue{nullptr, nullptr, 0, nullptr, p.out, act::kNone}};
+    };
+    const Tiles tx = tiles(x, plan.x, partial), tw = tiles(w, plan.w, partial + plan.x.workspace / 4);
+    return f16 ? launch_pair_form<true>(tx, tw, plan.x.form, plan.w_first, stream)
+               : launch_pair_form<false>(tx, tw, plan.x.form, plan.w_first, stream);
 }
 
 }  // namespace linear16

@@ -670,14 +670,22 @@ static w8a8_status linear16_shape(int64_t M, int64_t N, int64_t K) {
     return W8A8_OK;
 }
 
-// Not part of the interface (the tests ask it which sizes reach which kernel): of a 16-bit product, 10^6
-// for the kernel of few rows, otherwise the tiles' form * 10^5 + (whole tiles) * 10^4 + splits.
-int w16a16_debug_form(int64_t M, int64_t N, int64_t K, int forward) {
-    return linear16::debug_form(M, N, K, forward != 0);
+// Not part of the interface (the tests ask them which sizes reach which kernel): of a product of a 16-bit
+// layer (0 forward, 1 d_x, 2 d_w, 3 and 4 those in one launch, -1 without), 10^6 for the kernel of few rows,
+// otherwise the tiles' form * 10^5 + (whole tiles) * 10^4 + workgroups of the others.
+int w16a16_debug_form(int64_t M, int64_t N, int64_t K, int product) {
+    if (product == 0) {
+        const linear16::ForwardPlan p = linear16::plan_forward(M, N, K);
+        return p.rows ? 1000000 : p.tiles.form * 100000 + (p.tiles.whole > 0) * 10000 + p.tiles.splits;
+    }
+    const linear16::BackwardPlan p = linear16::plan_backward(M, N, K);
+    if (product > 2 && !p.together) return -1;
+    const linear16::Plan &t = product == 1 ? p.x : product == 2 ? p.w : product == 3 ? p.both.x : p.both.w;
+    return t.form * 100000 + (t.whole > 0) * 10000 + t.splits;
 }
 
 int64_t w16a16_linear_workspace(int64_t M, int64_t N, int64_t K) {
-    return linear16_shape(M, N, K) == W8A8_OK ? linear16::forward_workspace(M, N, K) : 0;
+    return linear16_shape(M, N, K) == W8A8_OK ? linear16::plan_forward(M, N, K).workspace() : 0;
 }
 
 w8a8_status w16a16_linear(const void *x, int64_t ldx, int64_t M, const void *w, int64_t N,
@@ -687,7 +695,8 @@ w8a8_status w16a16_linear(const void *x, int64_t ldx, int64_t M, const void *w, 
     if (w8a8_status s = linear16_shape(M, N, K)) return s;
     const int dt = selector(&dtype), a = selector(&activation);
     if ((dt != W4A16_BF16 && dt != W4A16_F16) || !act_ok(a)) return W8A8_ERR_DTYPE;
-    const int64_t need = linear16::forward_workspace(M, N, K);
+    const linear16::ForwardPlan plan = linear16::plan_forward(M, N, K);
+    const int64_t need = plan.workspace();
     if (ldx < K || ldx > INT_MAX || (residual && (ldr < N || ldr > INT_MAX)) || workspace_bytes < need)
         return W8A8_ERR_SHAPE;
     if (M == 0) return W8A8_OK;
@@ -696,12 +705,12 @@ w8a8_status w16a16_linear(const void *x, int64_t ldx, int64_t M, const void *w, 
         misaligned(pre) || misaligned(workspace) || ldx % 8 != 0 || (residual && ldr % 8 != 0))
         return W8A8_ERR_ALIGN;
     const linear16::Epilogue ep{bias, residual, ldr, pre, out, a};
-    return hip_status(linear16::launch_forward(x, ldx, M, w, N, K, dt == W4A16_F16, ep, workspace,
+    return hip_status(linear16::launch_forward(plan, x, ldx, M, w, N, K, dt == W4A16_F16, ep, workspace,
                                                static_cast<hipStream_t>(stream)));
 }
 
 int64_t w16a16_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
-    return linear16_shape(M, N, K) == W8A8_OK ? linear16::backward_workspace(M, N, K) : 0;
+    return linear16_shape(M, N, K) == W8A8_OK ? linear16::plan_backward(M, N, K).workspace : 0;
 }
 
 w8a8_status w16a16_linear_backward(const void *d_out, int64_t ldd, const void *x, int64_t ldx,
@@ -712,7 +721,8 @@ w8a8_status w16a16_linear_backward(const void *d_out, int64_t ldd, const void *x
     if (w8a8_status s = linear16_shape(M, N, K)) return s;
     const int dt = selector(&dtype), a = selector(&activation);
     if ((dt != W4A16_BF16 && dt != W4A16_F16) || !act_ok(a)) return W8A8_ERR_DTYPE;
-    const int64_t need = linear16::backward_workspace(M, N, K);
+    const linear16::BackwardPlan plan = linear16::plan_backward(M, N, K);
+    const int64_t need = plan.workspace;
     if (ldd < N || ldd > INT_MAX || ldx < K || ldx > INT_MAX || workspace_bytes < need)
         return W8A8_ERR_SHAPE;
     const bool slope = a != W8A8_ACT_NONE;
@@ -722,7 +732,7 @@ w8a8_status w16a16_linear_backward(const void *d_out, int64_t ldd, const void *x
         misaligned(d_x) || misaligned(d_w) || misaligned(d_bias) || misaligned(workspace) ||
         ldd % 8 != 0 || ldx % 8 != 0)
         return W8A8_ERR_ALIGN;
-    return hip_status(linear16::launch_backward(d_out, ldd, x, ldx, w, pre, M, N, K, dt == W4A16_F16, a,
+    return hip_status(linear16::launch_backward(plan, d_out, ldd, x, ldx, w, pre, M, N, K, dt == W4A16_F16, a,
                                                 d_pre, d_x, d_w, d_bias, workspace,
                                                 static_cast<hipStream_t>(stream)));
 }

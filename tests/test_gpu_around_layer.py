@@ -271,6 +271,20 @@ def test_lds_poisoned_tiles(M, N, K):
     assert all(torch.equal(a, c) for a, c in zip(got, want))
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 992, 8), (982, 8, 8), (8, 8, 8), (128, 2328, 1000), (1964, 72, 1240), (2008, 1816, 2144),
+                                   (1343, 7600, 656), (934, 776, 4808), (3855, 1000, 2272)])
+def test_lds_poisoned_gradients(M, N, K):
+    """Both in one launch."""
+    g = torch.Generator(device=DEV).manual_seed(K)
+    d, x, w = (torch.randn(s, generator=g, device=DEV).to(torch.bfloat16) for s in ((M, N), (M, K), (N, K)))
+    want = binding.w16a16_linear_backward(d, x, w)
+    torch.cuda.synchronize()
+    with library(POISON_LIB) as poisoned:
+        got = poisoned.w16a16_linear_backward(d, x, w)
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("H", [520, 1031, 5000, 9000, 9001, 16384])
 def test_gradients_in_place(dtype, H):

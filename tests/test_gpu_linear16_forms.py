@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import block_reference as ref
-from linear16_sizes import ROWS, TILED
+from linear16_sizes import PAIRS, ROWS, TILED
 from quantized_gemm_quantize_amd import binding as b
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +65,19 @@ def test_gradients(dtype, M, N, K):
     close(got, *product(d.t(), x.t()), dtype, "d_w")
     again = b.w16a16_linear_backward(d, x, torch.empty((M, N), dtype=TYPES[dtype], device=DEV), d_x=False, d_bias=False)[1]
     assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("M,N,K", PAIRS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_both_gradients(dtype, M, N, K):
+    """In one launch, against 64 bits and against one by one."""
+    g = torch.Generator(device=DEV).manual_seed(M + 3 * N + K)
+    d, x, w = rows(g, M, N, dtype, N ** -0.5), rows(g, M, K, dtype), rows(g, N, K, dtype, extra=0)
+    need = b.w16a16_linear_backward_workspace(M, N, K)
+    work = torch.full((need + 4096,), 77, dtype=torch.uint8, device=DEV)
+    d_x, d_w, d_bias, _ = b.w16a16_linear_backward(d, x, w, workspace=work[:need])
+    assert (work[need:] == 77).all()
+    close(d_x, *product(d, w.t()), dtype, "d_x")
+    close(d_w, *product(d.t(), x.t()), dtype, "d_w")
+    again = b.w16a16_linear_backward(d, x, w)
+    assert torch.equal(d_x, again[0]) and torch.equal(d_w, again[1]) and torch.equal(d_bias, again[2])

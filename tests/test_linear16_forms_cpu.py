@@ -4,7 +4,7 @@ import re
 
 import pytest
 
-from linear16_sizes import FORMS, ROWS, TILED, form
+from linear16_sizes import D_W, D_X, FORMS, PAIR_D_W, PAIR_D_X, PAIRS, ROWS, TILED, form
 from quantized_gemm_quantize_amd import binding, build
 
 
@@ -18,8 +18,9 @@ def lib():
 def test_every_tile_is_reached(lib):
     text = open(os.path.join(build.CSRC, "linear16_tiled.hip")).read()
     assert len(set(re.findall(r"return launch<F16, (\d+, \d+, \d, \d, \d), \d, KA, KB>", text))) == FORMS
-    for forward in (True, False):
-        reached = {form(lib, *size, forward) for size in TILED}
+    # as the forward product, as d_x of a layer of that inner axis, as d_w of one of as many rows
+    for reached in ({form(lib, *size) for size in TILED}, {form(lib, m, k, n, D_X) for m, n, k in TILED},
+                    {form(lib, k, m, n, D_W) for m, n, k in TILED}):
         assert {r[0] for r in reached} == set(range(FORMS))
         for f in range(FORMS):
             for tail in (False, True):
@@ -28,11 +29,21 @@ def test_every_tile_is_reached(lib):
                 assert f == 0 or (f, True, True, tail) in reached
 
 
-def test_gradients_reach_every_tile_too(lib):
-    """The same three sizes as (rows, inner, channels) and (channels, inner, rows) of a layer's gradients."""
-    for m, n, k in TILED:
-        assert m % 8 == n % 8 == k % 8 == 0
-        assert lib.w16a16_linear_backward_workspace(m, k, n) >= 0
+def test_every_tile_of_both_gradients_is_reached(lib):
+    text = open(os.path.join(build.CSRC, "linear16_tiled.hip")).read()
+    both = text[text.index("hipError_t launch_pair_form("):text.index("hipError_t launch_type(")]
+    assert len(re.findall(r"return launch_both<F16, ", both)) == 3
+    reached = {(form(lib, *size, PAIR_D_X), form(lib, *size, PAIR_D_W), size[0] >= size[1]) for size in PAIRS}
+    assert all(x and w and x[0] == w[0] for x, w, _ in reached)
+    for f in (0, 2, 4):
+        for first in (False, True):      # d_w first, of more rows than channels
+            for tx in (False, True):
+                for tw in (False, True):
+                    of = {(x[1:3], w[1:3]) for x, w, order in reached if (x[0], x[3], w[3], order) == (f, tx, tw, first)}
+                    assert ((True, False), (True, False)) in of, (f, first, tx, tw)
+            of = {(x[1:3], w[1:3]) for x, w, order in reached if (x[0], order) == (f, first)}
+            assert any((w if first else x) == (False, True) for x, w in of)      # the first one's tiles shared
+            assert f == 0 or any((x if first else w) == (True, True) for x, w in of)   # the second one's last
 
 
 def test_few_rows(lib):
