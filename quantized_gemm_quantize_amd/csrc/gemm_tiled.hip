@@ -401,7 +401,7 @@ __global__ __launch_bounds__(kThreads, OCC) void gemm_tiled_kernel(
                 }
             __syncthreads();
             // kAhead rows' residuals are on their way while as many rows are finished
-            constexpr int kTurns = kPass * (WN / 8) / kWave, kAhead = 4;
+            constexpr int kTurns = kPass * (WN / 8) / kWave, kAhead = kTurns < 4 ? kTurns : 4;
             static_assert(kTurns % kAhead == 0, "whole groups of turns");
             auto row_of = [&](int it) { return it * (kWave / (WN / 8)) + lane / (WN / 8); };
             auto residual_of = [&](int it) {
@@ -505,16 +505,22 @@ __global__ __launch_bounds__(kThreads, OCC) void gemm_tiled_kernel(
     }
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int CPR, int OCC, bool KTAIL>
+enum Use { kAll, kActOnly, kNoAct };
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int CPR, int OCC, bool KTAIL, Use USE>
 void launch_tail(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
                  int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
                  const ActEpilogue *ep) {
     const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
     const dim3 grid((unsigned)(tiles_m * tiles_n)), block(kThreads);
     const Addmm a = am ? *am : Addmm{nullptr, 1.0f, 0.0f};
-    if (ep)
-        gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, false, kAct>
-            <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, tiles_m, tiles_n, *ep);
+    if constexpr (USE != kNoAct)
+        if (ep) {
+            gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, false, kAct>
+                <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, tiles_m, tiles_n, *ep);
+            return;
+        }
+    if constexpr (USE == kActOnly) return;
     else if (out_i32)
         gemm_tiled_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, KTAIL, true, kPlain>
             <<<grid, block, 0, stream>>>(xq, xs, wq, ws, out, M, N, K, tiles_m, tiles_n, a);
@@ -527,16 +533,16 @@ void launch_tail(const int8_t *xq, const float *xs, int M, const int8_t *wq, con
 }
 
 // K not a multiple of the stage depth takes the variant that zeroes the
-// chunks past K.
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int CPR = 8, int OCC = 1>
+// chunks past K. USE: the epilogues that it carries.
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int CPR = 8, int OCC = 1, Use USE = kAll>
 hipError_t launch_cfg(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
                       int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
                       const ActEpilogue *ep) {
     if (K % (16 * CPR) == 0)
-        launch_tail<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, false>(xq, xs, M, wq, ws, N, K, out,
+        launch_tail<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, false, USE>(xq, xs, M, wq, ws, N, K, out,
                                                                        out_i32, stream, am, ep);
     else
-        launch_tail<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, true>(xq, xs, M, wq, ws, N, K, out,
+        launch_tail<BM, BN, WAVES_M, WAVES_N, STAGES, CPR, OCC, true, USE>(xq, xs, M, wq, ws, N, K, out,
                                                                       out_i32, stream, am, ep);
     return hipGetLastError();
 }
@@ -550,6 +556,14 @@ hipError_t launch_gemm_decode(const int8_t *xq, const float *xs, int M, const in
 static hipError_t launch_any(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
                              int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
                              const ActEpilogue *ep) {
+    // With the activation's epilogue: 64 x 64 tiles, three workgroups per CU, where one round holds them all,
+    // and for 33 to 64 rows where the streaming kernel reads many channels again for each group of rows
+    // (64 x 64 / otherwise, us: 65 x 4096 x 4096 10.4 / 23.3, 256 x 1344 x 5840 17.9 / 38.8, 256 x 11008
+    // x 4096 21.6 / 32.5, 633 x 288 x 272 5.2 / 10.7; 64 rows, 4096 x 4096 10.3 / 13.1, 11008 x 4096 16.5 /
+    // 36.4, 2176 x 8064 16.0 / 22.7, but 1344 x 5840 17.3 / 13.2 and 4096 x 11008 34.7 / 31.8).
+    const long t64 = (long)((M + 63) / 64) * ((N + 63) / 64);
+    if (ep && ((M > 64 && t64 <= 3 * 256) || (M > 32 && M <= 64 && N >= 2048 && K <= 8192)))
+        return launch_cfg<64, 64, 2, 2, 3, 8, 3, kActOnly>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     if (M <= 64) return launch_gemm_decode(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     // Many tiles (enough 256x256 ones to fill 256 CUs four times over): with
     // K up to 1024, two 256x128 workgroups per CU (64-byte K stages, 72 KB of
@@ -563,7 +577,9 @@ static hipError_t launch_any(const int8_t *xq, const float *xs, int M, const int
         return launch_cfg<256, 128, 2, 2, 3, 4, 2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     if (t256 >= 4 * 256) return launch_cfg<256, 256, 2, 2, 2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     if (t128 >= 256) return launch_cfg<256, 128, 2, 2, 3>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
-    return launch_cfg<128, 128, 2, 2, 2>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+    // two 128 x 64 tiles per CU (1024 x 4096 x 4096 26.5 us, 128 x 128 tiles 33.4; 4096 x 1024 x 4096 26.8 / 33.0)
+    if (ep) return launch_cfg<128, 64, 2, 2, 3, 8, 2, kActOnly>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+    return launch_cfg<128, 128, 2, 2, 2, 8, 1, kNoAct>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
 }
 
 hipError_t launch_gemm(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
