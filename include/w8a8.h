@@ -489,7 +489,7 @@ w8a8_status mxfp4_moe(const void *x, int64_t ldx, mxfp4_dtype dtype, int64_t T, 
 
 /* Activations of the epilogues, computed in fp32: v; max(v, 0); v P(v) with P the
  * normal distribution function; the tanh form of it, v (1 + tanh(sqrt(2 / pi) (v +
- * 0.044715 v^3))) / 2; v / (1 + exp(-v)). */
+ * 0.044715 v^3))) / 2; v / (1 + exp(-v)). Infinite v give their limits. */
 typedef enum {
     W8A8_ACT_NONE = 0,
     W8A8_ACT_RELU = 1,

@@ -953,8 +953,8 @@ def _norm_operands(residual, weight, y, post_norm, post_weight, gate, scale, eps
     dtype = residual.dtype
     w = _vector(weight, "weight", H)
     if y is None:
-        if gate is not None or post_norm or post_weight is not None:
-            raise ValueError("gate and post norm need y")
+        if gate is not None or post_norm or post_weight is not None or new_residual is not None:
+            raise ValueError("gate, post norm and new_residual need y")
         s = _current(residual, stream, weight, *outputs)
         return (residual.data_ptr(), ld, None, 0, 0, None, None, 0, scale, w, eps, T, H, code, None), residual, s
     y_at, ldy = _like_rows(y, "y", dtype, (T, H))

@@ -15,6 +15,8 @@
 // P(-a) = e^(-a^2/2) t Q(t), t = 1 / (1 + 0.28 a): a minimax fit of the
 // scaled complementary error function over a >= 0 (relative error 1.7e-7), so
 // gelu keeps its precision in the lower tail, where (1 + erf) / 2 has none left.
+// Infinite v give the limits (0 on the left, v on the right; slopes 0 and 1), NaN gives NaN (relu's
+// slope 0): factors that meet an exponential of 0 are bounded first.
 #pragma once
 
 #include "common.hpp"
@@ -34,12 +36,12 @@ struct Decay {
     }
 };
 
-// s(x) * u and, with `other`, 1 - s(x).
+// s(x) * u (u of x's sign, or positive) and, with `other`, 1 - s(x).
 __device__ __forceinline__ float sigmoid_times(float x, float u, float &other) {
     const Decay d(-__builtin_fabsf(x));
     const float r = __builtin_amdgcn_rcpf(1.0f + d.e);
     other = x < 0 ? r : d.e * r;
-    return x < 0 ? u * d.big * r * 0x1p-32f : u * r;
+    return x < 0 ? fmaxf(u, -0x1p64f) * d.big * r * 0x1p-32f : u * r;
 }
 
 // z(v) of the tanh form; an infinite cube keeps its sign.
@@ -70,7 +72,7 @@ __device__ __forceinline__ float value(float v) {
     if constexpr (A == kSilu) return sigmoid_times(v, v, unused);
     if constexpr (A == kGeluTanh) return sigmoid_times(tanh_argument(v), v, unused);
     if constexpr (A == kGelu) {
-        const float a = __builtin_fabsf(v);
+        const float a = fminf(__builtin_fabsf(v), 64.0f);   // the tail ends before
         const float tail = a * lower_tail_big(a, Decay(-0.5f * a * a)) * 0x1p-32f;
         return v < 0 ? -tail : v - tail;
     }
@@ -83,7 +85,7 @@ __device__ __forceinline__ float slope(float v) {
     if constexpr (A == kSilu) {
         float other;
         const float s = sigmoid_times(v, 1.0f, other);
-        return __builtin_fmaf(v * s, other, s);
+        return s == 0.0f || other == 0.0f ? s : __builtin_fmaf(v * s, other, s);
     }
     if constexpr (A == kGeluTanh) {
         constexpr float c = 1.59576912160573071f, c3 = 3 * 0.044715f * c;
@@ -97,8 +99,8 @@ __device__ __forceinline__ float slope(float v) {
         constexpr float density = 0.398942280401432678f;  // 1 / sqrt(2 pi)
         const float a = __builtin_fabsf(v);
         const Decay d(-0.5f * a * a);
-        const float tail = lower_tail_big(a, d) * 0x1p-32f;
-        return __builtin_fmaf(v * density, d.e, v < 0 ? tail : 1.0f - tail);
+        const float tail = lower_tail_big(a, d) * 0x1p-32f, p = v < 0 ? tail : 1.0f - tail;
+        return d.e == 0.0f ? p : __builtin_fmaf(v * density, d.e, p);
     }
     return 1.0f;
 }

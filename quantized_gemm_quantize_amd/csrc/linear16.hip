@@ -296,7 +296,7 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K) {
     const Estimate x = estimate(M, K, N);
     const PairEstimate both = estimate_pair(M, N, K);
     p.x = x.plan;
-    p.together = both.us < x.us + w.us + 2.0;
+    p.together = both.us >= 0 && both.us < x.us + w.us + 2.0;
     p.both = both.plan;
     p.workspace = std::max(p.workspace, p.x.workspace);   // (the column sums are done before the products)
     if (p.together) p.workspace = std::max(p.workspace, p.both.x.workspace + p.both.w.workspace);

@@ -93,7 +93,7 @@ def test_arguments(calls):  # noqa: F811
         (b.w16a16_linear_backward, (rows, x, w), dict(d_x=rows)), (b.w16a16_linear_backward, (rows, x, w), dict(d_bias=v)),
         (b.block_norm, (x, gpu(255, dtype=F32)), {}), (b.block_norm, (x, gpu(256, dtype=BF16)), {}),
         (b.block_norm, (x,), dict(gate=v)), (b.block_norm, (x,), dict(post_norm=True)), (b.block_norm, (x,), dict(post_weight=v)),
-        (b.block_norm, (x,), dict(y=rows)), (b.block_norm, (x,), dict(y=gpu(8, 256, dtype=F16))),
+        (b.block_norm, (x,), dict(new_residual=x)), (b.block_norm, (x,), dict(y=rows)), (b.block_norm, (x,), dict(y=gpu(8, 256, dtype=F16))),
         (b.block_norm, (x,), dict(y=x, gate=gpu(8, 256, dtype=F32))), (b.block_norm, (x,), dict(y=x, gate=gpu(8, dtype=F32))),
         (b.block_norm, (x,), dict(out=gpu(8, 256, dtype=F32))), (b.block_norm, (gpu(8, 256, dtype=torch.float64),), {}),
         (b.block_norm_w8a8, (x,), dict(xq=x)), (b.block_norm_mxfp4, (x,), dict(scales=gpu(2, 8, 8, dtype=torch.uint8))),

@@ -172,6 +172,25 @@ def test_not_finite():
         assert not (out[:, 5].isfinite() & (out[:, 5] != 0)).any()   # -inf times a negative slope is 0
 
 
+@pytest.mark.parametrize("M", [3, 100])
+@pytest.mark.parametrize("a", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_activations_at_infinity(a, M):
+    """Limits of values and slopes, also where only the square or the cube leaves the range; NaN stays."""
+    t = torch.bfloat16
+    inf, big = float("inf"), 2.0 ** 100
+    x, w = torch.zeros((M, 8), dtype=t, device=DEV), torch.zeros((8, 8), dtype=t, device=DEV)
+    bias = torch.tensor([inf, -inf, big, -big, float("nan"), 0.0, 80.0, -200.0], device=DEV)
+    out, pre = b.w16a16_linear(x, w, bias=bias, activation=a, pre=True)
+    xq, ones = torch.zeros((M, 16), dtype=torch.int8, device=DEV), torch.ones(16, device=DEV)
+    out8 = b.w8a8_gemm_act(xq, torch.ones(M, device=DEV), xq[:1].repeat(16, 1), ones, bias=bias.repeat(2), activation=a)
+    d = b.w16a16_linear_backward(torch.ones_like(pre), x, w, pre=pre, activation=a)[3]
+    for got in (out, out8[:, :8], out8[:, 8:]):
+        assert (got[:, [0, 2, 6]] == torch.tensor([inf, big, 80.0], device=DEV)).all()
+        assert (got[:, [1, 3, 5, 7]] == 0).all() and got[:, 4].isnan().all()
+    assert (d[:, [0, 2, 6]] == 1).all() and (d[:, [1, 3, 7]] == 0).all()
+    assert a == "relu" or d[:, 4].isnan().all()
+
+
 # ------------------------------------------------------------------ the int8 product's epilogue
 
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (1, 512, 4096), (7, 272, 1312), (16, 1040, 4096), (16, 272, 8192),
