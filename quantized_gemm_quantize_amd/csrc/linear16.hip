@@ -35,7 +35,8 @@ constexpr FormTime kTimes[kForms] = {
     {128, 128, 256, 4.8, 0.40, 0.49}, // k128x128deep
     {128, 128, 512, 4.0, 0.64, 0.90}, // k128x128
     {256, 128, 256, 6.0, 0.63, 0.82}, // k256x128
-    {256, 256, 256, 10.0, 1.10, 1.41} // k256x256
+    {256, 256, 256, 10.0, 1.10, 1.41},// k256x256
+    {64, 64, 256, 4.2, 0.12, 0.15}    // k64x64deep
 };
 
 double round_time(const FormTime &f, int64_t units, int64_t stages) {
@@ -80,19 +81,15 @@ Estimate estimate(int64_t M, int64_t N, int64_t K) {
     return best;
 }
 
-struct PairEstimate {
-    PairPlan plan;
-    double us;
-};
-
 // The plan with the least estimated time for both gradients in one launch. The product of the longer k goes
 // first, its tiles whole or all of them shared by s workgroups; the other's tiles follow on workgroup
 // slots as they come free, whole, or whole up to the end of one of their rounds and the rest shared.
 // With p slots free from `from` on, q from `later` on (a round of the first product more), and
 // `each` a tile: the rounds that hold n tiles, and the tiles done at a time.
-PairEstimate estimate_pair(int64_t M, int64_t N, int64_t K) {
-    PairEstimate best{{}, -1};
+PairPlan estimate_pair(int64_t M, int64_t N, int64_t K) {
     const bool w_first = M >= N;
+    PairPlan best{{k64x64, (int)(ceil_div(M, 64) * ceil_div(K, 64)), 1, 0}, {k64x64, (int)(ceil_div(N, 64) * ceil_div(K, 64)), 1, 0}, w_first};
+    double least = -1;
     // rows, columns and stages of the first product and the second
     const int64_t rows[2] = {w_first ? N : M, w_first ? M : N}, stages[2] = {ceil_div(w_first ? M : N, 64), ceil_div(w_first ? N : M, 64)};
     for (const Form form : {k64x64, k128x128, k256x256}) {
@@ -110,11 +107,12 @@ PairEstimate estimate_pair(int64_t M, int64_t N, int64_t K) {
                 return p * (int64_t)std::max(0.0, (t - from) / each + 1e-9) + q * (int64_t)std::max(0.0, (t - later) / each + 1e-9);
             };
             auto offer = [&](double us, int64_t whole, int64_t splits) {
-                if (best.us >= 0 && us >= best.us) return;
+                if (least >= 0 && us >= least) return;
+                least = us;
                 const int64_t bytes = (int64_t)f.bm * f.bn * 4;
                 const Plan a{form, s > 1 ? 0 : (int)first, (int)s, s > 1 ? units * bytes : 0};
                 const Plan b{form, (int)whole, (int)splits, (second - whole) * splits * bytes};
-                best = w_first ? PairEstimate{{b, a, true}, us} : PairEstimate{{a, b, false}, us};
+                best = w_first ? PairPlan{b, a, true} : PairPlan{a, b, false};
             };
             // ends after k rounds from `from` on (some before `later`), or from `later` on
             const int64_t early = ceil_div(second, p);
@@ -137,7 +135,8 @@ PairEstimate estimate_pair(int64_t M, int64_t N, int64_t K) {
 
 // The kernel of few rows: up to 16 rows always (1 x 4096 x 4096 5.8 us against 13 in tiles), up to 64
 // where it is estimated to be quicker: 3 us and both operands of a workgroup at 65 GB/s a round
-// (64 rows: 4096 x 4096 11.7 us against 13.0, 8192 x 2048 14.9 / 12.2, 4096 x 11008 32.7 / 23.7).
+// (64 rows: 1024 x 1024 5.2 us against 7.5, 4096 x 4096 12.7 / 13.4, 8192 x 2048 15.6 / 10.5, 4096 x 11008
+// 33.7 / 23.5, 11008 x 4096 36.3 / 18.9; 24 rows of 4096 x 4096 9.7 / 10.9).
 // Otherwise, the plan in tiles.
 bool few_rows(int64_t M, int64_t N, int64_t K, Plan &plan) {
     if (M <= 16) return true;
@@ -284,22 +283,17 @@ ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K) {
     return p;
 }
 
-// Both gradients in one launch where that is estimated to be quicker than one after the other, with 2 us
-// between them: 257 x 1040 x 1312 with silu 20.2 -> 14.0 us in all, 3611 x 304 x 1024 34.7 -> 29.7,
-// 16448 x 5120 x 1280 525 -> 484.
+// Both gradients, where both are wanted, in one launch: at 24 random sizes whose separate launches were estimated to be
+// quicker it took 0.66 to 1.04 of their time (257 x 1040 x 1312 with silu 20.2 -> 14.0 us in all, 3428 x 512 x 4688
+// 76.7 -> 59.7, 16448 x 5120 x 1280 525 -> 484; 6 x 3424 x 9600 39.3 -> 40.8).
 BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K) {
     BackwardPlan p{};
-    const Estimate w = estimate(N, K, M);
-    p.w = w.plan;
-    p.workspace = std::max(sums_bytes(M, N), p.w.workspace);
+    p.w = estimate(N, K, M).plan;
+    p.workspace = std::max(sums_bytes(M, N), p.w.workspace);   // (the column sums are done before the products)
     if (!M) return p;
-    const Estimate x = estimate(M, K, N);
-    const PairEstimate both = estimate_pair(M, N, K);
-    p.x = x.plan;
-    p.together = both.us >= 0 && both.us < x.us + w.us + 2.0;
-    p.both = both.plan;
-    p.workspace = std::max(p.workspace, p.x.workspace);   // (the column sums are done before the products)
-    if (p.together) p.workspace = std::max(p.workspace, p.both.x.workspace + p.both.w.workspace);
+    p.x = estimate(M, K, N).plan;
+    p.both = estimate_pair(M, N, K);
+    p.workspace = std::max({p.workspace, p.x.workspace, p.both.x.workspace + p.both.w.workspace});
     return p;
 }
 
@@ -321,7 +315,7 @@ hipError_t launch_backward(const BackwardPlan &plan, const void *d_out, int64_t 
     }
     const Operand rows{a == act::kNone ? d_out : d_pre, a == act::kNone ? ldd : N, false};
     const Operand weight{w, K, true}, columns{rows.p, rows.ld, true}, inputs{x, ldx, true};
-    if (d_x && d_w && plan.together)
+    if (d_x && d_w && M)
         return launch_pair({rows, weight, M, K, N, d_x}, {columns, inputs, N, K, M, d_w}, f16, plan.both, partial, stream);
     auto plain = [](void *out) { return Epilogue{nullptr, nullptr, 0, nullptr, out, act::kNone}; };
     if (d_x && M) e = launch_tiled(rows, weight, M, K, N, f16, plan.x, partial, plain(d_x), stream);

@@ -26,7 +26,7 @@ struct Operand {
 
 // The tiles of a product, how many of them (the first ones in the tile order) one workgroup computes
 // whole, and how many workgroups share each other one along k.
-enum Form { k64x64, k128x128deep, k128x128, k256x128, k256x256, kForms };
+enum Form { k64x64, k128x128deep, k128x128, k256x128, k256x256, k64x64deep, kForms };
 struct Plan {
     Form form;
     int whole, splits;
@@ -58,9 +58,8 @@ struct ForwardPlan {
     int64_t workspace() const { return rows ? 0 : tiles.workspace; }
 };
 struct BackwardPlan {
-    bool together;          // `both` where both gradients are wanted
-    PairPlan both;
-    Plan x, w;
+    PairPlan both;          // where both gradients are wanted
+    Plan x, w;              // of one alone
     int64_t workspace;
 };
 ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K);

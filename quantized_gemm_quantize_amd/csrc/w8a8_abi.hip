@@ -671,7 +671,7 @@ static w8a8_status linear16_shape(int64_t M, int64_t N, int64_t K) {
 }
 
 // Not part of the interface (the tests ask them which sizes reach which kernel): of a product of a 16-bit
-// layer (0 forward, 1 d_x, 2 d_w, 3 and 4 those in one launch, -1 without), 10^6 for the kernel of few rows,
+// layer (0 forward, 1 d_x, 2 d_w, 3 and 4 those in one launch), 10^6 for the kernel of few rows,
 // otherwise the tiles' form * 10^5 + (whole tiles) * 10^4 + workgroups of the others.
 int w16a16_debug_form(int64_t M, int64_t N, int64_t K, int product) {
     if (product == 0) {
@@ -679,7 +679,6 @@ int w16a16_debug_form(int64_t M, int64_t N, int64_t K, int product) {
         return p.rows ? 1000000 : p.tiles.form * 100000 + (p.tiles.whole > 0) * 10000 + p.tiles.splits;
     }
     const linear16::BackwardPlan p = linear16::plan_backward(M, N, K);
-    if (product > 2 && !p.together) return -1;
     const linear16::Plan &t = product == 1 ? p.x : product == 2 ? p.w : product == 3 ? p.both.x : p.both.w;
     return t.form * 100000 + (t.whole > 0) * 10000 + t.splits;
 }

@@ -67,24 +67,24 @@ SIZES = [dict(M=-1), dict(M=2 ** 27), dict(M=2 ** 62), dict(N=0), dict(N=-8), di
 
 
 def test_linear(lib):
-    base = dict(x=P, ldx=2 ** 20, M=300, w=P, N=40, K=1024, dt=0, bias=P, act=1, residual=P, ldr=2 ** 20, pre=P, out=P,
+    base = dict(x=P, ldx=2 ** 20, M=300, w=P, N=40, K=8192, dt=0, bias=P, act=1, residual=P, ldr=2 ** 20, pre=P, out=P,
                 work=P, size=1 << 40, stream=None)
     c = caller(lib.w16a16_linear, base)
     for size in SIZES:
         assert c(**size) == SHAPE, size
         assert lib.w16a16_linear_workspace(*[size.get(n, base[n]) for n in "MNK"]) == 0
-    need = lib.w16a16_linear_workspace(300, 40, 1024)
+    need = lib.w16a16_linear_workspace(300, 40, 8192)
     assert need > 0 and c(size=need - 1) == SHAPE and c(size=-1) == SHAPE
     assert c(dt=2) == DTYPE and c(dt=-1) == DTYPE and c(act=5) == DTYPE and c(act=-1) == DTYPE
-    assert c(ldx=1016) == SHAPE and c(ldx=2 ** 31) == SHAPE and c(ldx=1028) == ALIGN
+    assert c(ldx=1016) == SHAPE and c(ldx=2 ** 31) == SHAPE and c(ldx=8196) == ALIGN
     assert c(ldr=32) == SHAPE and c(ldr=2 ** 31) == SHAPE and c(ldr=44) == ALIGN
     for n in ("x", "w", "out", "work"):
         assert c(**{n: 0}) == NULL
     for n in ("x", "w", "out", "work", "bias", "residual", "pre"):
         assert c(**{n: P + 8}) == ALIGN
     # one row has no workspace, and asks for none
-    assert lib.w16a16_linear_workspace(1, 40, 1024) == 0 and c(M=1, work=0, size=0, out=0) == NULL
-    assert lib.w16a16_linear_workspace(0, 40, 1024) == 0
+    assert lib.w16a16_linear_workspace(1, 40, 8192) == 0 and c(M=1, work=0, size=0, out=0) == NULL
+    assert lib.w16a16_linear_workspace(0, 40, 8192) == 0
     assert c(M=0, x=0, w=0, out=0, residual=0, bias=0, pre=0, work=0, size=0) == OK
 
 

@@ -184,7 +184,7 @@ def test_captured(T):
 def test_two_graphs_share_a_workspace():
     """One workspace for two captured products with shared tiles and a norm's gradient: replayed in turn on one stream,
     each finds its own partial sums."""
-    M, N, K = 72, 8, 1024
+    M, N, K = 72, 8, 4096
     sets = []
     work = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
     need = [binding.w16a16_linear_workspace(M, N, K), binding.w16a16_linear_backward_workspace(600, N, K),
@@ -251,7 +251,7 @@ def test_lds_poisoned_norms(dtype, H):
         assert torch.equal(a.reshape(-1).view(torch.uint8), c.reshape(-1).view(torch.uint8))
 
 
-@pytest.mark.parametrize("M,N,K", [(72, 8, 1024), (1608, 1944, 200), (1280, 720, 5640), (2192, 1352, 136), (3064, 2480, 1792),
+@pytest.mark.parametrize("M,N,K", [(72, 8, 1024), (72, 8, 328), (200, 136, 3368), (768, 1408, 5080), (1608, 1944, 200), (1280, 720, 5640), (2192, 1352, 136), (3064, 2480, 1792),
                                    (2456, 3216, 344), (1504, 3536, 9544)])
 def test_lds_poisoned_tiles(M, N, K):
     g = torch.Generator(device=DEV).manual_seed(K)
@@ -271,7 +271,7 @@ def test_lds_poisoned_tiles(M, N, K):
     assert all(torch.equal(a, c) for a, c in zip(got, want))
 
 
-@pytest.mark.parametrize("M,N,K", [(2, 992, 8), (982, 8, 8), (8, 8, 8), (128, 2328, 1000), (1964, 72, 1240), (2008, 1816, 2144),
+@pytest.mark.parametrize("M,N,K", [(2, 992, 8), (331, 2224, 8), (333, 8, 8), (3547, 4744, 72), (982, 8, 8), (8, 8, 8), (128, 2328, 1000), (1964, 72, 1240), (2008, 1816, 2144),
                                    (1343, 7600, 656), (934, 776, 4808), (3855, 1000, 2272)])
 def test_lds_poisoned_gradients(M, N, K):
     """Both in one launch."""
