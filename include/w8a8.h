@@ -522,7 +522,8 @@ w8a8_status w8a8_gemm_act(const int8_t *xq, const float *x_scale, int64_t M, con
  * itself (with ldr = N). N and K positive multiples of 8 up to W16A16_MAX_WIDTH, M < 2^27,
  * M * N, M * K and N * K at most 2^35.
  * Few rows or few tiles of a long K are split over K and joined in a workspace: device,
- * 16-byte aligned, at least w16a16_linear_workspace(M, N, K) bytes (may be 0: then NULL).
+ * 16-byte aligned, at least w16a16_linear_workspace(M, N, K) bytes (may be 0: then NULL; 0 for up
+ * to 16 rows).
  * Errors: NULL, SHAPE (also a workspace that is too small), ALIGN (rows included: 2 * ld
  *         % 16), DTYPE (dtype, activation), HIP.
  */

@@ -870,7 +870,7 @@ def w16a16_linear(x, w, bias=None, activation="none", residual=None, pre=None, o
     out = _result(out, "out", (M, N), x.dtype, x, stream)
     lib = load()
     work, address, size = None, None, 0
-    need = lib.w16a16_linear_workspace(M, N, K)
+    need = 0 if M <= 16 else lib.w16a16_linear_workspace(M, N, K)
     if need or workspace is not None:
         work = _scratch(workspace, need, x, stream)
         address, size = work.data_ptr(), work.shape[0]

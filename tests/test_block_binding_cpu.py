@@ -22,8 +22,10 @@ def entries():
     x, w, rows, v = gpu(8, 256, dtype=BF16), gpu(64, 256, dtype=BF16), gpu(8, 64, dtype=BF16), gpu(256, dtype=F32)
     q = gpu(8, 256, dtype=I8), gpu(8, dtype=F32), gpu(64, 256, dtype=I8), gpu(64, dtype=F32)
     yield b.w8a8_gemm_act, q, dict(bias=gpu(64, dtype=F32), residual=rows), 1
-    yield b.w16a16_linear, (x, w), dict(activation="silu"), 2
-    yield b.w16a16_linear, (x, w), dict(activation="gelu", pre=True, residual=rows), 3
+    many = gpu(40, 256, dtype=BF16), w
+    yield b.w16a16_linear, (x, w), dict(activation="silu"), 1      # up to 16 rows need no workspace
+    yield b.w16a16_linear, many, dict(activation="silu"), 2
+    yield b.w16a16_linear, many, dict(activation="gelu", pre=True, residual=gpu(40, 64, dtype=BF16)), 3
     yield b.w16a16_linear_backward, (rows, x, w), dict(), 4
     yield b.w16a16_linear_backward, (rows, x, w), dict(pre=rows, activation="relu", d_x=False), 4
     yield b.block_norm, (x,), dict(), 1

@@ -70,3 +70,18 @@ def test_workspaces_hold_the_shared_tiles(lib):
         rest = tiles % slots if whole else tiles
         assert need % (4 * tile[f] * rest) == 0 and 2 <= need // (4 * tile[f] * rest) <= 64
         assert lib.w16a16_linear_workspace(m, n, k + 4) == 0      # a refused size
+
+
+def test_plans_of_the_largest_and_smallest_sizes(lib):
+    """Every plan has whole numbers of tiles and a workspace that fits the sums it needs, up to the limits."""
+    sizes = [(1, 8, 8), (16, 2 ** 20, 2 ** 15), (17, 8, 8), (2 ** 27 - 1, 8, 8), (2 ** 27 - 1, 256, 256), (2 ** 15, 2 ** 20, 8),
+             (2 ** 15, 8, 2 ** 20), (2 ** 15, 2 ** 20, 2 ** 15), (17, 2 ** 20, 2 ** 15), (64, 2 ** 15, 2 ** 20), (2 ** 20, 2 ** 15, 2 ** 15)]
+    for m, n, k in sizes:
+        forward = lib.w16a16_linear_workspace(m, n, k)
+        assert 0 <= forward <= 2 ** 31 and (m > 16 or forward == 0)
+        assert 0 <= lib.w16a16_linear_backward_workspace(m, n, k) <= 2 ** 31
+        assert form(lib, m, n, k) is not None
+        for product in (D_X, D_W, PAIR_D_X, PAIR_D_W):
+            f, whole, shared, _ = form(lib, m, n, k, product)
+            assert 0 <= f < FORMS and (whole or shared), (m, n, k, product)
+        assert form(lib, m, n, k, PAIR_D_X)[0] == form(lib, m, n, k, PAIR_D_W)[0]
