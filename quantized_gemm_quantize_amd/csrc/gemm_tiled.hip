@@ -39,6 +39,7 @@
 #include "activation.hpp"
 #include "common.hpp"
 #include "launch.hpp"
+#include "linear16.hpp"
 
 namespace w8a8 {
 namespace {
@@ -556,13 +557,18 @@ hipError_t launch_gemm_decode(const int8_t *xq, const float *xs, int M, const in
 static hipError_t launch_any(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
                              int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
                              const ActEpilogue *ep) {
-    // With the activation's epilogue: 64 x 64 tiles, three workgroups per CU, where one round holds them all,
-    // and for 33 to 64 rows where the streaming kernel reads many channels again for each group of rows
-    // (64 x 64 / otherwise, us: 65 x 4096 x 4096 10.4 / 23.3, 256 x 1344 x 5840 17.9 / 38.8, 256 x 11008
-    // x 4096 21.6 / 32.5, 633 x 288 x 272 5.2 / 10.7; 64 rows, 4096 x 4096 10.3 / 13.1, 11008 x 4096 16.5 /
-    // 36.4, 2176 x 8064 16.0 / 22.7, but 1344 x 5840 17.3 / 13.2 and 4096 x 11008 34.7 / 31.8).
+    // With the activation's epilogue: 64 x 64 tiles, three workgroups per CU, where one round holds them all, and for
+    // 33 to 64 rows of many channels, which the streaming kernel reads again for each group of rows (64 x 64 /
+    // otherwise, us: 65 x 4096 x 4096 10.4 / 23.3, 256 x 11008 x 4096 21.6 / 32.5, 633 x 288 x 272 5.2 / 10.7; 64
+    // rows, 4096 x 4096 10.3 / 13.1, 11008 x 4096 16.5 / 36.4, but 1344 x 5840 17.3 / 13.2).
     const long t64 = (long)((M + 63) / 64) * ((N + 63) / 64);
-    if (ep && ((M > 64 && t64 <= 3 * 256) || (M > 32 && M <= 64 && N >= 2048 && K <= 8192)))
+    // A tile per CU at most and a long K: wavefronts that take stages of their own (that / the tiles above or the
+    // streaming kernel: 128 x 1344 x 5840 12.1 / 17.6, 256 x 2176 x 8064 15.9 / 26.3, 128 x 4096 x 11008 20.7 /
+    // 34.5, 64 x 11008 x 4096 12.1 / 16.5, 24 x 11008 x 4096 10.7 / 18.6, but 400 x 4096 x 4096 18.7 / 14.7,
+    // 256 x 1024 x 1024 6.2 / 5.8 and 24 x 4096 x 4096 9.0 / 8.0).
+    if (ep && t64 <= 256 && K >= 4096 && (M > 32 || (M > 16 && N >= 8192)))
+        return linear16::launch_int8(xq, xs, M, wq, ws, N, K, {ep->bias, ep->residual, ep->ldr, nullptr, out, ep->act}, stream);
+    if (ep && ((M > 64 && t64 <= 3 * 256) || (M > 32 && M <= 64 && N >= 2048 && K >= 2048 && K <= 8192)))
         return launch_cfg<64, 64, 2, 2, 3, 8, 3, kActOnly>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     if (M <= 64) return launch_gemm_decode(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     // Many tiles (enough 256x256 ones to fill 256 CUs four times over): with

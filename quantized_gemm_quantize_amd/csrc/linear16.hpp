@@ -36,6 +36,11 @@ struct Plan {
 hipError_t launch_tiled(const Operand &a, const Operand &b, int64_t M, int64_t N, int64_t K, bool f16, const Plan &plan,
                         float *partial, const Epilogue &ep, hipStream_t stream);
 
+// The int8 product (bf16 outputs, whole tiles of the wavefronts that take stages of their own), K a
+// multiple of 16; its sums are scaled by rows and channels before the epilogue.
+hipError_t launch_int8(const int8_t *xq, const float *x_scale, int64_t M, const int8_t *wq, const float *w_scale, int64_t N,
+                       int64_t K, const Epilogue &ep, hipStream_t stream);
+
 // d_x and d_w in one launch: plain products of one form, b k-major, a of w too. The workgroups of one
 // come first.
 struct Product {

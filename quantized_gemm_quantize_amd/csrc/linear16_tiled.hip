@@ -28,10 +28,13 @@
 //    tiles in a workspace, which join_kernel adds in order and finishes.
 //  - Tiles are assigned XCD-contiguously, in groups of 8 tile rows, so that tiles that
 //    run at once share operand rows in the same L2.
+#include <type_traits>
+
 #include "activation.hpp"
 #include "launch.hpp"
 #include "linear16.hpp"
 #include "linear16_mfma.hpp"
+#include "quant_math.hpp"
 #include "rows.hpp"
 
 namespace linear16 {
@@ -138,6 +141,16 @@ struct Fragments {
     }
 };
 
+// What a product multiplies. Rows of int8 are taken as 16-bit rows of half their length: their loads,
+// LDS slots and fragments are the same bytes, and the MFMA of 64 int8 k takes them as the others take 32.
+enum Kind { kKindBf16, kKindF16, kKindInt8 };
+
+template <int KIND, typename A>
+__device__ __forceinline__ A multiply_add(v4i a, v4i b, A c) {
+    if constexpr (KIND == kKindInt8) return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+    else return mfma<KIND == kKindF16>(a, b, c);
+}
+
 struct Tiles {
     Operand a, b;
     int64_t M, N, K;
@@ -146,6 +159,7 @@ struct Tiles {
     int splits;             // workgroups of each other tile
     float *partial;         // their sums: [tile - whole][split][BM][BN]
     Epilogue ep;
+    const float *x_scale, *w_scale;   // int8: of the rows, of the channels
 };
 
 // The first row and column of tile t: in groups of 8 tile rows.
@@ -277,9 +291,9 @@ __device__ __forceinline__ v4i first_elements(v4i f, int valid) {
 
 // The products of a stage of k_left < 64 k, outside the pipeline: what lies past them counts as 0 on both
 // sides, whatever was read there.
-template <bool F16, int TM, int TN, int BM, typename FA, typename FB>
+template <int KIND, int TM, int TN, int BM, typename FA, typename FB, typename A>
 __device__ __forceinline__ void short_stage(const uint4 *__restrict__ rd, const FA &fa, const FB &fb, int k_left, int lane,
-                                            v4f (&acc)[TM][TN]) {
+                                            A (&acc)[TM][TN]) {
 #pragma unroll
     for (int kk = 0; kk < kSteps; ++kk) {
         const int valid = k_left - kStep * kk - 8 * (lane >> 4);
@@ -290,7 +304,7 @@ __device__ __forceinline__ void short_stage(const uint4 *__restrict__ rd, const 
         for (int i = 0; i < TM; ++i) {
             const v4i x = first_elements(fa.read(rd, i, kk), valid);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<F16>(w[j], x, acc[i][j]);
+            for (int j = 0; j < TN; ++j) acc[i][j] = multiply_add<KIND>(w[j], x, acc[i][j]);
         }
     }
 }
@@ -445,12 +459,12 @@ __device__ __forceinline__ void tile(const Tiles &g, const int block, uint4 *__r
 // The tile of 64 x 64 where few of them leave CUs idle: each of 4 wavefronts takes the whole tile over every
 // fourth stage, through two buffers of its own, so no barrier stands in its loop and a stage's chain of load, LDS
 // read and MFMA runs four times beside itself (257 x 1040 x 1312, 85 tiles of 21 stages: 10.8 -> 9.6 us; 300 x 2048 x
-// 2048 13.3 -> 10.4; with 512 tiles of 64 stages 33.1 against 29.1). The four sums
+// 2048 13.3 -> 10.4; with 512 tiles of 64 stages 33.1 against 29.1; int8 256 x 2176 x 8064 26.3 -> 15.9). The four sums
 // are added in LDS in order.
 constexpr int kDeepWaves = 4, kDeepBuffers = 2, kDeepStage = (64 + 64) * 8, kDeepSlots = kDeepWaves * kDeepBuffers * kDeepStage;
 
-template <bool F16, typename FA, typename FB>
-__device__ __forceinline__ void whole_stage(const uint4 *__restrict__ rd, const FA &fa, const FB &fb, v4f (&acc)[4][4]) {
+template <int KIND, typename FA, typename FB, typename A>
+__device__ __forceinline__ void whole_stage(const uint4 *__restrict__ rd, const FA &fa, const FB &fb, A (&acc)[4][4]) {
     v4i x[kSteps][4], w[kSteps][4];
 #pragma unroll
     for (int kk = 0; kk < kSteps; ++kk)
@@ -464,7 +478,7 @@ __device__ __forceinline__ void whole_stage(const uint4 *__restrict__ rd, const 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mfma<F16>(w[kk][j], x[kk][i], acc[i][j]);
+            for (int j = 0; j < 4; ++j) acc[i][j] = multiply_add<KIND>(w[kk][j], x[kk][i], acc[i][j]);
 }
 
 // A wavefront's own loads and LDS reads: all but the last N loads have landed; all reads are done.
@@ -475,7 +489,7 @@ __device__ __forceinline__ void wait_loads() {
 }
 __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-template <bool F16, bool KA, bool KB, bool TAIL>
+template <int KIND, bool KA, bool KB, bool TAIL>
 __device__ __forceinline__ void deep_tile(const Tiles &g, const int block, uint4 *__restrict__ lds) {
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const Place place(g, block, 64, 64);
@@ -485,11 +499,12 @@ __device__ __forceinline__ void deep_tile(const Tiles &g, const int block, uint4
     Fragments<KB, 64, 4> fb;
     fa.init(0, lane);
     fb.init(0, lane);
-    v4f acc[4][4];
+    typedef typename std::conditional<KIND == kKindInt8, v4i, v4f>::type Sum;
+    Sum acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = v4f{};
+        for (int j = 0; j < 4; ++j) acc[i][j] = Sum{};
 
     Loads<KA, 64, 1> la;
     Loads<KB, 64, 1> lb;
@@ -520,7 +535,7 @@ __device__ __forceinline__ void deep_tile(const Tiles &g, const int block, uint4
         } else {
             wait_loads<0>();
         }
-        short_stage<F16, 4, 4, 64>(mine, fa, fb, k_left, lane, acc);
+        short_stage<KIND, 4, 4, 64>(mine, fa, fb, k_left, lane, acc);
         wait_reads();
         if (count > 1) issue(0);
         at = 1;
@@ -532,7 +547,7 @@ __device__ __forceinline__ void deep_tile(const Tiles &g, const int block, uint4
     for (int i = 0; i < count; ++i) {
         if (i + 1 < count) wait_loads<NLD>();
         else wait_loads<0>();
-        whole_stage<F16>(mine + at * kDeepStage, fa, fb, acc);
+        whole_stage<KIND>(mine + at * kDeepStage, fa, fb, acc);
         wait_reads();   // before its buffer is filled again
         if (i + 2 < count) issue(at);
         at ^= 1;
@@ -550,13 +565,19 @@ __device__ __forceinline__ void deep_tile(const Tiles &g, const int block, uint4
         const int64_t m = place.m0 + row0 + 32 * h;
         residual[h] = residual_at(g.ep, m, n, !place.split && m < g.M && n < g.N);
     }
-    float4 *const sums = reinterpret_cast<float4 *>(mine);   // (this wavefront's reads are done)
+    float w_scale[8], x_scale[2];
+    if constexpr (KIND == kKindInt8) {
+        rows::load_vector<kBf16, true>(g.w_scale, (int)n, (int)g.N, 0.0f, w_scale);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x_scale[h] = g.x_scale[min(place.m0 + row0 + 32 * h, g.M - 1)];
+    }
+    Sum *const sums = reinterpret_cast<Sum *>(mine);   // (this wavefront's reads are done)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int row = 16 * i + (lane & 15);
-            sums[row * CH + ((j * 4 + (lane >> 4)) ^ (row & PM))] = __builtin_bit_cast(float4, acc[i][j]);
+            sums[row * CH + ((j * 4 + (lane >> 4)) ^ (row & PM))] = acc[i][j];
         }
     __syncthreads();
 #pragma unroll
@@ -564,33 +585,38 @@ __device__ __forceinline__ void deep_tile(const Tiles &g, const int block, uint4
         const int row = row0 + 32 * h;
         const int64_t m = place.m0 + row;
         if (m >= g.M || n >= g.N) continue;
-        float v[8];
+        Sum sum[2];
 #pragma unroll
         for (int w = 0; w < kDeepWaves; ++w)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const float4 f = reinterpret_cast<const float4 *>(lds + w * kDeepBuffers * kDeepStage)[row * CH + ((col / 4 + q) ^ (row & PM))];
-                v[4 * q] = w ? v[4 * q] + f.x : f.x;
-                v[4 * q + 1] = w ? v[4 * q + 1] + f.y : f.y;
-                v[4 * q + 2] = w ? v[4 * q + 2] + f.z : f.z;
-                v[4 * q + 3] = w ? v[4 * q + 3] + f.w : f.w;
+                const Sum f = reinterpret_cast<const Sum *>(lds + w * kDeepBuffers * kDeepStage)[row * CH + ((col / 4 + q) ^ (row & PM))];
+                sum[q] = w ? sum[q] + f : f;
             }
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (KIND == kKindInt8)
+                v[e] = w8a8::dequant(sum[e / 4][e % 4], w8a8::split_scale(x_scale[h]), w8a8::split_scale(w_scale[e]));
+            else
+                v[e] = sum[e / 4][e % 4];
+        }
         if (place.split) {
             float4 *to = reinterpret_cast<float4 *>(g.partial + ((int64_t)place.unit * 64 + row) * 64 + col);
             to[0] = make_float4(v[0], v[1], v[2], v[3]);
             to[1] = make_float4(v[4], v[5], v[6], v[7]);
         } else {
-            finish<F16, true>(v, bias, residual[h], g.ep, g.N, m, n);
+            finish<KIND == kKindF16, true>(v, bias, residual[h], g.ep, g.N, m, n);
         }
     }
 }
 
-template <bool F16, bool KA, bool KB, bool TAIL>
+template <int KIND, bool KA, bool KB, bool TAIL>
 __global__ __launch_bounds__(kDeepWaves *kWave, 1) void deep_kernel(const Tiles g) {
     __shared__ uint4 lds[kDeepSlots];
     w8a8::lds_poison(lds);
     w8a8::lds_poison_done();
-    deep_tile<F16, KA, KB, TAIL>(g, blockIdx.x, lds);
+    deep_tile<KIND, KA, KB, TAIL>(g, blockIdx.x, lds);
 }
 
 template <bool F16, int BM, int BN, int GM, int GN, int NB, int OCC, bool KA, bool KB, bool TAIL>
@@ -708,14 +734,14 @@ hipError_t launch(Tiles g, hipStream_t stream) {
     return e != hipSuccess || !shared ? e : launch_join<F16, BM, BN>(g, shared, stream);
 }
 
-template <bool F16, bool KA, bool KB>
+template <int KIND, bool KA, bool KB>
 hipError_t launch_deep(Tiles g, hipStream_t stream) {
     const dim3 grid((unsigned)blocks_of<64, 64>(g)), block(kDeepWaves * kWave);
-    if (g.K % kStageK == 0) deep_kernel<F16, KA, KB, false><<<grid, block, 0, stream>>>(g);
-    else deep_kernel<F16, KA, KB, true><<<grid, block, 0, stream>>>(g);
+    if (g.K % kStageK == 0) deep_kernel<KIND, KA, KB, false><<<grid, block, 0, stream>>>(g);
+    else deep_kernel<KIND, KA, KB, true><<<grid, block, 0, stream>>>(g);
     const hipError_t e = hipGetLastError();
     const int shared = g.tiles_m * g.tiles_n - g.whole;
-    return e != hipSuccess || !shared ? e : launch_join<F16, 64, 64>(g, shared, stream);
+    return e != hipSuccess || !shared ? e : launch_join<KIND == kKindF16, 64, 64>(g, shared, stream);
 }
 
 template <bool F16, bool KA, bool KB>
@@ -749,15 +775,23 @@ hipError_t launch_type(const Tiles &g, int form, hipStream_t stream) {
 
 hipError_t launch_tiled(const Operand &a, const Operand &b, int64_t M, int64_t N, int64_t K, bool f16, const Plan &plan,
                         float *partial, const Epilogue &ep, hipStream_t stream) {
-    const Tiles g{a, b, M, N, K, 0, 0, plan.whole, plan.splits, partial, ep};
+    const Tiles g{a, b, M, N, K, 0, 0, plan.whole, plan.splits, partial, ep, nullptr, nullptr};
     return f16 ? launch_type<true>(g, plan.form, stream) : launch_type<false>(g, plan.form, stream);
+}
+
+hipError_t launch_int8(const int8_t *xq, const float *x_scale, int64_t M, const int8_t *wq, const float *w_scale, int64_t N,
+                       int64_t K, const Epilogue &ep, hipStream_t stream) {
+    const int64_t half = K / 2;
+    const int tiles = (int)((M + 63) / 64 * ((N + 63) / 64));
+    return launch_deep<kKindInt8, false, false>(Tiles{{xq, half, false}, {wq, half, false}, M, N, half, 0, 0, tiles, 1, nullptr,
+                                                      ep, x_scale, w_scale}, stream);
 }
 
 hipError_t launch_pair(const Product &x, const Product &w, bool f16, const PairPlan &plan, float *partial,
                        hipStream_t stream) {
     auto tiles = [](const Product &p, const Plan &plan, float *partial) {
         return Tiles{p.a, p.b, p.M, p.N, p.K, 0, 0, plan.whole, plan.splits, partial,
-                     Epilogue{nullptr, nullptr, 0, nullptr, p.out, act::kNone}};
+                     Epilogue{nullptr, nullptr, 0, nullptr, p.out, act::kNone}, nullptr, nullptr};
     };
     const Tiles tx = tiles(x, plan.x, partial), tw = tiles(w, plan.w, partial + plan.x.workspace / 4);
     return f16 ? launch_pair_form<true>(tx, tw, plan.x.form, plan.w_first, stream)

@@ -12,9 +12,9 @@ from quantized_gemm_quantize_amd.build import POISON_LIB
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
-# 64 x 64 tiles (a round of them, and 33 to 64 rows of many channels), 128 x 64, 256 x 128 at one and at two workgroups
+# 64 x 64 tiles (a round of them, and 33 to 64 rows of many channels; wavefronts with stages of their own), 128 x 64, 256 x 128 at one and at two workgroups
 # per CU, 256 x 256, the streaming kernels
-SIZES = [(65, 144, 528), (300, 1040, 1024), (40, 2064, 400), (64, 2048, 1024), (33, 11008, 4096), (1100, 3008, 272), (1000, 4096, 256),
+SIZES = [(64, 2064, 2064), (50, 2048, 2048), (300, 1040, 4112), (256, 2048, 4096), (20, 8208, 4096), (65, 16, 8208), (65, 144, 528), (300, 1040, 1024), (40, 2064, 400), (64, 2048, 1024), (33, 11008, 4096), (1100, 3008, 272), (1000, 4096, 256),
          (4100, 2064, 400), (4096, 2048, 1024), (8200, 8208, 272), (8200, 8208, 256), (8200, 8208, 1040), (8192, 8192, 1152),
          (1, 4096, 4096), (16, 272, 8192), (24, 2064, 1040), (48, 1040, 1024), (64, 4096, 8208)]
 
