@@ -856,7 +856,7 @@ def w16a16_linear(x, w, bias=None, activation="none", residual=None, pre=None, o
     or both float16; bias float32 [N]; residual of x's dtype [M,N] (rows may lie apart), which may be `out`
     itself. pre: True or a tensor for x w^T + bias too, which the gradient of an activation needs; the result
     is (out, pre) then. workspace: uint8 of at least w16a16_linear_workspace(M, N, K) bytes (a new one if
-    None)."""
+    None); up to 16 rows a smaller one will do, in a longer time."""
     a = _activation(activation)
     code, ld, M, N, K = _linear16_operands(x, w)
     b = _vector(bias, "bias", N)
@@ -870,7 +870,8 @@ def w16a16_linear(x, w, bias=None, activation="none", residual=None, pre=None, o
     out = _result(out, "out", (M, N), x.dtype, x, stream)
     lib = load()
     work, address, size = None, None, 0
-    need = 0 if M <= 16 else lib.w16a16_linear_workspace(M, N, K)
+    # (none up to these sizes)
+    need = 0 if M <= 16 and N <= 4096 and K <= 8192 else lib.w16a16_linear_workspace(M, N, K)
     if need or workspace is not None:
         work = _scratch(workspace, need, x, stream)
         address, size = work.data_ptr(), work.shape[0]

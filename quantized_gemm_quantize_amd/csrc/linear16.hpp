@@ -72,6 +72,8 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K);
 
 // The product of up to kMaxRows rows, in one launch without a workspace.
 constexpr int kMaxRows = 64;
+// Up to so many rows a call may leave its workspace out: launch_rows stands for any other plan.
+constexpr int kNoWorkspaceRows = 16;
 hipError_t launch_rows(const void *x, int64_t ldx, int M, const void *w, int N, int K, bool f16, const Epilogue &ep,
                        hipStream_t stream);
 

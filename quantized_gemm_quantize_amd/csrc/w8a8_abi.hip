@@ -694,7 +694,8 @@ w8a8_status w16a16_linear(const void *x, int64_t ldx, int64_t M, const void *w, 
     if (w8a8_status s = linear16_shape(M, N, K)) return s;
     const int dt = selector(&dtype), a = selector(&activation);
     if ((dt != W4A16_BF16 && dt != W4A16_F16) || !act_ok(a)) return W8A8_ERR_DTYPE;
-    const linear16::ForwardPlan plan = linear16::plan_forward(M, N, K);
+    linear16::ForwardPlan plan = linear16::plan_forward(M, N, K);
+    if (M <= linear16::kNoWorkspaceRows && workspace_bytes >= 0 && workspace_bytes < plan.workspace()) plan.rows = true;
     const int64_t need = plan.workspace();
     if (ldx < K || ldx > INT_MAX || (residual && (ldr < N || ldr > INT_MAX)) || workspace_bytes < need)
         return W8A8_ERR_SHAPE;
