@@ -10,7 +10,7 @@
 // activation rows, of 8 chunks, chunk c of row r at slot c ^ swz(r) as in linear16_tiled.hip.
 // The wavefronts' partial tiles are summed in LDS in a fixed order; a thread then finishes four
 // consecutive channels of a row.
-// Measured: 1 x 4096 x 4096 5.8 us (5.8 TB/s of weights), 64 x 4096 x 4096 12.7: there the rows' own
+// Measured: 1 x 4096 x 4096 5.8 us (5.8 TB/s of weights), 64 x 4096 x 2048 9.0: there the rows' own
 // loads are four times the weights'.
 #include "activation.hpp"
 #include "launch.hpp"

@@ -50,3 +50,15 @@ def test_a_workspace_may_be_left_out_up_to_16_rows(lib, M, N, K):
         assert c(size=size) == NULL and c(size=size, work=P) == NULL
     assert c(size=-1) == SHAPE and c(size=need, out=P) == NULL      # a size without an address
     assert c(size=need, work=P + 8, out=P) == ALIGN and c(size=16, work=P + 8, out=P) == ALIGN
+
+
+# weights that tiles read no faster than memory gives them, a part of a round at a time (streaming kernel / tiles, us): 16.8 /
+# 20.1, 17.5 / 20.3, 18.0 / 20.5, 39.5 / 45.8, 43.7 / 46.7
+FROM_MEMORY = [(17, 4096, 8192), (24, 4096, 8192), (32, 4096, 8192), (17, 8192, 11008), (24, 8192, 11008)]
+
+
+def test_17_to_64_rows(lib):
+    for size in [*FROM_MEMORY, (24, 4096, 4096), (64, 1024, 1024), (64, 4096, 1024), (24, 1024, 2048)]:
+        assert form(lib, *size) == ROWS and lib.w16a16_linear_workspace(*size) == 0, size
+    for size in [(64, 4096, 8192), (64, 4096, 11008), (64, 8192, 2048), (64, 11008, 4096), (24, 256, 8192), (24, 16384, 8192)]:
+        assert form(lib, *size) != ROWS, size
