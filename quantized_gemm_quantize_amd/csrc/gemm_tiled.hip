@@ -554,22 +554,38 @@ hipError_t launch_gemm_decode(const int8_t *xq, const float *xs, int M, const in
                               const float *ws, int N, int K, void *out, bool out_i32,
                               hipStream_t stream, const Addmm *am, const ActEpilogue *ep);
 
+// The kernel of a product with the activation's epilogue (that / the quickest of the others, us, each pass on operands of
+// its own).
+//  - Wavefronts that take stages of their own, for a tile of 64 x 64 per CU at most and a long K (128 x 1344 x 5840 17.3 /
+//    21.5, 256 x 2176 x 8064 17.9 / 31.0, 128 x 4096 x 11008 28.6 / 46.2, 64 x 4096 x 4096 10.3 / 14.6, 64 x 11008 x 4096
+//    15.9 / 24.1, 24 x 11008 x 4096 13.0 / 20.8, but 400 x 4096 x 4096 19.9 / 17.1 and 24 x 4096 x 4096 9.1 / 8.9), for 33
+//    to 64 rows of many channels from K = 2048 on (64 x 4096 x 2048 8.0 / 8.8, 48 x 2048 x 3584 9.4 / 11.2, 33 x 16384 x
+//    2048 10.8 / 14.8, but 33 x 2048 x 2048 7.6 / 6.5).
+//  - 64 x 64 tiles, three workgroups per CU, where one round holds them all (633 x 288 x 272 5.3 / 7.5, 400 x 4096 x 4096
+//    17.1 / 17.5, 256 x 11008 x 4096 31.7 / 32.7, but 1024 x 4096 x 4096, 1024 tiles, 36.5 / 27.6), and for 17 to 64
+//    rows of more than 16384 channels: the streaming kernel reads those again for each group of 16 rows (64 rows, that /
+//    streaming: 32000 x 11008 87 / 257, 16640 x 8208 70 / 130, 32000 x 1024 12.2 / 39.7; 17 rows: 32000 x 2048 17.6 / 25.4,
+//    16400 x 64 5.6 / 5.9).
+//  - Otherwise the kernel of the product without it: streaming up to 64 rows, larger tiles.
+ActForm act_form(int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = (M + 63) / 64 * ((N + 63) / 64);
+    const bool decode = M > 32 && M <= 64;
+    if (tiles <= 256 && ((K >= 4096 && (M > 32 || (M > 16 && N >= 8192))) || (decode && K >= 2048 && N >= 2048)))
+        return kActOwnStages;
+    if (M > 64 ? tiles <= 3 * 256 : M > 16 && tiles > 256) return kAct64x64;
+    return M <= 64 ? kActStreaming : kActTiles;
+}
+
 static hipError_t launch_any(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
                              int N, int K, void *out, bool out_i32, hipStream_t stream, const Addmm *am,
                              const ActEpilogue *ep) {
-    // With the activation's epilogue: 64 x 64 tiles, three workgroups per CU, where one round holds them all, and for
-    // 33 to 64 rows of many channels, which the streaming kernel reads again for each group of rows (64 x 64 /
-    // otherwise, us: 65 x 4096 x 4096 10.4 / 23.3, 256 x 11008 x 4096 21.6 / 32.5, 633 x 288 x 272 5.2 / 10.7; 64
-    // rows, 4096 x 4096 10.3 / 13.1, 11008 x 4096 16.5 / 36.4, but 1344 x 5840 17.3 / 13.2).
-    const long t64 = (long)((M + 63) / 64) * ((N + 63) / 64);
-    // A tile per CU at most and a long K: wavefronts that take stages of their own (that / the tiles above or the
-    // streaming kernel: 128 x 1344 x 5840 12.1 / 17.6, 256 x 2176 x 8064 15.9 / 26.3, 128 x 4096 x 11008 20.7 /
-    // 34.5, 64 x 11008 x 4096 12.1 / 16.5, 24 x 11008 x 4096 10.7 / 18.6, but 400 x 4096 x 4096 18.7 / 14.7,
-    // 256 x 1024 x 1024 6.2 / 5.8 and 24 x 4096 x 4096 9.0 / 8.0).
-    if (ep && t64 <= 256 && K >= 4096 && (M > 32 || (M > 16 && N >= 8192)))
-        return linear16::launch_int8(xq, xs, M, wq, ws, N, K, {ep->bias, ep->residual, ep->ldr, nullptr, out, ep->act}, stream);
-    if (ep && ((M > 64 && t64 <= 3 * 256) || (M > 32 && M <= 64 && N >= 2048 && K >= 2048 && K <= 8192)))
-        return launch_cfg<64, 64, 2, 2, 3, 8, 3, kActOnly>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+    if (ep) {
+        const ActForm form = act_form(M, N, K);
+        if (form == kActOwnStages)
+            return linear16::launch_int8(xq, xs, M, wq, ws, N, K, {ep->bias, ep->residual, ep->ldr, nullptr, out, ep->act}, stream);
+        if (form == kAct64x64)
+            return launch_cfg<64, 64, 2, 2, 3, 8, 3, kActOnly>(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
+    }
     if (M <= 64) return launch_gemm_decode(xq, xs, M, wq, ws, N, K, out, out_i32, stream, am, ep);
     // Many tiles (enough 256x256 ones to fill 256 CUs four times over): with
     // K up to 1024, two 256x128 workgroups per CU (64-byte K stages, 72 KB of

@@ -22,13 +22,15 @@ hipError_t launch_gemm(const int8_t *xq, const float *xs, int M, const int8_t *w
                        const Addmm *am = nullptr);
 
 // Epilogue act(acc * sa * sb + bias[n]) + residual[m, n] (bias and residual may be null; act an
-// act::Activation), and the product with it, on the same kernels.
+// act::Activation), and the product with it: on the same kernels, or on tiles of its own.
 struct ActEpilogue {
     const float *bias;
     const void *residual;  // bf16 rows, row stride ldr
     int64_t ldr;
     int act;
 };
+enum ActForm { kActStreaming, kActOwnStages, kAct64x64, kActTiles };
+ActForm act_form(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_act(const int8_t *xq, const float *xs, int M, const int8_t *wq, const float *ws,
                            int N, int K, void *out, const ActEpilogue &ep, hipStream_t stream);
 

@@ -661,6 +661,9 @@ w8a8_status w8a8_gemm_act(const int8_t *xq, const float *x_scale, int64_t M, con
                                             static_cast<hipStream_t>(stream)));
 }
 
+// Not part of the interface (the tests ask it which sizes reach which kernel).
+int w8a8_act_debug_form(int64_t M, int64_t N, int64_t K) { return w8a8::act_form(M, N, K); }
+
 static w8a8_status linear16_shape(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || M >= (1 << 27) || N <= 0 || K <= 0 || N % 8 != 0 || K % 8 != 0 ||
         N > W16A16_MAX_WIDTH || K > W16A16_MAX_WIDTH)
