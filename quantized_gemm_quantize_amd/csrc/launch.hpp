@@ -156,9 +156,6 @@ namespace block {
 struct Forward;
 struct Backward;
 
-// Row widths that stay in registers.
-constexpr int kMaxH = 16384;
-
 // The block norm (norm.hpp's arguments; dtype 0 bf16, 1 binary16, 2 binary32;
 // out 0 rows of dtype, 1 int8 rows, 2 MXFP4 rows) and its gradients.
 hipError_t launch_forward(const Forward &a, int dtype, int out, hipStream_t stream);

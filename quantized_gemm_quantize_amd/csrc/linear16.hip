@@ -53,8 +53,8 @@ struct Estimate {
 // workgroup; the rest's tiles are shared along k by as many workgroups as run at once (at least
 // two stages each), whose partial sums a second launch joins (3 us and their bytes at 4.5 TB/s).
 // What splitting the rest is worth: 16448 x 5120 x 1280 (1300 tiles of 256 x 256, 1280 of them in five
-// rounds) 207 -> 193 us, 16448 x 1280 x 5120 (325 tiles) 218 -> 181; 257 x 1040 x 1312 (85 tiles of
-// 64 x 64, three workgroups each) 12.8 -> 10.4.
+// rounds) 218 -> 203 us, 16448 x 1280 x 5120 (325 tiles) 221 -> 207; 64 x 4096 x 8192 (64 tiles of 64 x 64, four
+// workgroups each) 37.6 -> 21.7, 300 x 72 x 8200 (10 tiles, twelve each) 34.6 -> 10.5.
 Estimate estimate(int64_t M, int64_t N, int64_t K) {
     Estimate best{{k64x64, 0, 1, 0}, -1};
     const int64_t stages = ceil_div(K, 64);

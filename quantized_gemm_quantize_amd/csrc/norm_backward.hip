@@ -14,9 +14,10 @@
 // keeps its threads' columns of the sums over rows in registers (fp32); at its
 // end they go to partial[b], and a second kernel adds the G partials of each
 // column in a fixed order, so repeated runs agree bit for bit.
-// Bound by HBM: five (six with a gate row) reads and two (three) writes of
-// T x H elements. Measured: 8192 x 4096 bf16 with post norm and gate rows 94 us (5.7 TB/s),
-// 16448 x 1280 with a gate vector 65 us (3.9 TB/s), 4096 x 8192 109 us (3.7); a single row 5 us.
+// Bound by HBM: four reads (d_o, d_new, r', y; five with a gate row) and two (three) writes of
+// T x H elements. Measured, both kernels: 8192 x 4096 bf16 with post norm and gate rows 91 us (5.9 TB/s), in
+// 32 bits 189 (5.7), 16448 x 1280 bf16 with a gate vector 64 us (3.9), 4096 x 8192 105 (3.8), 1000 x 16384 110 (1.8:
+// its rows are read three times, and 250 partial sums of three vectors joined); a single row 5 us.
 #include <algorithm>
 
 #include "launch.hpp"

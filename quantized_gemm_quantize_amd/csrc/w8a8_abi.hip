@@ -742,7 +742,8 @@ w8a8_status w16a16_linear_backward(const void *d_out, int64_t ldd, const void *x
 
 // Sizes, type and scalars of a block norm.
 static w8a8_status norm_shape(int64_t T, int64_t H) {
-    // workgroups of up to 1024 threads per row above 4096 elements, 256 below
+    // above 512 rows, a row of up to 512 elements has at most 64 threads and a longer one (128 to 1024 by type and
+    // width) fewer than H / 4: less than 2^30 and 2^32 threads in all
     if (T < 0 || T >= (1 << 24) || H <= 0 || H > BLOCK_NORM_MAX_H || T * H > ((int64_t)1 << 34))
         return W8A8_ERR_SHAPE;
     return W8A8_OK;
