@@ -523,8 +523,9 @@ w8a8_status w8a8_gemm_act(const int8_t *xq, const float *x_scale, int64_t M, con
  * M * N, M * K and N * K at most 2^35.
  * Few rows or few tiles of a long K are split over K and joined in a workspace: device,
  * 16-byte aligned, at least w16a16_linear_workspace(M, N, K) bytes (may be 0: then NULL; 0 for up
- * to 16 rows with N up to 4096 and K up to 8192). Up to 16 rows a smaller one, or none, may be
- * passed: a long K then stays with one workgroup per 16 channels, which takes longer.
+ * to 16 rows with K up to 8192 and, above 4096 channels, from 1024 on). Up to 16 rows a smaller
+ * one, or none, may be passed: a long K then stays with one workgroup per 16 channels, which takes
+ * longer.
  * Errors: NULL, SHAPE (also a workspace that is too small), ALIGN (rows included: 2 * ld
  *         % 16), DTYPE (dtype, activation), HIP.
  */

@@ -870,8 +870,8 @@ def w16a16_linear(x, w, bias=None, activation="none", residual=None, pre=None, o
     out = _result(out, "out", (M, N), x.dtype, x, stream)
     lib = load()
     work, address, size = None, None, 0
-    # (none up to these sizes)
-    need = 0 if M <= 16 and N <= 4096 and K <= 8192 else lib.w16a16_linear_workspace(M, N, K)
+    # (none at these sizes)
+    need = 0 if M <= 16 and K <= 8192 and (N <= 4096 or K >= 1024) else lib.w16a16_linear_workspace(M, N, K)
     if need or workspace is not None:
         work = _scratch(workspace, need, x, stream)
         address, size = work.data_ptr(), work.shape[0]

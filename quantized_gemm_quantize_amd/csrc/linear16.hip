@@ -142,20 +142,20 @@ double rows_time(int64_t M, int64_t N, int64_t K) {
 }
 
 // The kernel of few rows or, if false, the plan in tiles: the kernel unless tiles are estimated to be quicker, which take
-// 3 us and the weight at 4.9 TB/s at least. Over 556 measured sizes that this decides, the choice loses 0.3% of the time
+// 3 us and the weight at 4.9 TB/s at least. Over 496 measured sizes that this decides, the choice loses 0.3% of the time
 // on average and 20% at most.
 //  - Up to 16 rows (rows kernel / tiles, us): a workgroup reads a whole K by itself, so a long one over few channels is
 //    shared by tiles (16 x 64 x 16384 18.2 / 9.0, 16 x 256 x 9216 12.6 / 8.4, 16 x 8 x 2^20 1361 / 51, but 16 x 4096 x
 //    16384 31.1 / 31.3); many workgroups of a short one pay their start (16 x 32000 x 64 7.6 / 4.1, but x 2048 25.8 /
-//    33.5). With at most 4096 channels and 8192 inner elements the kernel stays at every size, and those plans cost the
-//    host nothing: tiles are the quicker ones there at few channels and the longest K only (16 x 64 x 4096 6.2 / 6.9, 1 x
-//    4096 x 4096 7.7 / 11.7, 16 x 64 x 8192 10.0 / 8.4), and their second launch takes the host 3 us (calls of 16 x 64 x
-//    8192 10.0 / 11.0).
+//    33.5). With up to 8192 inner elements (from 1024 on above 4096 channels) the kernel stays at every size, so that
+//    those plans cost the host nothing (two of 0.4 us beside a call of 8). Tiles are the quicker ones there at few
+//    channels and the longest K only (16 x 64 x 4096 6.2 / 6.9, 1 x 4096 x 4096 7.7 / 11.7, but 16 x 256 x 8192 10.3 / 7.6, 16
+//    x 64 x 8192 10.0 / 8.4), and their second launch takes the host 3 us (calls of 16 x 64 x 8192 10.0 / 11.0).
 //  - Up to 64: 24 x 4096 x 4096 10.0 / 12.3, 24 x 4096 x 8192 17.5 / 20.3, 17 x 8192 x 11008 39.5 / 45.8, 64 x 1024 x 1024
 //    5.5 / 6.5, 64 x 4096 x 1024 6.0 / 6.6, but 24 x 256 x 8192 13.7 / 8.5, 64 x 4096 x 4096 13.9 / 14.0 (tiles), 64 x
 //    8192 x 2048 15.8 / 13.6, 64 x 4096 x 11008 33.3 / 25.9, 64 x 11008 x 4096 36.1 / 25.2.
 bool few_rows(int64_t M, int64_t N, int64_t K, Plan &plan) {
-    if (M <= 16 && N <= 4096 && K <= 8192) return true;
+    if (M <= 16 && K <= 8192 && (N <= 4096 || K >= 1024)) return true;
     const Estimate tiled = estimate(M, N, K);
     plan = tiled.plan;
     return M <= kMaxRows && rows_time(M, N, K) < std::max(tiled.us, 3.0 + 2.0 * N * K / 4.9e6);

@@ -33,11 +33,11 @@ def test_up_to_16_rows(lib):
         assert form(lib, *size) != ROWS and lib.w16a16_linear_workspace(*size) > 0, size
     for size in WIDE:
         assert form(lib, *size) != ROWS, size
-    # none up to these widths, which the binding relies on
+    # none at these widths, which the binding relies on
     for m in (1, 5, 16):
-        for n in (8, 64, 1000, 4096):
-            for k in (8, 64, 1000, 8192):
-                assert form(lib, m, n, k) == ROWS and lib.w16a16_linear_workspace(m, n, k) == 0
+        for n, k in [(n, k) for n in (8, 64, 1000, 4096) for k in (8, 64, 1000, 8192)] + [
+                (n, k) for n in (4104, 11008, 1 << 20) for k in (1024, 4096, 8192)]:
+            assert form(lib, m, n, k) == ROWS and lib.w16a16_linear_workspace(m, n, k) == 0, (m, n, k)
 
 
 @pytest.mark.parametrize("M,N,K", LONG)
