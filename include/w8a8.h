@@ -119,7 +119,8 @@ w8a8_status w8a8_quantize_rows_f32(const float *x, int64_t M, int64_t K, int8_t 
  *           or int32 acc when out_dtype == W8A8_OUT_I32.
  * The int32 accumulators stay on chip. M >= 0 (any value; M <= 64 takes a
  * weight-streaming path), N a positive multiple of 16.
- * Errors: NULL, SHAPE (M < 0, N <= 0, N % 16, K <= 0, K % 16), K_OVERFLOW,
+ * Errors: NULL, SHAPE (M < 0, N <= 0, N % 16, K <= 0, K % 16; with up to 64 rows N >= 2^27, or
+ *         2^26 for K > 4096: a launch holds fewer than 2^32 threads), K_OVERFLOW,
  *         ALIGN, DTYPE, HIP.
  */
 w8a8_status w8a8_gemm(const int8_t *xq, const float *x_scale, int64_t M, const int8_t *wq,

@@ -54,6 +54,13 @@ w8a8_status check_k(int64_t K) {
 // Sizes the kernels index with 32-bit integers.
 bool too_big(int64_t M, int64_t N) { return M > INT_MAX / 2 || N > INT_MAX / 2; }
 
+// Whether a dense product's launch holds fewer than 2^32 threads: up to 64 rows, 512 of them (1024 for a long K) for 16
+// channels; above, 256 for a tile of 256 x 128 (smaller tiles are taken for a few hundred of them only).
+bool dense_launch(int64_t M, int64_t N, int64_t K) {
+    return M <= 64 ? w8a8::grid_fits(N / 16, K > 4096 ? 1024 : 512)
+                   : w8a8::grid_fits((M + 255) / 256 * ((N + 127) / 128), 256);
+}
+
 template <typename T>
 w8a8_status quantize_entry(const T *x, int64_t M, int64_t K, int8_t *xq, float *x_scale,
                            void *stream,
@@ -110,6 +117,7 @@ w8a8_status w8a8_gemm(const int8_t *xq, const float *x_scale, int64_t M, const i
     if (od != W8A8_OUT_BF16 && od != W8A8_OUT_I32) return W8A8_ERR_DTYPE;
     if ((M + 127) / 128 > INT_MAX / ((N + 127) / 128)) return W8A8_ERR_SHAPE;  // grid.x
     if (M == 0) return W8A8_OK;
+    if (!dense_launch(M, N, K)) return W8A8_ERR_SHAPE;
     if (!xq || !x_scale || !wq || !w_scale || !out) return W8A8_ERR_NULL;
     if (misaligned(xq) || misaligned(x_scale) || misaligned(wq) || misaligned(w_scale) ||
         misaligned(out))
@@ -127,6 +135,7 @@ w8a8_status w8a8_gemm_addmm(const int8_t *xq, const float *x_scale, int64_t M, c
     if (!std::isfinite(alpha) || !std::isfinite(beta)) return W8A8_ERR_VALUE;
     if ((M + 127) / 128 > INT_MAX / ((N + 127) / 128)) return W8A8_ERR_SHAPE;  // grid.x
     if (M == 0) return W8A8_OK;
+    if (!dense_launch(M, N, K)) return W8A8_ERR_SHAPE;
     if (!xq || !x_scale || !wq || !w_scale || !out) return W8A8_ERR_NULL;
     if (!bias && beta != 0.0f) return W8A8_ERR_NULL;
     if (misaligned(xq) || misaligned(x_scale) || misaligned(wq) || misaligned(w_scale) ||
@@ -652,6 +661,7 @@ w8a8_status w8a8_gemm_act(const int8_t *xq, const float *x_scale, int64_t M, con
     if ((M + 127) / 128 > INT_MAX / ((N + 127) / 128)) return W8A8_ERR_SHAPE;  // grid.x
     if (residual && (ldr < N || ldr > INT_MAX)) return W8A8_ERR_SHAPE;
     if (M == 0) return W8A8_OK;
+    if (!dense_launch(M, N, K)) return W8A8_ERR_SHAPE;
     if (!xq || !x_scale || !wq || !w_scale || !out) return W8A8_ERR_NULL;
     if (misaligned(xq) || misaligned(x_scale) || misaligned(wq) || misaligned(w_scale) ||
         misaligned(out) || misaligned(bias) || misaligned(residual) || (residual && ldr % 8 != 0))
