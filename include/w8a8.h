@@ -38,6 +38,8 @@
  *  - Arguments are validated on the host before any HIP call; a failed check
  *    returns its code and launches nothing. M == 0 is a valid empty call that
  *    launches nothing (pointers sized by M may then be NULL).
+ *  - Outputs and workspaces overlap neither the operands nor each other, except
+ *    where an entry point allows it.
  *  - Base pointers must be 16-byte aligned (W8A8_ERR_ALIGN), except where an
  *    entry point states another rule.
  *  - K must be a positive multiple of 16 and at most W8A8_MAX_K, so that
